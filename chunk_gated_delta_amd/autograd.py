@@ -4,7 +4,8 @@ Argument marshalling only: each forward calls the library's forward that keeps w
 backward needs (carve_fwd_save, carve_fwd_logits_save, or the content-aware carve_fwd
 with its per-period records) and holds that buffer on the autograd context; the backward
 calls the matching library backward (carve_bwd_saved, carve_bwd_logits_saved,
-carve_bwd_content) with the incoming gradients.  Every step of both passes runs in the
+carve_bwd_content) with the incoming gradients; swa_attention does the same over
+carve_swa_fwd and carve_swa_bwd.  Every step of both passes runs in the
 HIP kernels; there is no CPU fallback.
 
     from chunk_gated_delta_amd.autograd import carve_attention
@@ -71,6 +72,27 @@ class _ContentPair(torch.autograd.Function):
                               want_dS0=ctx.has_S0, want_dm0=ctx.has_m0)
         return (g["dq"], g["dk"], g["dv"], g["dlog_g"], g["dw"], g["db_x"], g["dU1"], g["dU2"], g["dm0"], g["dS0"],
                 None)
+
+
+class _SwaPair(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lens, window, sinks, scale):
+        o, lse = carve.swa_fwd(q, k, v, window, sinks=sinks, scale=scale, lens=lens)
+        ctx.at = dict(window=window, sinks=sinks, scale=scale)
+        ctx.save_for_backward(q, k, v, lens, o, lse)
+        return o
+
+    @staticmethod
+    def backward(ctx, dO):
+        q, k, v, lens, o, lse = ctx.saved_tensors
+        g = carve.swa_bwd(q, k, v, o, lse, _c(dO), lens=lens, **ctx.at)
+        return g["dq"], g["dk"], g["dv"], None, None, None, None
+
+
+def swa_attention(q, k, v, window, sinks=0, scale=None, lens=None):
+    """o of sliding-window attention with sinks, differentiable in q, k and v (carve_swa_fwd /
+    carve_swa_bwd; arguments as carve.swa_fwd)."""
+    return _SwaPair.apply(q, k, v, lens, window, sinks, scale)
 
 
 def carve_attention(q, k, v, log_g, w, b=None, S0=None, L=64):

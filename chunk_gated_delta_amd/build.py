@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libcarve.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["carve_api.cpp", "fwd_kernels.hip", "bwd_kernels.hip", "decode_kernels.hip", "content_bwd_kernels.hip",
-           "stream_kernels.hip", "width_kernels.hip"]
+           "stream_kernels.hip", "width_kernels.hip", "attention/attn_api.cpp", "attention/swa_fwd.hip",
+           "attention/swa_bwd.hip", "attention/weights.hip", "attention/cache_decode.hip", "attention/cache_fill.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -28,7 +29,7 @@ CFLAGS = [
 
 
 def source_digest():
-    """Digest of every kernel source (csrc/*); counter measurements record it so that a
+    """Digest of the delta rule's kernel sources (csrc/*, without csrc/attention); counter measurements record it so that a
     later change to the kernels marks them stale."""
     import hashlib
     h = hashlib.sha256()
@@ -41,7 +42,7 @@ def source_digest():
 
 
 def _compile(src):
-    obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+    obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
     cmd = [HIPCC] + CFLAGS + (["-x", "hip"] if src.endswith(".cpp") else []) + \
         ["-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -63,6 +63,18 @@ class carve_decode_content(ctypes.Structure):
                 ("csum", ctypes.c_void_p), ("pos", ctypes.c_int)]
 
 
+class carve_swa_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("T", ctypes.c_int),
+                ("D", ctypes.c_int), ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int)]
+
+
+class carve_budget_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("T", ctypes.c_int),
+                ("D", ctypes.c_int), ("C", ctypes.c_int), ("sinks", ctypes.c_int), ("recent", ctypes.c_int),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
 class carve_profile(ctypes.Structure):
     _fields_ = [("events", ctypes.c_void_p * 9), ("n_events", ctypes.c_int)]
 
@@ -136,6 +148,23 @@ def load_library():
     dcp = ctypes.POINTER(carve_decode_content)
     lib.carve_decode_step.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, dcp, vp, vp]
     lib.carve_decode_step.restype = i
+    wp = ctypes.POINTER(carve_swa_shape)
+    bp = ctypes.POINTER(carve_budget_shape)
+    for name, args in (("carve_swa_bwd", [wp]), ("carve_swa_decode", [wp]), ("carve_budget_weights", [wp]),
+                       ("carve_budget_decode", [bp])):
+        size = getattr(lib, name + "_workspace_size")
+        size.argtypes = args
+        size.restype = sz
+    for name, args in (("carve_swa_fwd", [wp, vp, vp, vp, vp, vp, vp, vp]),
+                       ("carve_swa_bwd", [wp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+                       ("carve_swa_fill", [wp, vp, vp, vp, vp, vp, vp]),
+                       ("carve_swa_decode", [wp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+                       ("carve_budget_weights", [wp, vp, vp, vp, vp, vp, vp, sz, vp]),
+                       ("carve_budget_keep", [bp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+                       ("carve_budget_decode", [bp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = i
     lib.carve_stream_copy.argtypes = [vp, vp, sz, vp]
     lib.carve_stream_copy.restype = i
     lib.carve_status_string.argtypes = [i]
@@ -606,6 +635,213 @@ def decode_step(q, k, v, log_g, w, S, b=None, L=64, content=None, o=None):
                                  _ptr(S), ctypes.byref(cs) if cs is not None else None, _ptr(o), _stream(dev))
     _raise(code, "carve_decode_step")
     return o, m_out
+
+
+# ------------------------------------------------------------------ attention of fixed memory
+def _call(what, dev, *args):
+    """One library call on the tensors' device and its current stream; raises on a status."""
+    fn = getattr(load_library(), what)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _raise(code, what)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _heads(q, k, ndim):
+    """(B, Hq, Hkv, T, D, device, dtype) of q [B,Hq,(T,)D] and k [B,Hkv,(T,)D]."""
+    if q.dim() != ndim or k.dim() != ndim:
+        raise ValueError(f"q and k must have {ndim} dimensions, got {q.dim()} and {k.dim()}")
+    B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
+    Hkv = k.shape[1]
+    T = q.shape[2] if ndim == 4 else 1
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    if not q.is_cuda:
+        raise ValueError(f"q: expected a GPU tensor, got {q.device}")
+    return B, Hq, Hkv, T, D, q.device, q.dtype
+
+
+def _swa_shape(q, k, ndim, window, sinks, scale):
+    B, Hq, Hkv, T, D, dev, dt = _heads(q, k, ndim)
+    s = carve_swa_shape(B, Hq, Hkv, T, D, window, sinks, D ** -0.5 if scale is None else scale, _dtype_code(q))
+    return s, dev, dt
+
+
+def _workspace(what, s, dev, workspace):
+    need = getattr(load_library(), what + "_workspace_size")(ctypes.byref(s))
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace is not None and workspace.device != dev:
+        raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, _addr(workspace), nbytes
+
+
+def swa_fwd(q, k, v, window, sinks=0, scale=None, lens=None, o=None, lse=None):
+    """Sliding-window attention with sinks: (o [B,Hq,T,D], lse [B,Hq,T] float32).
+
+    q [B,Hq,T,D], k, v [B,Hkv,T,D] (float32 or bfloat16, Hq a multiple of Hkv: query head h
+    reads key head h // (Hq // Hkv)).  Token t sees s when s <= t and (t - s < window or
+    s < sinks).  scale: factor of q . k, 1/sqrt(D) by default.  lens [B] int32 or None: tokens of
+    each sequence of a padded batch; rows behind them give o = 0 and lse = -inf.  Outputs may be
+    passed preallocated."""
+    s, dev, dt = _swa_shape(q, k, 4, window, sinks, scale)
+    kv = (s.B, s.Hkv, s.T, s.D)
+    _check(k, "k", kv, dt, dev)
+    _check(v, "v", kv, dt, dev)
+    _check(lens, "lens", (s.B,), torch.int32, dev)
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    _check(o, "o", q.shape, dt, dev)
+    _check(lse, "lse", q.shape[:3], torch.float32, dev)
+    _call("carve_swa_fwd", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(v), _addr(lens), _addr(o), _addr(lse))
+    return o, lse
+
+
+def swa_bwd(q, k, v, o, lse, dO, window, sinks=0, scale=None, lens=None, workspace=None):
+    """Backward of swa_fwd from its o and lse: {"dq", "dk", "dv"} for the output gradient dO
+    [B,Hq,T,D] (dk, dv summed over the query heads that share the key head)."""
+    s, dev, dt = _swa_shape(q, k, 4, window, sinks, scale)
+    kv = (s.B, s.Hkv, s.T, s.D)
+    _check(k, "k", kv, dt, dev)
+    _check(v, "v", kv, dt, dev)
+    _check(o, "o", q.shape, dt, dev)
+    _check(dO, "dO", q.shape, dt, dev)
+    _check(lse, "lse", q.shape[:3], torch.float32, dev)
+    _check(lens, "lens", (s.B,), torch.int32, dev)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
+    workspace, ws, nbytes = _workspace("carve_swa_bwd", s, dev, workspace)
+    _call("carve_swa_bwd", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(v), _addr(lens), _addr(o), _addr(lse),
+          _addr(dO), _addr(g["dq"]), _addr(g["dk"]), _addr(g["dv"]), ws, nbytes)
+    return g
+
+
+def swa_cache(B, Hkv, D, window, sinks=0, dtype=torch.bfloat16, device="cuda"):
+    """An empty ring cache of a windowed layer: (cache_k, cache_v), [B,Hkv,sinks+window,D] each."""
+    shape = (B, Hkv, sinks + window, D)
+    return torch.zeros(shape, dtype=dtype, device=device), torch.zeros(shape, dtype=dtype, device=device)
+
+
+def swa_fill(k, v, cache_k, cache_v, window, sinks=0, lens=None):
+    """Writes a prompt's k, v [B,Hkv,T,D] (starting at position 0; lens [B] int32 of T tokens) into
+    the ring cache [B,Hkv,sinks+window,D]; slots that hold none of its tokens stay as they are."""
+    s, dev, dt = _swa_shape(k, k, 4, window, sinks, 1.0)
+    _check(v, "v", k.shape, dt, dev)
+    cache = (s.B, s.Hkv, window + sinks, s.D)
+    _check(cache_k, "cache_k", cache, dt, dev)
+    _check(cache_v, "cache_v", cache, dt, dev)
+    _check(lens, "lens", (s.B,), torch.int32, dev)
+    _call("carve_swa_fill", dev, ctypes.byref(s), _addr(k), _addr(v), _addr(lens), _addr(cache_k), _addr(cache_v))
+
+
+def swa_decode(q, k, v, cache_k, cache_v, pos, window, sinks=0, scale=None, o=None, workspace=None):
+    """One new token per sequence on the ring cache, which is updated in place: o [B,Hq,D].
+
+    q [B,Hq,D], k, v [B,Hkv,D], cache_k, cache_v [B,Hkv,sinks+window,D]; pos [B] int32, on the
+    device: tokens of each sequence before this one (negative: no token; o = 0, cache untouched).
+    pos is not advanced: one array serves all layers of a step."""
+    s, dev, dt = _swa_shape(q, k, 3, window, sinks, scale)
+    kv = (s.B, s.Hkv, s.D)
+    cache = (s.B, s.Hkv, window + sinks, s.D)
+    _check(k, "k", kv, dt, dev)
+    _check(v, "v", kv, dt, dev)
+    _check(cache_k, "cache_k", cache, dt, dev)
+    _check(cache_v, "cache_v", cache, dt, dev)
+    _check(pos, "pos", (s.B,), torch.int32, dev)
+    if o is None:
+        o = torch.empty_like(q)
+    _check(o, "o", q.shape, dt, dev)
+    workspace, ws, nbytes = _workspace("carve_swa_decode", s, dev, workspace)
+    _call("carve_swa_decode", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(v), _addr(cache_k), _addr(cache_v),
+          _addr(pos), _addr(o), ws, nbytes)
+    return o
+
+
+def budget_weights(q, k, lse, window=None, sinks=0, scale=None, lens=None, weights=None, workspace=None):
+    """The attention weight every token of a prompt has received, [B,Hkv,T] float32: summed over the
+    tokens that see it and the query heads that share its key head.  lse [B,Hq,T] is swa_fwd's of
+    the same window and sinks (window None: all tokens before, as swa_fwd with window >= T)."""
+    if window is None:
+        window = max(q.shape[2], 1)
+    s, dev, dt = _swa_shape(q, k, 4, window, sinks, scale)
+    _check(k, "k", (s.B, s.Hkv, s.T, s.D), dt, dev)
+    _check(lse, "lse", q.shape[:3], torch.float32, dev)
+    _check(lens, "lens", (s.B,), torch.int32, dev)
+    if weights is None:
+        weights = torch.empty((s.B, s.Hkv, s.T), dtype=torch.float32, device=dev)
+    _check(weights, "weights", (s.B, s.Hkv, s.T), torch.float32, dev)
+    workspace, ws, nbytes = _workspace("carve_budget_weights", s, dev, workspace)
+    _call("carve_budget_weights", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(lse), _addr(lens), _addr(weights),
+          ws, nbytes)
+    return weights
+
+
+def budget_cache(B, Hkv, D, C, dtype=torch.bfloat16, device="cuda"):
+    """An empty cache of C slots kept by accumulated attention weight: (cache_k, cache_v
+    [B,Hkv,C,D], cache_w [B,Hkv,C] float32, cache_pos [B,Hkv,C] int32, -1 = empty)."""
+    return (torch.zeros((B, Hkv, C, D), dtype=dtype, device=device), torch.zeros((B, Hkv, C, D), dtype=dtype, device=device),
+            torch.zeros((B, Hkv, C), dtype=torch.float32, device=device),
+            torch.full((B, Hkv, C), -1, dtype=torch.int32, device=device))
+
+
+def _check_cache(cache, B, Hkv, C, D, dt, dev):
+    cache_k, cache_v, cache_w, cache_pos = cache
+    _check(cache_k, "cache_k", (B, Hkv, C, D), dt, dev)
+    _check(cache_v, "cache_v", (B, Hkv, C, D), dt, dev)
+    _check(cache_w, "cache_w", (B, Hkv, C), torch.float32, dev)
+    _check(cache_pos, "cache_pos", (B, Hkv, C), torch.int32, dev)
+    return tuple(map(_addr, cache))
+
+
+def budget_keep(k, v, weights, C, sinks=0, recent=1, lens=None, cache=None):
+    """The cache of C slots of a prompt (starting at position 0): the first `sinks` tokens, the last
+    `recent`, and the heaviest of the others, in order of position; (cache_k, cache_v, cache_w,
+    cache_pos) as budget_cache makes it, or `cache` itself, overwritten (rows of empty slots stay)."""
+    B, _, Hkv, T, D, dev, dt = _heads(k, k, 4)
+    s = carve_budget_shape(B, Hkv, Hkv, T, D, C, sinks, recent, 1.0, _dtype_code(k))
+    _check(v, "v", k.shape, dt, dev)
+    _check(weights, "weights", (B, Hkv, T), torch.float32, dev)
+    _check(lens, "lens", (B,), torch.int32, dev)
+    if cache is None:
+        cache = budget_cache(B, Hkv, D, C, dt, dev)
+    ptrs = _check_cache(cache, B, Hkv, C, D, dt, dev)
+    _call("carve_budget_keep", dev, ctypes.byref(s), _addr(k), _addr(v), _addr(weights), _addr(lens), *ptrs)
+    return tuple(cache)
+
+
+def budget_decode(q, k, v, cache, pos, sinks=0, recent=1, scale=None, o=None, slot=None, workspace=None):
+    """One new token per sequence on the cache kept by weight (updated in place):
+    (o [B,Hq,D], slot [B,Hkv] int32, the slot each key head gave it).
+
+    q [B,Hq,D], k, v [B,Hkv,D]; cache as budget_cache makes it; pos [B] int32 as for swa_decode.
+    The token takes an empty slot, or that of the least weight among tokens neither in the first
+    `sinks` nor the last `recent` positions (the new one counted); every live slot's weight grows
+    by its attention weight of this token."""
+    B, Hq, Hkv, _, D, dev, dt = _heads(q, k, 3)
+    C = cache[0].shape[2]
+    s = carve_budget_shape(B, Hq, Hkv, 1, D, C, sinks, recent, D ** -0.5 if scale is None else scale, _dtype_code(q))
+    _check(k, "k", (B, Hkv, D), dt, dev)
+    _check(v, "v", (B, Hkv, D), dt, dev)
+    _check(pos, "pos", (B,), torch.int32, dev)
+    ptrs = _check_cache(cache, B, Hkv, C, D, dt, dev)
+    if o is None:
+        o = torch.empty_like(q)
+    if slot is None:
+        slot = torch.empty((B, Hkv), dtype=torch.int32, device=dev)
+    _check(o, "o", q.shape, dt, dev)
+    _check(slot, "slot", (B, Hkv), torch.int32, dev)
+    workspace, ws, nbytes = _workspace("carve_budget_decode", s, dev, workspace)
+    _call("carve_budget_decode", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(v), *ptrs, _addr(pos), _addr(o),
+          _addr(slot), ws, nbytes)
+    return o, slot
 
 
 def stream_copy(dst, src):

@@ -1,0 +1,146 @@
+// Building blocks of the attention kernels: 32x32 MFMA tiles and staging of token rows.
+//
+// A score tile is always formed with the tokens that own the softmax statistics on its
+// columns, so that a lane holds values of ONE token: v_mfma_f32_32x32x16_bf16 returns
+//   C (32 x 32): lane l holds C[8 (i / 4) + 4 (l / 32) + i % 4][l % 32], i = 0..15,
+// of operands A (32 x 16): lane l holds A[l % 32][8 (l / 32) + j], and B (16 x 32): lane l
+// holds B[8 (l / 32) + j][l % 32], j = 0..7 (fp32: eight v_mfma_f32_32x32x2 steps over
+// the same lane values).  Registers 8 x .. 8 x + 7 of C are, rounded, a B operand whose
+// contraction index runs over the rows 16 x + 8 (j / 4) + 4 (l / 32) + j % 4 of C, so
+// weights go from the score tile into the next product without leaving their lane; the
+// other operand of that product is read with its rows in the same order (frag_cols32).
+#pragma once
+#include "../carve_device.h"
+#include "attn_internal.h"
+
+namespace carve {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegBig = -1.0e30f;     // running maximum before any visible score
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+__device__ __forceinline__ void mma32(f32x16& c, const Frag<bf16>& a, const Frag<bf16>& b) {
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ void mma32(f32x16& c, const Frag<float>& a, const Frag<float>& b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.lo[j], b.lo[j], c, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.hi[j], b.hi[j], c, 0, 0, 0);
+}
+// row of register i of a 32 x 32 accumulator tile
+__device__ __forceinline__ int acc_row(int i, int half) { return 8 * (i >> 2) + 4 * half + (i & 3); }
+
+// Rows r0 .. r0 + 31 of a row-major LDS matrix, 16-deep block at column k0 (A operand).
+template <typename T>
+__device__ __forceinline__ Frag<T> frag_rows32(const T* m, int ld, int r0, int k0) {
+  const int lane = lane_id();
+  return load_frag(m + (r0 + (lane & 31)) * ld + k0 + 8 * (lane >> 5));
+}
+// Columns c0 .. c0 + 31 of a row-major LDS matrix as the 32 rows of an A operand, its 16-deep
+// contraction over rows k0 + 8 (j / 4) + 4 (l / 32) + j % 4.  bf16: two transpose reads
+// (lane s of a 16-lane group points at row s / 4, columns 4 (s % 4) of a 4 x 16 block and
+// receives column s; checked with the layout of lds_frag_tr).
+__device__ __forceinline__ Frag<bf16> frag_cols32(const bf16* m, int ld, int c0, int k0) {
+  const int lane = lane_id(), s = lane & 15, g = lane >> 4;
+  bf16* p = const_cast<bf16*>(m) + (k0 + 4 * (g >> 1) + (s >> 2)) * ld + c0 + 16 * (g & 1) + 4 * (s & 3);
+  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * ld));
+  Frag<bf16> f;
+  f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  return f;
+}
+__device__ __forceinline__ Frag<float> frag_cols32(const float* m, int ld, int c0, int k0) {
+  const int lane = lane_id();
+  const float* p = m + (k0 + 4 * (lane >> 5)) * ld + c0 + (lane & 31);
+  Frag<float> f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f.lo[j] = p[j * ld];
+    f.hi[j] = p[(j + 8) * ld];
+  }
+  return f;
+}
+// registers 8 x .. 8 x + 7 of an accumulator tile as a B operand (rounded for bf16)
+__device__ __forceinline__ void acc_frag(const f32x16& c, int x, Frag<bf16>& f) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.v[j] = (bf16)c[8 * x + j];
+}
+__device__ __forceinline__ void acc_frag(const f32x16& c, int x, Frag<float>& f) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f.lo[j] = c[8 * x + j];
+    f.hi[j] = c[8 * x + 4 + j];
+  }
+}
+
+// ROWS token rows of a [n][D] matrix, moved through registers into a padded LDS tile by
+// NT threads in pieces of 8 elements; rows at or past n become zero, so that nothing
+// behind a sequence's end (not a number, say) reaches a product.
+template <typename T, int ROWS, int D, int NT>
+struct RowStage {
+  static constexpr int PR = D / 8, NP = ROWS * PR, NST = NP / NT;
+  static_assert(NP % NT == 0, "whole pieces per thread");
+  static constexpr int LD = D + Pad<T>::v;
+  Frag<T> x[NST];
+  __device__ __forceinline__ void load(const T* base, int r0, int n) {
+#pragma unroll
+    for (int u = 0; u < NST; ++u) {
+      const int p = threadIdx.x + NT * u, r = r0 + p / PR;
+      x[u] = load_frag(base + (size_t)(r < n ? r : n - 1) * D + 8 * (p % PR));
+      if (r >= n) x[u] = zero_frag(T());
+    }
+  }
+  __device__ __forceinline__ void store(T* tile) const {
+#pragma unroll
+    for (int u = 0; u < NST; ++u) {
+      const int p = threadIdx.x + NT * u;
+      *reinterpret_cast<Frag<T>*>(tile + (p / PR) * LD + 8 * (p % PR)) = x[u];
+    }
+  }
+};
+
+__device__ __forceinline__ int seq_len(const int* lens, int b, int T) {
+  return lens ? min(max(lens[b], 0), T) : T;
+}
+
+// Workgroups are dispatched round-robin over the 8 XCDs: consecutive units of work, which
+// share keys, go to one XCD and its L2.
+__device__ __forceinline__ int xcd_unit(int total) {
+  const int id = blockIdx.x, per = total / 8;
+  return id < 8 * per ? (id % 8) * per + id / 8 : id;
+}
+
+// Launch with `lds` bytes of dynamic LDS (above 64 KB the limit has to be raised first).
+template <size_t LDS, typename Args>
+static hipError_t launch_kernel(void (*kern)(Args), dim3 grid, int threads, const Args& a, hipStream_t st) {
+  if constexpr (LDS > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)LDS);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kern, grid, dim3(threads), LDS, st, a);
+  return hipGetLastError();
+}
+
+// One token's accumulator column, d = 32 dt + acc_row(i), written to its row times f.
+template <typename T, int D>
+__device__ __forceinline__ void store_column(T* row, const f32x16 (&c)[D / 32], float f) {
+  const int half = lane_id() >> 5;
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      store4(row + 32 * dt + 8 * m + 4 * half,
+             f32x4{c[dt][4 * m] * f, c[dt][4 * m + 1] * f, c[dt][4 * m + 2] * f, c[dt][4 * m + 3] * f});
+}
+
+}  // namespace carve

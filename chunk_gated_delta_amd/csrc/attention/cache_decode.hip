@@ -1,0 +1,329 @@
+// One new token per sequence against a cache of C slots: the ring cache of windowed attention,
+// and the cache whose slots are given up by accumulated attention weight.
+//
+// Workgroup = a range of slots of one key head, for all query heads that share it (16 a tile on
+// the columns of v_mfma_f32_16x16x32): every cached row is read once.  S^T = K Q^T and
+// O^T = V^T P^T per 32 slots of a wave, running maximum and sum per head; the four waves
+// and then the ranges are joined by rescaling.  The new token's k, v are taken from the call
+// and written by the workgroup whose range holds their slot, so no other workgroup reads it.
+#include <algorithm>
+
+#include "attn_device.h"
+
+namespace carve {
+
+constexpr int kDecThreads = 256;
+
+// Slot of the new token in a cache kept by weight, by the least (class, weight, slot):
+// class 0 the slot that holds this position already (a repeated call), 1 an empty one, 2 one
+// that is neither first nor recent, 3 any other.  NaN counts as the largest weight.
+__device__ __forceinline__ unsigned weight_order(float w) {
+  const unsigned u = __builtin_bit_cast(unsigned, w + 0.f);
+  return w != w ? 0xffffffffu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ int pick_slot(const CacheArgs& a, int bk, int p, unsigned long long* red) {
+  const float* w = a.cache_w + (size_t)bk * a.C;
+  const int* held = a.cache_pos + (size_t)bk * a.C;
+  unsigned long long best = ~0ull;
+  for (int j = threadIdx.x; j < a.C; j += kDecThreads) {
+    const int h = held[j];
+    const int cls = h == p ? 0 : h < 0 ? 1 : (h >= a.sinks && h <= p - a.recent) ? 2 : 3;
+    const unsigned o = cls < 2 ? 0u : weight_order(w[j]);
+    const unsigned long long key = ((unsigned long long)cls << 62) | ((unsigned long long)o << 30) | (unsigned)j;
+    best = key < best ? key : best;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const unsigned long long x = __shfl_xor(best, o);
+    best = x < best ? x : best;
+  }
+  if (lane_id() == 0) red[wave_id()] = best;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kDecThreads / 64; ++i) best = red[i] < best ? red[i] : best;
+  return (int)(best & ((1u << 30) - 1));
+}
+
+__device__ __forceinline__ int ring_slot(const CacheArgs& a, int p) {
+  return p < a.sinks ? p : a.sinks + (p - a.sinks) % a.window;
+}
+
+// Adds the token's weights to the cache's: slots lo .. hi - 1, with max and sum of every head
+// (log2 domain) in st[head] = {m, 1 / l}.
+__device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st) {
+  const int G = a.Hq / a.Hkv;
+  for (int j = lo + threadIdx.x; j < hi; j += kDecThreads) {
+    const size_t i = (size_t)bk * a.C + j;
+    const bool mine = j == at;
+    if (!mine && a.cache_pos[i] < 0) continue;
+    const float* s = a.score + i * G;
+    float x = 0.f;
+    for (int g = 0; g < G; ++g) x += __builtin_amdgcn_exp2f(s[g] - st[2 * g]) * st[2 * g + 1];
+    a.cache_w[i] = mine ? x : a.cache_w[i] + x;
+    if (mine) a.cache_pos[i] = p;
+  }
+}
+
+template <typename T, int D, int NT, bool BUDGET>
+__global__ __launch_bounds__(kDecThreads) void cache_decode_kernel(CacheArgs a) {
+  constexpr int LD = D + Pad<T>::v, PR = D / 8, NV = 32 * PR / 64, LDM = D + 4;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ unsigned long long red[kDecThreads / 64];
+  __shared__ float ml[4][16][2];
+  __shared__ float st[16 * NT][2];
+  const int G = a.Hq / a.Hkv;
+  const int split = blockIdx.x % a.n_split, bk = blockIdx.x / a.n_split, b = bk / a.Hkv;
+  const int lane = lane_id(), wave = wave_id(), lr = lane & 15, lg = lane >> 4;
+  const int p = a.pos[b];
+  T* ob = reinterpret_cast<T*>(a.o) + (size_t)bk * G * D;
+  if (p < 0) {                                   // no token: the cache stays as it is
+    if (split == 0) {
+      for (int i = threadIdx.x; i < G * D; i += kDecThreads) ob[i] = to<T>(0.f);
+      if (BUDGET && threadIdx.x == 0) a.slot[bk] = -1;
+    }
+    return;
+  }
+  const int at = BUDGET ? pick_slot(a, bk, p, red) : ring_slot(a, p);
+  if (BUDGET && split == 0 && threadIdx.x == 0) a.slot[bk] = at;
+  const int count = BUDGET ? a.C : min(p, a.C - 1) + 1;          // a ring holds its tokens from slot 0 up
+  const int lo = split * a.split_len, hi = min(min(lo + a.split_len, a.C), count);
+  T* ck = reinterpret_cast<T*>(a.cache_k) + (size_t)bk * a.C * D;
+  T* cv = reinterpret_cast<T*>(a.cache_v) + (size_t)bk * a.C * D;
+  const T* kn = reinterpret_cast<const T*>(a.k) + (size_t)bk * D;
+  const T* vn = reinterpret_cast<const T*>(a.v) + (size_t)bk * D;
+  const int* held = BUDGET ? a.cache_pos + (size_t)bk * a.C : nullptr;
+
+  Frag<T> Q[NT][D / 32];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int g = min(16 * nt + lr, G - 1);
+#pragma unroll
+    for (int kk = 0; kk < D / 32; ++kk)
+      Q[nt][kk] = load_frag(reinterpret_cast<const T*>(a.q) + ((size_t)bk * G + g) * D + 32 * kk + 8 * lg);
+  }
+  const float c = a.scale * kLog2e;
+  f32x4 O[NT][D / 16];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = kNegBig;
+    l[nt] = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt) O[nt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  T* Vs = reinterpret_cast<T*>(smem) + wave * 32 * LD;
+  for (int j0 = lo + 32 * wave; j0 < hi; j0 += 128) {
+    // live slots of the 32, one bit each
+    const int jl = j0 + (lane & 31);
+    bool on = jl < hi;
+    if (BUDGET) on = on && (jl == at || held[min(jl, a.C - 1)] >= 0);
+    const unsigned live = (unsigned)__ballot(on);
+    Frag<T> K[2][D / 32], V[NV];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = min(j0 + 16 * u + lr, hi - 1);
+      const T* row = j == at ? kn : ck + (size_t)j * D;
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) K[u][kk] = load_frag(row + 32 * kk + 8 * lg);
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int pc = lane + 64 * u, r = pc / PR, j = min(j0 + r, hi - 1);
+      const T* row = j == at ? vn : cv + (size_t)j * D;
+      V[u] = load_frag(row + 8 * (pc % PR));
+      if (!((live >> r) & 1)) V[u] = zero_frag(T());
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int pc = lane + 64 * u;
+      *reinterpret_cast<Frag<T>*>(Vs + (pc / PR) * LD + 8 * (pc % PR)) = V[u];
+    }
+    __builtin_amdgcn_wave_barrier();             // the wave's own tile: written, then read across its lanes
+    Frag<T> P[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 S[2];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        S[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) mma(S[u], K[u][kk], Q[nt][kk]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * u + 4 * lg + i;
+          S[u][i] = ((live >> r) & 1) ? S[u][i] * c : -INFINITY;
+          if (BUDGET && 16 * nt + lr < G && j0 + r < hi)
+            a.score[((size_t)bk * a.C + j0 + r) * G + 16 * nt + lr] = S[u][i];
+          mx = fmaxf(mx, S[u][i]);
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float mn = fmaxf(m[nt], mx), alpha = __builtin_amdgcn_exp2f(m[nt] - mn);
+      m[nt] = mn;
+      l[nt] *= alpha;
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) O[nt][dt] *= alpha;
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[4 * u + i] = __builtin_amdgcn_exp2f(S[u][i] - mn);
+          l[nt] += x[4 * u + i];
+        }
+      // the weights are rounded to the operand type for the product with v (the sum l is not)
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) P[nt].v[j] = (bf16)x[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          P[nt].lo[j] = x[j];
+          P[nt].hi[j] = x[4 + j];
+        }
+      }
+    }
+    // V^T operand, its contraction in the order of P: slots 4 lg + j, then 16 + 4 lg + j
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt) {
+      Frag<T> F;
+      if constexpr (sizeof(T) == 2) {
+        bf16* q = Vs + (4 * lg + (lr >> 2)) * LD + 16 * dt + 4 * (lr & 3);
+        const i16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)q);
+        const i16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q + 16 * LD));
+        F.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          F.lo[j] = Vs[(4 * lg + j) * LD + 16 * dt + lr];
+          F.hi[j] = Vs[(16 + 4 * lg + j) * LD + 16 * dt + lr];
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma(O[nt][dt], F, P[nt]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  // the new rows, by the workgroup that owns their slot
+  if (at >= lo && at < hi && threadIdx.x < 2 * PR) {
+    const int i = 8 * (threadIdx.x % PR);
+    if (threadIdx.x < PR) *reinterpret_cast<Frag<T>*>(ck + (size_t)at * D + i) = load_frag(kn + i);
+    else *reinterpret_cast<Frag<T>*>(cv + (size_t)at * D + i) = load_frag(vn + i);
+  }
+  // join the waves, 16 heads at a time
+  float* mg = reinterpret_cast<float*>(smem);                      // [4][16][LDM]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (16 * nt >= G) break;
+    float lt = l[nt] + __shfl_xor(l[nt], 16);
+    lt += __shfl_xor(lt, 32);
+    __syncthreads();
+    if (lg == 0) {
+      ml[wave][lr][0] = m[nt];
+      ml[wave][lr][1] = lt;
+    }
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt) store4(mg + (wave * 16 + lr) * LDM + 16 * dt + 4 * lg, O[nt][dt]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * D / 4; i += kDecThreads) {
+      const int h = i / (D / 4), d = 4 * (i % (D / 4)), g = 16 * nt + h;
+      if (g >= G) continue;
+      float M = kNegBig, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[w][h][0]);
+      f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w][h][0] - M);
+        L += f * ml[w][h][1];
+        x += load4f(mg + (w * 16 + h) * LDM + d) * f;
+      }
+      if (a.n_split == 1) {
+        const float f = L > 0.f ? 1.f / L : 0.f;
+        store4(ob + (size_t)g * D + d, x * f);
+        if (d == 0) {
+          st[g][0] = M;
+          st[g][1] = f;
+        }
+      } else {
+        float* dst = a.part + (((size_t)bk * a.n_split + split) * G + g) * (D + 4);
+        store4(dst + 4 + d, x);
+        if (d == 0) {
+          dst[0] = M;
+          dst[1] = L;
+        }
+      }
+    }
+  }
+  if (BUDGET && a.n_split == 1) {
+    __syncthreads();                             // scores of all waves, and st
+    add_weights(a, bk, p, at, 0, a.C, &st[0][0]);
+  }
+}
+
+// Joins the ranges of one key head: the output (range 0's workgroup), and for a cache kept by
+// weight the weights of the workgroup's own range of slots.
+template <typename T, int D, bool BUDGET>
+__global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
+  __shared__ float st[64][2];
+  const int G = a.Hq / a.Hkv;
+  const int split = BUDGET ? blockIdx.x % a.n_split : 0, bk = BUDGET ? blockIdx.x / a.n_split : blockIdx.x;
+  const int b = bk / a.Hkv, p = a.pos[b];
+  if (p < 0) return;
+  const float* part = a.part + (size_t)bk * a.n_split * G * (D + 4);
+  if (threadIdx.x < G) {
+    float M = kNegBig, L = 0.f;
+    for (int s = 0; s < a.n_split; ++s) M = fmaxf(M, part[((size_t)s * G + threadIdx.x) * (D + 4)]);
+    for (int s = 0; s < a.n_split; ++s) {
+      const float* q = part + ((size_t)s * G + threadIdx.x) * (D + 4);
+      L += __builtin_amdgcn_exp2f(q[0] - M) * q[1];
+    }
+    st[threadIdx.x][0] = M;
+    st[threadIdx.x][1] = L > 0.f ? 1.f / L : 0.f;
+  }
+  __syncthreads();
+  if (split == 0) {
+    T* ob = reinterpret_cast<T*>(a.o) + (size_t)bk * G * D;
+    for (int i = threadIdx.x; i < G * D / 4; i += kDecThreads) {
+      const int g = i / (D / 4), d = 4 * (i % (D / 4));
+      f32x4 x = {0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < a.n_split; ++s) {
+        const float* q = part + ((size_t)s * G + g) * (D + 4);
+        x += load4f(q + 4 + d) * __builtin_amdgcn_exp2f(q[0] - st[g][0]);
+      }
+      store4(ob + (size_t)g * D + d, x * st[g][1]);
+    }
+  }
+  if constexpr (BUDGET) {
+    const int lo = split * a.split_len, hi = min(lo + a.split_len, a.C);
+    add_weights(a, bk, p, a.slot[bk], lo, hi, &st[0][0]);
+  }
+}
+
+template <typename T, int D, int NT, bool BUDGET>
+static hipError_t launch_nt(const CacheArgs& a, hipStream_t st) {
+  constexpr size_t lds = std::max(sizeof(T) * 4 * 32 * (D + Pad<T>::v), sizeof(float) * 4 * 16 * (D + 4));
+  const int units = a.B * a.Hkv;
+  hipError_t e = launch_kernel<lds>(cache_decode_kernel<T, D, NT, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);
+  if (e != hipSuccess || a.n_split == 1) return e;
+  return launch_kernel<0>(cache_join_kernel<T, D, BUDGET>, dim3(BUDGET ? units * a.n_split : units), kDecThreads, a, st);
+}
+template <typename T, int D, bool BUDGET>
+static hipError_t launch_g(const CacheArgs& a, hipStream_t st) {
+  const int G = a.Hq / a.Hkv;
+  if (G <= 16) return launch_nt<T, D, 1, BUDGET>(a, st);
+  if (G <= 32) return launch_nt<T, D, 2, BUDGET>(a, st);
+  return launch_nt<T, D, 4, BUDGET>(a, st);
+}
+template <typename T, int D>
+static hipError_t launch(const CacheArgs& a, hipStream_t st) {
+  return a.cache_w ? launch_g<T, D, true>(a, st) : launch_g<T, D, false>(a, st);
+}
+hipError_t launch_cache_decode(const CacheArgs& a, hipStream_t st) {
+  if (a.dtype) return a.D == 128 ? launch<bf16, 128>(a, st) : launch<bf16, 64>(a, st);
+  return a.D == 128 ? launch<float, 128>(a, st) : launch<float, 64>(a, st);
+}
+
+}  // namespace carve

@@ -407,6 +407,138 @@ carve_status carve_decode_step(const carve_shape* s,
                                void* o, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------------------
+ * Attention whose memory per sequence is fixed, like the recurrent state's: the windowed
+ * attention layers of a hybrid stack (CARVE notes, section 2.4: blocks of CARVE layers and
+ * sliding-window attention layers), and a cache of a fixed number of slots that keeps what
+ * attention has used most.  The conventions at the top of this file hold (dense row-major
+ * device tensors, 16-byte aligned; float and int tensors of [B,H,T], [B,H,C] and [B]
+ * 4-byte aligned; caller-owned buffers; host checks before any launch).  No output may
+ * overlap an input, except that caches are updated in place.
+ *
+ * Query head h reads key head h / (Hq / Hkv).  q, k, v, o and the caches are of one dtype;
+ * scores, softmax statistics and sums are float32; the softmax weights (and, backward, the
+ * score gradients) are rounded to the dtype as operands of the products with v, k, q and dO.
+ * Every result is computed in a fixed order: the same call gives the same bits.
+ *
+ * lens (device) [B] int32 or NULL (= T): tokens of each sequence in a padded batch, taken
+ * in [0, T].  Rows at and behind a sequence's end are not read into any result, whatever
+ * they hold; outputs there are zero (lse: -infinity).
+ */
+typedef struct {
+  int B, Hq, Hkv, T;   /* batch, query heads, key/value heads (Hq a multiple of Hkv), tokens  */
+  int D;               /* head width, 64 or 128                                               */
+  int window;          /* >= 1: tokens a token sees, itself included                          */
+  int sinks;           /* >= 0: first tokens that stay visible behind the window              */
+  float scale;         /* factor of q . k, > 0 (1/sqrt(D) as a rule)                          */
+  carve_dtype dtype;
+} carve_swa_shape;
+
+/*
+ * Sliding-window attention with sinks: token t sees s when s <= t and (t - s < window or
+ * s < sinks);  o_t = sum_s p_ts v_s,  p_ts = exp(scale q_t . k_s - lse_t),
+ * lse_t = log sum_s exp(scale q_t . k_s).  window >= T is plain causal attention.
+ *   q (device) [B,Hq,T,D], k, v (device) [B,Hkv,T,D]
+ *   o (device) [B,Hq,T,D] written; lse (device) [B,Hq,T] float written, or NULL
+ * A key or value that is not a number or infinite within a sequence may also reach tokens of
+ * the neighbouring 128 that do not see it.
+ */
+carve_status carve_swa_fwd(const carve_swa_shape* s, const void* q, const void* k, const void* v, const int* lens,
+                           void* o, float* lse, void* stream);
+
+/*
+ * Its backward from the forward's o and lse: with delta_t = dO_t . o_t and
+ * ds_ts = p_ts (dO_t . v_s - delta_t),  dq_t = scale sum_s ds_ts k_s,
+ * dk_s = scale sum_t ds_ts q_t,  dv_s = sum_t p_ts dO_t (dk, dv summed over the group's heads).
+ *   dO (device) [B,Hq,T,D]; dq as q, dk and dv as k (all written)
+ */
+size_t carve_swa_bwd_workspace_size(const carve_swa_shape* s);
+carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* k, const void* v, const int* lens,
+                           const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Ring cache of the windowed layer: [B,Hkv,C,D] with C = sinks + window slots; position p
+ * lives in slot p for p < sinks, else in slot sinks + (p - sinks) mod window.  At any time
+ * it holds the first `sinks` tokens and the last `window` of the others: what the next
+ * token sees and the one it replaces.
+ *
+ * carve_swa_fill writes the cache of a prompt of T tokens (lens of them) that starts at
+ * position 0; slots that hold no token of it are left as they are.
+ *   k, v (device) [B,Hkv,T,D]; cache_k, cache_v (device) [B,Hkv,C,D]
+ *
+ * carve_swa_decode (shape->T = 1) takes one new token per sequence: writes its k, v to its
+ * slot and attends from q over the cache, the new token included.
+ *   q (device) [B,Hq,D]; k, v (device) [B,Hkv,D]; o (device) [B,Hq,D] written
+ *   pos (device) [B] int32: tokens of the sequence before this one; negative: no token for
+ *       this row (o = 0, its cache stays as it is).  Read on the device, so a captured
+ *       graph follows it; the caller advances it (one array serves every layer).
+ * At most 64 query heads per key head (decode entry points).
+ */
+carve_status carve_swa_fill(const carve_swa_shape* s, const void* k, const void* v, const int* lens, void* cache_k,
+                            void* cache_v, void* stream);
+size_t carve_swa_decode_workspace_size(const carve_swa_shape* s);
+carve_status carve_swa_decode(const carve_swa_shape* s, const void* q, const void* k, const void* v, void* cache_k,
+                              void* cache_v, const int* pos, void* o, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Cache of C slots kept by accumulated attention weight.  Every slot of cache_k, cache_v
+ * [B,Hkv,C,D] has a position cache_pos [B,Hkv,C] int32 (negative: empty) and the weight
+ * cache_w [B,Hkv,C] float that its token has received: the sum of p over the tokens since
+ * and the query heads of the group.  The first `sinks` positions and the last `recent`
+ * (the new token counted) are never given up; sinks + recent <= C.
+ */
+typedef struct {
+  int B, Hq, Hkv, T;   /* as above (carve_budget_keep does not use Hq beyond the checks)      */
+  int D;
+  int C;               /* slots of the cache                                                  */
+  int sinks;           /* >= 0                                                                */
+  int recent;          /* >= 1                                                                */
+  float scale;
+  carve_dtype dtype;
+} carve_budget_shape;
+
+/*
+ * The weight every token of a prompt has received: weights[b,h,s] = sum over the tokens t that
+ * see s and the query heads of key head h of exp(scale q_t . k_s - lse_t), with carve_swa_fwd's
+ * lse of the same window and sinks (window >= T: all tokens before).
+ *   q (device) [B,Hq,T,D], k (device) [B,Hkv,T,D], lse (device) [B,Hq,T] float
+ *   weights (device) [B,Hkv,T] float written (zero behind a sequence's end)
+ */
+size_t carve_budget_weights_workspace_size(const carve_swa_shape* s);
+carve_status carve_budget_weights(const carve_swa_shape* s, const void* q, const void* k, const float* lse,
+                                  const int* lens, float* weights, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * The cache of a prompt that starts at position 0: keeps the first `sinks` tokens, the last
+ * `recent`, and of the others those of the largest weight (of equal ones the lowest
+ * position; not-a-number counts as the largest) until C are kept, in order of position from
+ * slot 0 up.  Slots behind them become empty (position -1, weight 0; their rows stay as
+ * they are).
+ *   k, v (device) [B,Hkv,T,D], weights (device) [B,Hkv,T] float; the cache is written
+ */
+carve_status carve_budget_keep(const carve_budget_shape* s, const void* k, const void* v, const float* weights,
+                               const int* lens, void* cache_k, void* cache_v, float* cache_w, int* cache_pos,
+                               void* stream);
+
+/*
+ * One new token per sequence (shape->T = 1).  It takes an empty slot (the lowest), or else the
+ * slot of the least weight among those neither first nor recent (the lowest of equal ones);
+ * a slot that already holds position pos[b] is taken again, so a repeated call does not
+ * store the token twice.  Then q attends over the live slots, the new token included,
+ * and every live slot's weight grows by its p summed over the group's heads (the new
+ * slot's weight is its own p).
+ *   q, k, v, pos, o as for carve_swa_decode; slot (device) [B,Hkv] int32 written: the
+ *   slot taken, -1 for a row without a token
+ */
+size_t carve_budget_decode_workspace_size(const carve_budget_shape* s);
+carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, const void* k, const void* v,
+                                 void* cache_k, void* cache_v, float* cache_w, int* cache_pos, const int* pos, void* o,
+                                 int* slot, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Measurement helper, not part of the CARVE operation: copies `bytes` from src to dst
  * (both device pointers, 16-byte aligned, non-overlapping; bytes a multiple of 16) with a
  * plain streaming kernel (each byte read once and written once by 16-byte vector accesses,
