@@ -108,8 +108,10 @@ struct RowStage {
   }
 };
 
-// wave index as a scalar: branches on it are uniform
-__device__ __forceinline__ int wave_uid() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+// A value every lane of the wave has, as a scalar: branches on it are uniform, and buffer
+// descriptors made of it need no loop over the lanes.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int wave_uid() { return uniform(threadIdx.x >> 6); }
 
 // ROWS bf16 token rows of width D in LDS, brought there by buffer loads that write LDS directly
 // (16 bytes a lane, 1 KB a wave and instruction, no registers on the way; rows past a sequence's
@@ -132,7 +134,7 @@ struct SwzTile {
   static __device__ __forceinline__ void load(unsigned char* tile, const bf16* base, int r0, int n, int wave) {
     constexpr int PER = ROWS / RPI / NW;
     static_assert(PER * RPI * NW == ROWS, "whole instructions per wave");
-    const int lane = lane_id(), rows = max(0, min(n - r0, ROWS));
+    const int lane = lane_id(), rows = uniform(max(0, min(n - r0, ROWS)));
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16*>(base) + (size_t)r0 * D, 0, rows * RB, 0x00020000);
 #pragma unroll
@@ -181,7 +183,7 @@ struct KeyTiles {
 };
 
 __device__ __forceinline__ int seq_len(const int* lens, int b, int T) {
-  return lens ? min(max(lens[b], 0), T) : T;
+  return uniform(lens ? min(max(lens[b], 0), T) : T);
 }
 
 // Workgroups are dispatched round-robin over the 8 XCDs: consecutive units of work, which

@@ -20,10 +20,10 @@ __device__ __forceinline__ FwdUnit fwd_unit(const SwaArgs& a, int QT) {
   const int G = a.Hq / a.Hkv, NQ = (a.T + QT - 1) / QT;
   const int unit = xcd_unit(a.B * a.Hq * NQ);
   FwdUnit u;
-  u.bk = unit / (G * NQ);
-  u.t0 = (NQ - 1 - (unit / G) % NQ) * QT;
-  u.b = u.bk / a.Hkv;
-  u.hq = (u.bk % a.Hkv) * G + unit % G;
+  u.bk = uniform(unit / (G * NQ));
+  u.t0 = uniform((NQ - 1 - (unit / G) % NQ) * QT);
+  u.b = uniform(u.bk / a.Hkv);
+  u.hq = uniform((u.bk % a.Hkv) * G + unit % G);
   u.n = seq_len(a.lens, u.b, a.T);
   return u;
 }
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
     const int rb = Tile::row_base(), cb = Tile::col_base();
 
     // one tile of 64 keys from s0 against the wave's 32 tokens from ts
-    auto block = [&](const unsigned char* Ks, const unsigned char* Vs, int s0, int ts, auto masked, const Frag<bf16>(&Qf)[KK],
+    auto block = [&](const unsigned char* Ks, const unsigned char* Vs, int s0, int ts, bool masked, const Frag<bf16>(&Qf)[KK],
                      f32x16(&Of)[DT], float& mf, float& lf) {
       f32x16 S[2];
 #pragma unroll
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) mma32(S[u], Tile::row_frag(Ks, rb, 32 * u, kk), Qf[kk]);
       }
-      if constexpr (decltype(masked)::value) {
+      if (masked) {
         const int t = ts + (lane & 31);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -142,10 +142,8 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
         const int ts = tw + 32 * q;
         // nothing of the tile is seen / all of it is seen by all of the 32 tokens
         if (s0 > ts + 31 || (s0 >= a.sinks && ts - (s0 + kFwdK - 1) >= a.window)) continue;
-        if (s0 + kFwdK - 1 <= ts && (ts + 31 - s0 < a.window || s0 + kFwdK <= a.sinks))
-          block(Ks, Vs, s0, ts, std::false_type{}, Q[q], O[q], m[q], l[q]);
-        else
-          block(Ks, Vs, s0, ts, std::true_type{}, Q[q], O[q], m[q], l[q]);
+        const bool full = s0 + kFwdK - 1 <= ts && (ts + 31 - s0 < a.window || s0 + kFwdK <= a.sinks);
+        block(Ks, Vs, s0, ts, !full, Q[q], O[q], m[q], l[q]);
       }
     };
     for (int i = 0; i < kt.count; i += 2) {
@@ -156,12 +154,11 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
       }
       step(K0, V0, kt[i]);
       __syncthreads();
-      if (i + 1 >= kt.count) break;
       if (i + 2 < kt.count) {
         Tile::template load<kFwdK, 4>(K0, kb, kt[i + 2], n, wave);
         Tile::template load<kFwdK, 4>(V0, vb, kt[i + 2], n, wave);
       }
-      step(K1, V1, kt[i + 1]);
+      if (i + 1 < kt.count) step(K1, V1, kt[i + 1]);
     }
   }
 #pragma unroll
