@@ -156,7 +156,7 @@ carve_status carve_swa_fwd(const carve_swa_shape* s, const void* q, const void* 
 size_t carve_swa_bwd_workspace_size(const carve_swa_shape* s) {
   if (check_swa(s) != CARVE_OK || empty(s)) return 0;
   const SwaPlan p = swa_plan(s);
-  return p.delta_bytes + p.part_bytes + 256;
+  return 2 * p.delta_bytes + p.part_bytes + 256;
 }
 
 carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* k, const void* v, const int* lens,
@@ -171,7 +171,7 @@ carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* 
   const SwaPlan p = swa_plan(s);
   if ((long long)s->B * s->Hq * (ceil_div(s->T, 128) + (long long)p.n_sink_tiles * p.n_far) > kMaxUnits)
     return CARVE_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < p.delta_bytes + p.part_bytes + 256) return CARVE_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < 2 * p.delta_bytes + p.part_bytes + 256) return CARVE_ERR_WORKSPACE;
   carve::SwaArgs a = swa_args(s, q, k, v, lens);
   a.o = const_cast<void*>(o);
   a.lse = const_cast<float*>(lse);
@@ -181,7 +181,8 @@ carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* 
   a.dv = dv;
   char* ws = reinterpret_cast<char*>(up256(reinterpret_cast<uintptr_t>(workspace)));
   a.delta = reinterpret_cast<float*>(ws);
-  a.part = reinterpret_cast<float*>(ws + p.delta_bytes);
+  a.lse2 = reinterpret_cast<float*>(ws + p.delta_bytes);
+  a.part = reinterpret_cast<float*>(ws + 2 * p.delta_bytes);
   a.n_sink_tiles = p.n_sink_tiles;
   a.n_far = p.n_far;
   a.far_len = p.far_len;

@@ -25,6 +25,7 @@ struct SwaArgs {
   void* dk;
   void* dv;
   float* delta;               // [B,Hq,T] dO . o
+  float* lse2;                // [B,Hq,T] lse in the log2 domain (+inf: no visible weight)
   // tokens far behind the window of the sink tiles: partial dk, dv of the first n_sink_tiles
   // key tiles, [B*Hkv][n_sink_tiles][1 + n_far][2][kSwaKeyTile][D] fp32
   float* part;

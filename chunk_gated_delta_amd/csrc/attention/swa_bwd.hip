@@ -15,25 +15,343 @@ namespace carve {
 
 constexpr int kDqQ = 128, kDqK = 64;
 
-// ------------------------------------------------------------------ dq
-// Workgroup = 128 tokens of one query head, as in the forward pass.
+struct DqUnit {
+  int b, bk, hq, t0, n;
+};
+__device__ __forceinline__ DqUnit dq_unit(const SwaArgs& a, int QT) {
+  const int G = a.Hq / a.Hkv, NQ = (a.T + QT - 1) / QT;
+  const int unit = xcd_unit(a.B * a.Hq * NQ);
+  DqUnit u;
+  u.bk = uniform(unit / (G * NQ));
+  u.t0 = uniform((NQ - 1 - (unit / G) % NQ) * QT);
+  u.b = uniform(u.bk / a.Hkv);
+  u.hq = uniform((u.bk % a.Hkv) * G + unit % G);
+  u.n = seq_len(a.lens, u.b, a.T);
+  return u;
+}
+// the lane's element of the diagonal of a 32 x 32 accumulator tile (both halves of the wave)
+__device__ __forceinline__ float diagonal(const f32x16& c) {
+  const int lane = lane_id(), half = lane >> 5;
+  float x = 0.f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) x = acc_row(r, half) == (lane & 31) ? c[r] : x;
+  const float other = __shfl_xor(x, 32);
+  return ((lane >> 2) & 1) == half ? x : other;
+}
+// no visible weight (lse = -inf): every p is exp2(. - inf) = 0
+__device__ __forceinline__ float log2_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
+// A workgroup of the dk / dv pass: kSwaKeyTile keys of one key head (32 a wave, a lane owns one
+// key), over the tokens t_lo .. t_hi - 1 that see them inside the window and all heads of the
+// group.  The tokens behind the window of a tile that holds sinks see only the sinks: they are cut
+// into n_far ranges with workgroups of their own, whose sums, like the tile's, go to `part`
+// and are added by swa_sink_kernel.
+struct KeyUnit {
+  int b, bk, n, kt, s0, t_lo, t_hi, part;     // part: index of the partial sum, -1 = final
+};
+__device__ __forceinline__ KeyUnit key_unit(const SwaArgs& a) {
+  constexpr int KT = kSwaKeyTile;
+  const int NK = (a.T + KT - 1) / KT, per = NK + a.n_sink_tiles * a.n_far;
+  const int unit = xcd_unit(a.B * a.Hkv * per);
+  KeyUnit u;
+  u.bk = uniform(unit / per);
+  u.b = uniform(u.bk / a.Hkv);
+  u.n = seq_len(a.lens, u.b, a.T);
+  const int w = uniform(unit % per);
+  const bool far = w >= NK;
+  u.kt = uniform(far ? (w - NK) / a.n_far : w);
+  const int fi = uniform(far ? (w - NK) % a.n_far : 0);
+  u.s0 = u.kt * KT;
+  const long long band = (long long)u.s0 + KT - 1 + a.window;     // first token that sees no key of the tile
+  const long long lo = far ? band + (long long)fi * a.far_len : u.s0, hi = far ? lo + a.far_len : band;
+  u.t_lo = uniform((int)min((long long)u.n, lo));
+  u.t_hi = uniform((int)min((long long)u.n, hi));
+  u.part = u.kt < a.n_sink_tiles && a.n_far > 0 ? (far ? 1 + fi : 0) : -1;
+  return u;
+}
 template <typename T, int D>
-__global__ __launch_bounds__(256) void swa_dq_kernel(SwaArgs a) {
+__device__ __forceinline__ void store_key_grads(const SwaArgs& a, const KeyUnit& u, int s, int wave, f32x16 (&dK)[D / 32],
+                                                f32x16 (&dV)[D / 32]) {
+  constexpr int KT = kSwaKeyTile;
+  if (u.part >= 0) {
+    float* dst = a.part + ((((size_t)u.bk * a.n_sink_tiles + u.kt) * (1 + a.n_far) + u.part) * 2 * KT + 32 * wave +
+                           (lane_id() & 31)) * D;
+    store_column<float, D>(dst, dK, a.scale);
+    store_column<float, D>(dst + (size_t)KT * D, dV, 1.f);
+  } else if (s < a.T) {
+    if (s >= u.n) {
+#pragma unroll
+      for (int dt = 0; dt < D / 32; ++dt) {
+        dK[dt] = zero16();
+        dV[dt] = zero16();
+      }
+    }
+    const size_t row = ((size_t)u.bk * a.T + s) * D;
+    store_column<T, D>(reinterpret_cast<T*>(a.dk) + row, dK, a.scale);
+    store_column<T, D>(reinterpret_cast<T*>(a.dv) + row, dV, 1.f);
+  }
+}
+
+// ------------------------------------------------------------------ bf16: dq
+// Workgroup = 128 tokens of one query head (32 a wave, a lane owns one), tiles of 64 keys in two
+// pairs of swizzled LDS buffers as in the forward pass.  delta comes from the rounded o
+// where many keys share it; where at most kExactKeys are seen its rounding (half a step of o)
+// would be as large as that of ds itself, so a first sweep forms delta_t = sum_s p_ts (dO_t . v_s).
+constexpr int kExactKeys = 64;
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
+  using Tile = SwzTile<D>;
+  constexpr int KK = D / 16, DT = D / 32;
+  __shared__ __align__(16) unsigned char K0[kDqK * Tile::RB], K1[kDqK * Tile::RB];
+  __shared__ __align__(16) unsigned char V0[kDqK * Tile::RB], V1[kDqK * Tile::RB];
+  const DqUnit un = dq_unit(a, kDqQ);
+  const int n = un.n, t0 = un.t0, lane = lane_id(), wave = wave_uid(), half = lane >> 5;
+  const int tw = t0 + 32 * wave, t = tw + (lane & 31);
+  const size_t row = (size_t)(un.b * a.Hq + un.hq) * a.T;
+  const bf16* kb = reinterpret_cast<const bf16*>(a.k) + (size_t)un.bk * a.T * D;
+  const bf16* vb = reinterpret_cast<const bf16*>(a.v) + (size_t)un.bk * a.T * D;
+
+  f32x16 dQ[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) dQ[dt] = zero16();
+  if (t0 < n) {
+    const KeyTiles<kDqK> kt(t0, min(t0 + kDqQ, n), a.window, a.sinks);
+    Frag<bf16> Q[KK], dO[KK];
+    const size_t at = (row + min(t, n - 1)) * D + 8 * half;
+    // delta_t = dO_t . o_t as the diagonal of a product formed as dO . v is below: a token that
+    // sees one key has o = v, and its ds is zero to the last bit
+    f32x16 od = zero16();
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      Q[kk] = load_frag(reinterpret_cast<const bf16*>(a.q) + at + 16 * kk);
+      dO[kk] = load_frag(reinterpret_cast<const bf16*>(a.dO) + at + 16 * kk);
+      mma32(od, load_frag(reinterpret_cast<const bf16*>(a.o) + at + 16 * kk), dO[kk]);
+    }
+    float delta = diagonal(od);
+    const float c = a.scale * kLog2e;
+    const float lse2 = log2_lse(a.lse[row + min(t, n - 1)]);
+    const int rb = Tile::row_base(), cb = Tile::col_base();
+
+    // weights p and dp = dO . v of 64 keys; what is not seen has p = 0
+    auto scores = [&](const unsigned char* Ks, const unsigned char* Vs, int s0, f32x16(&S)[2], f32x16(&dP)[2]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        S[u] = zero16();
+        dP[u] = zero16();
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) mma32(S[u], Tile::row_frag(Ks, rb, 32 * u, kk), Q[kk]);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) mma32(dP[u], Tile::row_frag(Vs, rb, 32 * u, kk), dO[kk]);
+      }
+      const bool full = s0 + kDqK - 1 <= tw && (tw + 31 - s0 < a.window || s0 + kDqK <= a.sinks);
+      if (!full) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int s = s0 + 32 * u + acc_row(r, half);
+            const bool see = (s <= t) & ((t - s < a.window) | (s < a.sinks));
+            S[u][r] = see ? S[u][r] : -INFINITY;
+            dP[u][r] = see ? dP[u][r] : delta;
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[u][r] = __builtin_amdgcn_exp2f(S[u][r] * c - lse2);
+    };
+    auto seen = [&](int s0) {
+      return !(s0 > tw + 31 || (s0 >= a.sinks && tw - (s0 + kDqK - 1) >= a.window));
+    };
+    auto load = [&](unsigned char* Ks, unsigned char* Vs, int i) {
+      if (i < kt.count) {
+        Tile::template load<kDqK, 4>(Ks, kb, kt[i], n, wave);
+        Tile::template load<kDqK, 4>(Vs, vb, kt[i], n, wave);
+      }
+    };
+    auto sweep = [&](auto&& step) {
+      load(K0, V0, 0);
+      for (int i = 0; i < kt.count; i += 2) {
+        __syncthreads();
+        load(K1, V1, i + 1);
+        if (seen(kt[i])) step(K0, V0, kt[i]);
+        __syncthreads();
+        load(K0, V0, i + 2);
+        if (i + 1 < kt.count && seen(kt[i + 1])) step(K1, V1, kt[i + 1]);
+      }
+    };
+    if (a.window + a.sinks <= kExactKeys) {
+      float sum = 0.f;
+      sweep([&](const unsigned char* Ks, const unsigned char* Vs, int s0) {
+        f32x16 S[2], dP[2];
+        scores(Ks, Vs, s0, S, dP);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sum += S[u][r] * (dP[u][r] - delta);   // a correction of the rounded one
+      });
+      delta += sum + __shfl_xor(sum, 32);
+      __syncthreads();                               // the second sweep loads over the last tile
+    }
+    if (half == 0 && t < n) {
+      a.delta[row + t] = delta;
+      a.lse2[row + t] = lse2;
+    }
+    sweep([&](const unsigned char* Ks, const unsigned char* Vs, int s0) {
+      f32x16 S[2], dP[2];
+      scores(Ks, Vs, s0, S, dP);
+      // ds rounded to bf16 for its product with k
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[u][r] *= dP[u][r] - delta;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          Frag<bf16> F;
+          acc_frag(S[u], x, F);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) mma32(dQ[dt], Tile::col_frag(Ks, cb, dt, 32 * u + 16 * x), F);
+        }
+      }
+    });
+  }
+  if (t < a.T) {
+    if (t >= n) {
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) dQ[dt] = zero16();
+    }
+    store_column<bf16, D>(reinterpret_cast<bf16*>(a.dq) + (row + t) * D, dQ, a.scale);
+  }
+}
+
+// ------------------------------------------------------------------ bf16: dk, dv
+// Tiles of 64 tokens (q, dO, lse, delta) in two sets of LDS buffers.  Rows at and past t_hi read as
+// zero throughout: p = 1 there, but dO = 0 and ds = 1 (0 - 0), so they add nothing.
+constexpr int kDkRows = 64;
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
+  using Tile = SwzTile<D>;
+  constexpr int KK = D / 16, DT = D / 32;
+  __shared__ __align__(16) unsigned char Q0[kDkRows * Tile::RB], Q1[kDkRows * Tile::RB];
+  __shared__ __align__(16) unsigned char G0[kDkRows * Tile::RB], G1[kDkRows * Tile::RB];
+  __shared__ __align__(16) float L0[2 * kDkRows], L1[2 * kDkRows];     // lse (log2), delta
+  const KeyUnit un = key_unit(a);
+  const int G = a.Hq / a.Hkv, n = un.n, s0 = un.s0, t_lo = un.t_lo, t_hi = un.t_hi;
+  const int lane = lane_id(), wave = wave_uid(), half = lane >> 5;
+  const int sw = s0 + 32 * wave, s = sw + (lane & 31);
+  f32x16 dK[DT], dV[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) {
+    dK[dt] = zero16();
+    dV[dt] = zero16();
+  }
+  if (t_lo < t_hi && s0 < n) {
+    Frag<bf16> K[KK], V[KK];
+    const size_t at = ((size_t)un.bk * a.T + min(s, n - 1)) * D + 8 * half;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      K[kk] = load_frag(reinterpret_cast<const bf16*>(a.k) + at + 16 * kk);
+      V[kk] = load_frag(reinterpret_cast<const bf16*>(a.v) + at + 16 * kk);
+    }
+    const float c = a.scale * kLog2e;
+    const int nt = (t_hi - t_lo + kDkRows - 1) / kDkRows, total = nt * G;
+    const int rb = Tile::row_base(), cb = Tile::col_base();
+    const int row0 = (un.b * a.Hq + (un.bk % a.Hkv) * G);
+    int lg = 0, lt = 0;                    // head and tile of the next load
+    auto load = [&](unsigned char* Qs, unsigned char* Gs, float* Ls) {
+      if (lg >= G) return;
+      const size_t row = (size_t)(row0 + lg) * a.T;
+      const int tt = t_lo + lt * kDkRows;
+      Tile::template load<kDkRows, 4>(Qs, reinterpret_cast<const bf16*>(a.q) + row * D, tt, t_hi, wave);
+      Tile::template load<kDkRows, 4>(Gs, reinterpret_cast<const bf16*>(a.dO) + row * D, tt, t_hi, wave);
+      if (wave < 2) {
+        const float* src = (wave ? a.delta : a.lse2) + row + tt;
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<float*>(src), 0, uniform(min(t_hi - tt, kDkRows)) * 4, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(Ls + kDkRows * wave), 4, 4 * lane, 0, 0, 0);
+      }
+      if (++lt == nt) {
+        lt = 0;
+        ++lg;
+      }
+    };
+    auto step = [&](const unsigned char* Qs, const unsigned char* Gs, const float* Ls, int tile0) {
+#pragma unroll
+      for (int u = 0; u < kDkRows / 32; ++u) {
+        const int tt = tile0 + 32 * u;
+        if (sw > tt + 31 || (sw >= a.sinks && tt - (sw + 31) >= a.window)) continue;
+        f32x16 S = zero16(), dP = zero16();
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) mma32(S, Tile::row_frag(Qs, rb, 32 * u, kk), K[kk]);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) mma32(dP, Tile::row_frag(Gs, rb, 32 * u, kk), V[kk]);
+        const bool full = sw + 31 <= tt && (tt + 31 - sw < a.window || sw + 32 <= a.sinks);
+        if (!full) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int t = tt + acc_row(r, half);
+            const bool see = (s <= t) & ((t - s < a.window) | (s < a.sinks));
+            S[r] = see ? S[r] : -INFINITY;
+            dP[r] = see ? dP[r] : 0.f;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 32 * u + 8 * q + 4 * half);
+          const f32x4 de = *reinterpret_cast<const f32x4*>(Ls + kDkRows + 32 * u + 8 * q + 4 * half);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            S[4 * q + e] = __builtin_amdgcn_exp2f(S[4 * q + e] * c - ls[e]);
+            dP[4 * q + e] = S[4 * q + e] * (dP[4 * q + e] - de[e]);
+          }
+        }
+        // p and ds rounded to bf16 for their products with dO and q
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          Frag<bf16> P, F;
+          acc_frag(S, x, P);
+          acc_frag(dP, x, F);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) mma32(dV[dt], Tile::col_frag(Gs, cb, dt, 32 * u + 16 * x), P);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) mma32(dK[dt], Tile::col_frag(Qs, cb, dt, 32 * u + 16 * x), F);
+        }
+      }
+    };
+    load(Q0, G0, L0);
+    int ct = 0;                            // tile of the next step
+    for (int i = 0; i < total; i += 2) {
+      __syncthreads();
+      load(Q1, G1, L1);
+      step(Q0, G0, L0, t_lo + ct * kDkRows);
+      ct = ct + 1 == nt ? 0 : ct + 1;
+      __syncthreads();
+      load(Q0, G0, L0);
+      if (i + 1 < total) step(Q1, G1, L1, t_lo + ct * kDkRows);
+      ct = ct + 1 == nt ? 0 : ct + 1;
+    }
+  }
+  store_key_grads<bf16, D>(a, un, s, wave, dK, dV);
+}
+
+// ------------------------------------------------------------------ fp32
+// The same two passes with one tile in LDS (padded rows, staged through registers).
+template <int D>
+__global__ __launch_bounds__(256) void swa_dq_f32_kernel(SwaArgs a) {
+  using T = float;
   using St = RowStage<T, kDqK, D, 256>;
   constexpr int LD = St::LD;
   extern __shared__ __align__(16) unsigned char smem[];
   T* Ks = reinterpret_cast<T*>(smem);
   T* Vs = Ks + kDqK * LD;
-  const int G = a.Hq / a.Hkv, NQ = (a.T + kDqQ - 1) / kDqQ;
-  const int unit = xcd_unit(a.B * a.Hq * NQ);
-  const int g = unit % G, qt = NQ - 1 - (unit / G) % NQ, bk = unit / (G * NQ);
-  const int b = bk / a.Hkv, hq = (bk % a.Hkv) * G + g;
-  const int n = seq_len(a.lens, b, a.T);
-  const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
-  const int t0 = qt * kDqQ, tw = t0 + 32 * wave, t = tw + (lane & 31);
-  const size_t row = (size_t)(b * a.Hq + hq) * a.T;
-  const T* kb = reinterpret_cast<const T*>(a.k) + (size_t)bk * a.T * D;
-  const T* vb = reinterpret_cast<const T*>(a.v) + (size_t)bk * a.T * D;
+  const DqUnit un = dq_unit(a, kDqQ);
+  const int n = un.n, t0 = un.t0, lane = lane_id(), wave = wave_uid(), half = lane >> 5;
+  const int tw = t0 + 32 * wave, t = tw + (lane & 31);
+  const size_t row = (size_t)(un.b * a.Hq + un.hq) * a.T;
+  const T* kb = reinterpret_cast<const T*>(a.k) + (size_t)un.bk * a.T * D;
+  const T* vb = reinterpret_cast<const T*>(a.v) + (size_t)un.bk * a.T * D;
 
   f32x16 dQ[D / 32];
 #pragma unroll
@@ -41,8 +359,6 @@ __global__ __launch_bounds__(256) void swa_dq_kernel(SwaArgs a) {
   if (t0 < n) {
     Frag<T> Q[D / 16], dO[D / 16];
     const size_t at = (row + min(t, n - 1)) * D + 8 * half;
-    // delta_t from the product of the rows of o with dO, formed as dO . v is below: a token
-    // that sees one key has o = v, and its ds is zero to the last bit
     f32x16 od = zero16();
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
@@ -50,32 +366,26 @@ __global__ __launch_bounds__(256) void swa_dq_kernel(SwaArgs a) {
       dO[kk] = load_frag(reinterpret_cast<const T*>(a.dO) + at + 16 * kk);
       mma32(od, load_frag(reinterpret_cast<const T*>(a.o) + at + 16 * kk), dO[kk]);
     }
-    float delta = 0.f;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) delta = acc_row(r, half) == (lane & 31) ? od[r] : delta;
-    const float other = __shfl_xor(delta, 32);
-    if (((lane >> 2) & 1) != half) delta = other;
-    if (half == 0 && t < n) a.delta[row + t] = delta;
+    const float delta = diagonal(od);
+    const float lse2 = log2_lse(a.lse[row + min(t, n - 1)]);
+    if (half == 0 && t < n) {
+      a.delta[row + t] = delta;
+      a.lse2[row + t] = lse2;
+    }
     const float c = a.scale * kLog2e;
-    const float lse = a.lse[row + min(t, n - 1)];
-    const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;    // no visible weight: p = 0
-    const int hi = min(t0 + kDqQ, n);
-    const int kt_lo = max(0, t0 - a.window + 1) / kDqK, kt_hi = (hi - 1) / kDqK;
-    const int nsink = min((min(a.sinks, hi) + kDqK - 1) / kDqK, kt_lo);
-    const int ntile = nsink + kt_hi - kt_lo + 1;
-    auto tile = [&](int i) { return (i < nsink ? i : kt_lo + i - nsink) * kDqK; };
+    const KeyTiles<kDqK> tile(t0, min(t0 + kDqQ, n), a.window, a.sinks);
     St kst, vst;
-    kst.load(kb, tile(0), n);
-    vst.load(vb, tile(0), n);
-    for (int i = 0; i < ntile; ++i) {
-      const int s0 = tile(i);
+    kst.load(kb, tile[0], n);
+    vst.load(vb, tile[0], n);
+    for (int i = 0; i < tile.count; ++i) {
+      const int s0 = tile[i];
       __syncthreads();
       kst.store(Ks);
       vst.store(Vs);
       __syncthreads();
-      if (i + 1 < ntile) {
-        kst.load(kb, tile(i + 1), n);
-        vst.load(vb, tile(i + 1), n);
+      if (i + 1 < tile.count) {
+        kst.load(kb, tile[i + 1], n);
+        vst.load(vb, tile[i + 1], n);
       }
 #pragma unroll
       for (int u = 0; u < kDqK / 32; ++u) {
@@ -116,42 +426,21 @@ __global__ __launch_bounds__(256) void swa_dq_kernel(SwaArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ dk, dv
-// Workgroup = 128 keys of one key head (32 a wave, a lane owns one key), over the tokens that
-// see them inside the window and all heads of the group.  The tokens behind the window of a
-// tile that holds sinks see only the sinks: they are cut into n_far ranges with workgroups of
-// their own, whose sums, like the tile's, go to `part` and are added by swa_sink_kernel.
 constexpr int kDkQ = 32;
 
-template <typename T, int D>
-__global__ __launch_bounds__(256) void swa_dkdv_kernel(SwaArgs a) {
+template <int D>
+__global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
+  using T = float;
   using St = RowStage<T, kDkQ, D, 256>;
   constexpr int LD = St::LD, KT = kSwaKeyTile;
   extern __shared__ __align__(16) unsigned char smem[];
   T* Qs = reinterpret_cast<T*>(smem);
   T* Gs = Qs + kDkQ * LD;                                  // dO
   float* Ls = reinterpret_cast<float*>(Gs + kDkQ * LD);    // lse in the log2 domain, delta
-  const int G = a.Hq / a.Hkv, NK = (a.T + KT - 1) / KT;
-  const int per = NK + a.n_sink_tiles * a.n_far;           // units of one key head
-  const int unit = xcd_unit(a.B * a.Hkv * per);
-  const int bk = unit / per, w = unit % per;
-  const bool far = w >= NK;
-  const int kt = far ? (w - NK) / a.n_far : w, fi = far ? (w - NK) % a.n_far : 0;
-  const int b = bk / a.Hkv;
-  const int n = seq_len(a.lens, b, a.T);
-  const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
-  const int s0 = kt * KT, sw = s0 + 32 * wave, s = sw + (lane & 31);
-  // tokens of this unit
-  const long long band = (long long)s0 + KT - 1 + a.window;          // first token that sees no key of the tile
-  int t_lo, t_hi;
-  if (!far) {
-    t_lo = s0;
-    t_hi = (int)min((long long)n, band);
-  } else {
-    const long long f = band + (long long)fi * a.far_len;
-    t_lo = (int)min((long long)n, f);
-    t_hi = (int)min((long long)n, f + a.far_len);
-  }
+  const KeyUnit un = key_unit(a);
+  const int G = a.Hq / a.Hkv, bk = un.bk, b = un.b, n = un.n, s0 = un.s0, t_lo = un.t_lo, t_hi = un.t_hi;
+  const int lane = lane_id(), wave = wave_uid(), half = lane >> 5;
+  const int sw = s0 + 32 * wave, s = sw + (lane & 31);
   f32x16 dK[D / 32], dV[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) {
@@ -177,9 +466,8 @@ __global__ __launch_bounds__(256) void swa_dkdv_kernel(SwaArgs a) {
       gst.load(reinterpret_cast<const T*>(a.dO) + row * D, tt, t_hi);
       if (threadIdx.x < kDkQ) {
         const int t = tt + threadIdx.x;
-        // past the end, or no visible weight: p = exp2(. - inf) = 0
-        const float lse = t < t_hi ? a.lse[row + t] : -INFINITY;
-        lst = lse == -INFINITY ? INFINITY : lse * kLog2e;
+        // (past the end: p = exp2(. - inf) = 0)
+        lst = t < t_hi ? a.lse2[row + t] : INFINITY;
         dst = t < t_hi ? a.delta[row + t] : 0.f;
       }
     };
@@ -232,23 +520,7 @@ __global__ __launch_bounds__(256) void swa_dkdv_kernel(SwaArgs a) {
       }
     }
   }
-  if (kt < a.n_sink_tiles && a.n_far > 0) {
-    float* dst = a.part + ((((size_t)bk * a.n_sink_tiles + kt) * (1 + a.n_far) + (far ? 1 + fi : 0)) * 2 * KT +
-                           32 * wave + (lane & 31)) * D;
-    store_column<float, D>(dst, dK, a.scale);
-    store_column<float, D>(dst + (size_t)KT * D, dV, 1.f);
-  } else if (s < a.T) {
-    if (s >= n) {
-#pragma unroll
-      for (int dt = 0; dt < D / 32; ++dt) {
-        dK[dt] = zero16();
-        dV[dt] = zero16();
-      }
-    }
-    const size_t row = ((size_t)bk * a.T + s) * D;
-    store_column<T, D>(reinterpret_cast<T*>(a.dk) + row, dK, a.scale);
-    store_column<T, D>(reinterpret_cast<T*>(a.dv) + row, dV, 1.f);
-  }
+  store_key_grads<T, D>(a, un, s, wave, dK, dV);
 }
 
 // dk, dv of the tiles that hold sinks: the sums of the tile's window and far ranges, in order.
@@ -271,13 +543,18 @@ __global__ __launch_bounds__(256) void swa_sink_kernel(SwaArgs a) {
 
 template <typename T, int D>
 static hipError_t launch(const SwaArgs& a, hipStream_t st) {
-  constexpr size_t lds_q = sizeof(T) * 2 * kDqK * RowStage<T, kDqK, D, 256>::LD;
-  constexpr size_t lds_k = sizeof(T) * 2 * kDkQ * RowStage<T, kDkQ, D, 256>::LD + sizeof(float) * 2 * kDkQ;
-  hipError_t e =
-      launch_kernel<lds_q>(swa_dq_kernel<T, D>, dim3(a.B * a.Hq * ((a.T + kDqQ - 1) / kDqQ)), 256, a, st);
-  if (e != hipSuccess) return e;
-  const int per = (a.T + kSwaKeyTile - 1) / kSwaKeyTile + a.n_sink_tiles * a.n_far;
-  e = launch_kernel<lds_k>(swa_dkdv_kernel<T, D>, dim3(a.B * a.Hkv * per), 256, a, st);
+  const dim3 grid_q(a.B * a.Hq * ((a.T + kDqQ - 1) / kDqQ));
+  const dim3 grid_k(a.B * a.Hkv * ((a.T + kSwaKeyTile - 1) / kSwaKeyTile + a.n_sink_tiles * a.n_far));
+  hipError_t e;
+  if constexpr (sizeof(T) == 2) {
+    e = launch_kernel<0>(swa_dq_bf16_kernel<D>, grid_q, 256, a, st);
+    if (e == hipSuccess) e = launch_kernel<0>(swa_dkdv_bf16_kernel<D>, grid_k, 256, a, st);
+  } else {
+    constexpr size_t lds_q = sizeof(T) * 2 * kDqK * RowStage<T, kDqK, D, 256>::LD;
+    constexpr size_t lds_k = sizeof(T) * 2 * kDkQ * RowStage<T, kDkQ, D, 256>::LD + sizeof(float) * 2 * kDkQ;
+    e = launch_kernel<lds_q>(swa_dq_f32_kernel<D>, grid_q, 256, a, st);
+    if (e == hipSuccess) e = launch_kernel<lds_k>(swa_dkdv_f32_kernel<D>, grid_k, 256, a, st);
+  }
   if (e != hipSuccess || a.n_sink_tiles * a.n_far == 0) return e;
   return launch_kernel<0>(swa_sink_kernel<T, D>, dim3(a.B * a.Hkv * a.n_sink_tiles, 8), 256, a, st);
 }
