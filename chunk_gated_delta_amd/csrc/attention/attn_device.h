@@ -116,54 +116,52 @@ __device__ __forceinline__ int wave_uid() { return uniform(threadIdx.x >> 6); }
 // ROWS bf16 token rows of width D in LDS, brought there by buffer loads that write LDS directly
 // (16 bytes a lane, 1 KB a wave and instruction, no registers on the way; rows past a sequence's
 // end lie past the buffer's end and read as zero).  Such loads fill LDS in lane order, so rows
-// cannot be padded; instead the 16-byte piece c of row r stands at piece c ^ swz(r) of the
-// row, which leaves both read patterns free of bank conflicts: 16 rows at one piece (row
-// operand), and 4 rows at 4 neighbouring pieces (transpose read).
+// cannot be padded.  The tile is D / 32 blocks of [ROWS][64 bytes], and the 16-byte piece c of
+// a row's 64 stands at piece c ^ (r / 4) % 4: both read patterns are free of bank conflicts (16
+// rows at one piece for the row operand, 4 rows at 4 neighbouring pieces for the transpose
+// read), and blocks and rows are reached by constant offsets from two addresses a pattern.
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
-template <int D>
+template <int D, int ROWS>
 struct SwzTile {
-  static constexpr int RB = 2 * D;                       // bytes of a row
-  static constexpr int RPI = 1024 / RB;                  // rows of an instruction
-  static constexpr int PR = D / 8;                       // pieces of a row
-  static __device__ __forceinline__ int swz(int r) {
-    return D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-  }
+  static constexpr int RB = 2 * D, BLOCK = 64 * ROWS, bytes = ROWS * RB;
   // rows r0 .. r0 + ROWS - 1 of base [n][D] by NW waves
-  template <int ROWS, int NW>
+  template <int NW>
   static __device__ __forceinline__ void load(unsigned char* tile, const bf16* base, int r0, int n, int wave) {
-    constexpr int PER = ROWS / RPI / NW;
-    static_assert(PER * RPI * NW == ROWS, "whole instructions per wave");
+    constexpr int INS = bytes / 1024, PER = INS / NW, IPB = BLOCK / 1024;   // instructions: all, a wave's, a block's
+    static_assert(PER * NW == INS && IPB % PER == 0, "a wave's instructions lie in one block");
     const int lane = lane_id(), rows = uniform(max(0, min(n - r0, ROWS)));
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16*>(base) + (size_t)r0 * D, 0, rows * RB, 0x00020000);
+    const int rl = lane >> 2, voff = rl * RB + (((lane & 3) ^ ((rl >> 2) & 3)) << 4);
+    const int blk = wave * PER / IPB, row0 = wave * PER % IPB * 16;
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int at = (wave * PER + u) * RPI, rl = lane / PR;
-      // swz(at + rl): at is a multiple of the rows of an instruction
-      const int voff = rl * RB + (((lane % PR) ^ swz(at + rl)) << 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(tile + at * RB), 16, voff, at * RB, 0, 0);
-    }
+    for (int u = 0; u < PER; ++u)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(tile + blk * BLOCK + (row0 + 16 * u) * 64), 16, voff,
+                                               blk * 64 + (row0 + 16 * u) * RB, 0, 0);
   }
-  // byte offset of the lane's row operand, contraction block 0 (block kk: ^ (kk << 5))
+  // byte offset of the lane's row operand (odd contraction blocks: ^ 32)
   static __device__ __forceinline__ int row_base() {
     const int lane = lane_id(), r = lane & 31;
-    return r * RB + (((lane >> 5) ^ swz(r)) << 4);
+    return r * 64 + (((lane >> 5) ^ ((r >> 2) & 3)) << 4);
   }
+  // rows r0 .. r0 + 31, 16-deep block kk
   static __device__ __forceinline__ Frag<bf16> row_frag(const unsigned char* tile, int base, int r0, int kk) {
     Frag<bf16> f;
-    f.v = *(lds_bf16x8*)(tile + r0 * RB + (base ^ (kk << 5)));
+    f.v = *(lds_bf16x8*)(tile + (kk >> 1) * BLOCK + r0 * 64 + (base ^ ((kk & 1) << 5)));
     return f;
   }
-  // byte offset of the lane's transpose read, columns 0 (columns 32 dt: ^ (dt << 6); rows + 8: ^ 32, + 8 RB)
+  // byte offset of the lane's transpose read (rows + 8: ^ 32, + 512)
   static __device__ __forceinline__ int col_base() {
     const int lane = lane_id(), s = lane & 15, g = lane >> 4, r = 4 * (g >> 1) + (s >> 2);
-    return r * RB + (((2 * (g & 1) + ((s & 3) >> 1)) ^ swz(r)) << 4) + 8 * (s & 1);
+    return r * 64 + (((2 * (g & 1) + ((s & 3) >> 1)) ^ ((r >> 2) & 3)) << 4) + 8 * (s & 1);
   }
   // columns 32 dt .. + 31 as rows of an A operand, contraction over rows k0 + 8 (j / 4) + 4 (l / 32) + j % 4
+  // (k0 a multiple of 16)
   static __device__ __forceinline__ Frag<bf16> col_frag(const unsigned char* tile, int base, int dt, int k0) {
-    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(tile + k0 * RB + (base ^ (dt << 6))));
-    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(tile + (k0 + 8) * RB + (base ^ (dt << 6) ^ 32)));
+    const unsigned char* p = tile + dt * BLOCK + k0 * 64;
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + base));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 512 + (base ^ 32)));
     Frag<bf16> f;
     f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     return f;

@@ -31,7 +31,7 @@ struct SwaArgs {
   float* part;
   int n_sink_tiles, n_far, far_len;
 };
-constexpr int kSwaKeyTile = 128;       // keys of a workgroup of the dk / dv pass
+constexpr int kSwaKeyTile = 64;        // keys of a workgroup of the dk / dv pass
 
 // Accumulated attention weight of every key.
 struct WeightArgs {

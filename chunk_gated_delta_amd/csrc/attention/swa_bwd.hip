@@ -41,8 +41,7 @@ __device__ __forceinline__ float diagonal(const f32x16& c) {
 // no visible weight (lse = -inf): every p is exp2(. - inf) = 0
 __device__ __forceinline__ float log2_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-// A workgroup of the dk / dv pass: kSwaKeyTile keys of one key head (32 a wave, a lane owns one
-// key), over the tokens t_lo .. t_hi - 1 that see them inside the window and all heads of the
+// A workgroup of the dk / dv pass: kSwaKeyTile keys of one key head (a lane owns one key), over the tokens t_lo .. t_hi - 1 that see them inside the window and all heads of the
 // group.  The tokens behind the window of a tile that holds sinks see only the sinks: they are cut
 // into n_far ranges with workgroups of their own, whose sums, like the tile's, go to `part`
 // and are added by swa_sink_kernel.
@@ -70,11 +69,11 @@ __device__ __forceinline__ KeyUnit key_unit(const SwaArgs& a) {
   return u;
 }
 template <typename T, int D>
-__device__ __forceinline__ void store_key_grads(const SwaArgs& a, const KeyUnit& u, int s, int wave, f32x16 (&dK)[D / 32],
+__device__ __forceinline__ void store_key_grads(const SwaArgs& a, const KeyUnit& u, int s, int kb, f32x16 (&dK)[D / 32],
                                                 f32x16 (&dV)[D / 32]) {
   constexpr int KT = kSwaKeyTile;
   if (u.part >= 0) {
-    float* dst = a.part + ((((size_t)u.bk * a.n_sink_tiles + u.kt) * (1 + a.n_far) + u.part) * 2 * KT + 32 * wave +
+    float* dst = a.part + ((((size_t)u.bk * a.n_sink_tiles + u.kt) * (1 + a.n_far) + u.part) * 2 * KT + 32 * kb +
                            (lane_id() & 31)) * D;
     store_column<float, D>(dst, dK, a.scale);
     store_column<float, D>(dst + (size_t)KT * D, dV, 1.f);
@@ -92,6 +91,28 @@ __device__ __forceinline__ void store_key_grads(const SwaArgs& a, const KeyUnit&
   }
 }
 
+// x of the waves th = 1 added to that of the waves th = 0, through 128 D bytes of LDS a pair
+template <int D>
+__device__ __forceinline__ void join_halves(float* park, int th, f32x16 (&x)[D / 32]) {
+  const int lane = lane_id();
+  __syncthreads();
+  if (th) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      store4(park + (i * 64 + lane) * 4, f32x4{x[i / 4][4 * (i & 3)], x[i / 4][4 * (i & 3) + 1], x[i / 4][4 * (i & 3) + 2],
+                                               x[i / 4][4 * (i & 3) + 3]});
+  }
+  __syncthreads();
+  if (!th) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const f32x4 y = load4f(park + (i * 64 + lane) * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i / 4][4 * (i & 3) + e] += y[e];
+    }
+  }
+}
+
 // ------------------------------------------------------------------ bf16: dq
 // Workgroup = 128 tokens of one query head (32 a wave, a lane owns one), tiles of 64 keys in two
 // pairs of swizzled LDS buffers as in the forward pass.  delta comes from the rounded o
@@ -101,10 +122,10 @@ constexpr int kExactKeys = 64;
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
-  using Tile = SwzTile<D>;
+  using Tile = SwzTile<D, kDqK>;
   constexpr int KK = D / 16, DT = D / 32;
-  __shared__ __align__(16) unsigned char K0[kDqK * Tile::RB], K1[kDqK * Tile::RB];
-  __shared__ __align__(16) unsigned char V0[kDqK * Tile::RB], V1[kDqK * Tile::RB];
+  __shared__ __align__(16) unsigned char K0[Tile::bytes], K1[Tile::bytes];
+  __shared__ __align__(16) unsigned char V0[Tile::bytes], V1[Tile::bytes];
   const DqUnit un = dq_unit(a, kDqQ);
   const int n = un.n, t0 = un.t0, lane = lane_id(), wave = wave_uid(), half = lane >> 5;
   const int tw = t0 + 32 * wave, t = tw + (lane & 31);
@@ -166,8 +187,8 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
     };
     auto load = [&](unsigned char* Ks, unsigned char* Vs, int i) {
       if (i < kt.count) {
-        Tile::template load<kDqK, 4>(Ks, kb, kt[i], n, wave);
-        Tile::template load<kDqK, 4>(Vs, vb, kt[i], n, wave);
+        Tile::template load<4>(Ks, kb, kt[i], n, wave);
+        Tile::template load<4>(Vs, vb, kt[i], n, wave);
       }
     };
     auto sweep = [&](auto&& step) {
@@ -226,21 +247,24 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
 }
 
 // ------------------------------------------------------------------ bf16: dk, dv
-// Tiles of 64 tokens (q, dO, lse, delta) in two sets of LDS buffers.  Rows at and past t_hi read as
+// Workgroup = 64 keys: waves 0, 1 take 32 keys each with the first 32 tokens of every tile, waves 2,
+// 3 the same keys with the last 32 (their sums are added at the end), so that a unit of work is
+// half as long as with 32 keys a wave.  Tiles of 64 tokens (q, dO, lse, delta) in two sets of LDS buffers.  Rows at and past t_hi read as
 // zero throughout: p = 1 there, but dO = 0 and ds = 1 (0 - 0), so they add nothing.
 constexpr int kDkRows = 64;
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
-  using Tile = SwzTile<D>;
+  using Tile = SwzTile<D, kDkRows>;
   constexpr int KK = D / 16, DT = D / 32;
-  __shared__ __align__(16) unsigned char Q0[kDkRows * Tile::RB], Q1[kDkRows * Tile::RB];
-  __shared__ __align__(16) unsigned char G0[kDkRows * Tile::RB], G1[kDkRows * Tile::RB];
+  __shared__ __align__(16) unsigned char Q0[Tile::bytes], Q1[Tile::bytes];
+  __shared__ __align__(16) unsigned char G0[Tile::bytes], G1[Tile::bytes];
   __shared__ __align__(16) float L0[2 * kDkRows], L1[2 * kDkRows];     // lse (log2), delta
   const KeyUnit un = key_unit(a);
   const int G = a.Hq / a.Hkv, n = un.n, s0 = un.s0, t_lo = un.t_lo, t_hi = un.t_hi;
   const int lane = lane_id(), wave = wave_uid(), half = lane >> 5;
-  const int sw = s0 + 32 * wave, s = sw + (lane & 31);
+  const int kb = wave & 1, th = wave >> 1;
+  const int sw = s0 + 32 * kb, s = sw + (lane & 31);
   f32x16 dK[DT], dV[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) {
@@ -257,15 +281,15 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
     }
     const float c = a.scale * kLog2e;
     const int nt = (t_hi - t_lo + kDkRows - 1) / kDkRows, total = nt * G;
-    const int rb = Tile::row_base(), cb = Tile::col_base();
+    const int rt = Tile::row_base() + 2048 * th, ct0 = Tile::col_base() + 2048 * th;   // (32 rows of a block)
     const int row0 = (un.b * a.Hq + (un.bk % a.Hkv) * G);
     int lg = 0, lt = 0;                    // head and tile of the next load
     auto load = [&](unsigned char* Qs, unsigned char* Gs, float* Ls) {
       if (lg >= G) return;
       const size_t row = (size_t)(row0 + lg) * a.T;
       const int tt = t_lo + lt * kDkRows;
-      Tile::template load<kDkRows, 4>(Qs, reinterpret_cast<const bf16*>(a.q) + row * D, tt, t_hi, wave);
-      Tile::template load<kDkRows, 4>(Gs, reinterpret_cast<const bf16*>(a.dO) + row * D, tt, t_hi, wave);
+      Tile::template load<4>(Qs, reinterpret_cast<const bf16*>(a.q) + row * D, tt, t_hi, wave);
+      Tile::template load<4>(Gs, reinterpret_cast<const bf16*>(a.dO) + row * D, tt, t_hi, wave);
       if (wave < 2) {
         const float* src = (wave ? a.delta : a.lse2) + row + tt;
         const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
@@ -278,15 +302,13 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
       }
     };
     auto step = [&](const unsigned char* Qs, const unsigned char* Gs, const float* Ls, int tile0) {
-#pragma unroll
-      for (int u = 0; u < kDkRows / 32; ++u) {
-        const int tt = tile0 + 32 * u;
-        if (sw > tt + 31 || (sw >= a.sinks && tt - (sw + 31) >= a.window)) continue;
+      const int tt = tile0 + 32 * th;
+      if (!(sw > tt + 31 || (sw >= a.sinks && tt - (sw + 31) >= a.window))) {
         f32x16 S = zero16(), dP = zero16();
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) mma32(S, Tile::row_frag(Qs, rb, 32 * u, kk), K[kk]);
+        for (int kk = 0; kk < KK; ++kk) mma32(S, Tile::row_frag(Qs, rt, 0, kk), K[kk]);
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) mma32(dP, Tile::row_frag(Gs, rb, 32 * u, kk), V[kk]);
+        for (int kk = 0; kk < KK; ++kk) mma32(dP, Tile::row_frag(Gs, rt, 0, kk), V[kk]);
         const bool full = sw + 31 <= tt && (tt + 31 - sw < a.window || sw + 32 <= a.sinks);
         if (!full) {
 #pragma unroll
@@ -299,8 +321,8 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 32 * u + 8 * q + 4 * half);
-          const f32x4 de = *reinterpret_cast<const f32x4*>(Ls + kDkRows + 32 * u + 8 * q + 4 * half);
+          const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 32 * th + 8 * q + 4 * half);
+          const f32x4 de = *reinterpret_cast<const f32x4*>(Ls + kDkRows + 32 * th + 8 * q + 4 * half);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             S[4 * q + e] = __builtin_amdgcn_exp2f(S[4 * q + e] * c - ls[e]);
@@ -314,9 +336,9 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
           acc_frag(S, x, P);
           acc_frag(dP, x, F);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) mma32(dV[dt], Tile::col_frag(Gs, cb, dt, 32 * u + 16 * x), P);
+          for (int dt = 0; dt < DT; ++dt) mma32(dV[dt], Tile::col_frag(Gs, ct0, dt, 16 * x), P);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) mma32(dK[dt], Tile::col_frag(Qs, cb, dt, 32 * u + 16 * x), F);
+          for (int dt = 0; dt < DT; ++dt) mma32(dK[dt], Tile::col_frag(Qs, ct0, dt, 16 * x), F);
         }
       }
     };
@@ -333,7 +355,11 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
       ct = ct + 1 == nt ? 0 : ct + 1;
     }
   }
-  store_key_grads<bf16, D>(a, un, s, wave, dK, dV);
+  // add the sums of the two token halves, dK and then dV, through the tiles' memory
+  float* park = reinterpret_cast<float*>(kb ? G0 : Q0);
+  join_halves<D>(park, th, dK);
+  join_halves<D>(park, th, dV);
+  if (!th) store_key_grads<bf16, D>(a, un, s, kb, dK, dV);
 }
 
 // ------------------------------------------------------------------ fp32
@@ -426,13 +452,13 @@ __global__ __launch_bounds__(256) void swa_dq_f32_kernel(SwaArgs a) {
   }
 }
 
-constexpr int kDkQ = 32;
+constexpr int kDkQ = 64;
 
 template <int D>
 __global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
   using T = float;
   using St = RowStage<T, kDkQ, D, 256>;
-  constexpr int LD = St::LD, KT = kSwaKeyTile;
+  constexpr int LD = St::LD;
   extern __shared__ __align__(16) unsigned char smem[];
   T* Qs = reinterpret_cast<T*>(smem);
   T* Gs = Qs + kDkQ * LD;                                  // dO
@@ -440,7 +466,7 @@ __global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
   const KeyUnit un = key_unit(a);
   const int G = a.Hq / a.Hkv, bk = un.bk, b = un.b, n = un.n, s0 = un.s0, t_lo = un.t_lo, t_hi = un.t_hi;
   const int lane = lane_id(), wave = wave_uid(), half = lane >> 5;
-  const int sw = s0 + 32 * wave, s = sw + (lane & 31);
+  const int kb = wave & 1, th = wave >> 1, sw = s0 + 32 * kb, s = sw + (lane & 31);
   f32x16 dK[D / 32], dV[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) {
@@ -473,7 +499,7 @@ __global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
     };
     load(0);
     for (int i = 0; i < total; ++i) {
-      const int tt = t_lo + (i % nt) * kDkQ;
+      const int tt = t_lo + (i % nt) * kDkQ + 32 * th;
       __syncthreads();
       qst.store(Qs);
       gst.store(Gs);
@@ -487,14 +513,14 @@ __global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
       f32x16 S = zero16(), dP = zero16();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        mma32(S, frag_rows32(Qs, LD, 0, 16 * kk), K[kk]);
-        mma32(dP, frag_rows32(Gs, LD, 0, 16 * kk), V[kk]);
+        mma32(S, frag_rows32(Qs, LD, 32 * th, 16 * kk), K[kk]);
+        mma32(dP, frag_rows32(Gs, LD, 32 * th, 16 * kk), V[kk]);
       }
       const bool full = sw + 31 <= tt && (tt + 31 - sw < a.window || sw + 32 <= a.sinks);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 8 * q + 4 * half);
-        const f32x4 de = *reinterpret_cast<const f32x4*>(Ls + kDkQ + 8 * q + 4 * half);
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 32 * th + 8 * q + 4 * half);
+        const f32x4 de = *reinterpret_cast<const f32x4*>(Ls + kDkQ + 32 * th + 8 * q + 4 * half);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 4 * q + e;
@@ -514,13 +540,16 @@ __global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
         acc_frag(dP, x, F);
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) {
-          mma32(dV[dt], frag_cols32(Gs, LD, 32 * dt, 16 * x), P);
-          mma32(dK[dt], frag_cols32(Qs, LD, 32 * dt, 16 * x), F);
+          mma32(dV[dt], frag_cols32(Gs, LD, 32 * dt, 32 * th + 16 * x), P);
+          mma32(dK[dt], frag_cols32(Qs, LD, 32 * dt, 32 * th + 16 * x), F);
         }
       }
     }
   }
-  store_key_grads<T, D>(a, un, s, wave, dK, dV);
+  T* park = kb ? Gs : Qs;
+  join_halves<D>(park, th, dK);
+  join_halves<D>(park, th, dV);
+  if (!th) store_key_grads<T, D>(a, un, s, kb, dK, dV);
 }
 
 // dk, dv of the tiles that hold sinks: the sums of the tile's window and far ranges, in order.

@@ -50,10 +50,10 @@ constexpr int kFwdK = 64;
 
 template <int D, int NQ>
 __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
-  using Tile = SwzTile<D>;
+  using Tile = SwzTile<D, kFwdK>;
   constexpr int QW = 32 * NQ, QT = 4 * QW, KK = D / 16, DT = D / 32;
-  __shared__ __align__(16) unsigned char K0[kFwdK * Tile::RB], K1[kFwdK * Tile::RB];
-  __shared__ __align__(16) unsigned char V0[kFwdK * Tile::RB], V1[kFwdK * Tile::RB];
+  __shared__ __align__(16) unsigned char K0[Tile::bytes], K1[Tile::bytes];
+  __shared__ __align__(16) unsigned char V0[Tile::bytes], V1[Tile::bytes];
   const FwdUnit un = fwd_unit(a, QT);
   const int n = un.n, t0 = un.t0, lane = lane_id(), wave = wave_uid(), half = lane >> 5;
   const int tw = t0 + QW * wave;
@@ -71,8 +71,8 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
   }
   if (t0 < n) {
     const KeyTiles<kFwdK> kt(t0, min(t0 + QT, n), a.window, a.sinks);
-    Tile::template load<kFwdK, 4>(K0, kb, kt[0], n, wave);
-    Tile::template load<kFwdK, 4>(V0, vb, kt[0], n, wave);
+    Tile::template load<4>(K0, kb, kt[0], n, wave);
+    Tile::template load<4>(V0, vb, kt[0], n, wave);
     Frag<bf16> Q[NQ][KK];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
@@ -149,14 +149,14 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
     for (int i = 0; i < kt.count; i += 2) {
       __syncthreads();
       if (i + 1 < kt.count) {
-        Tile::template load<kFwdK, 4>(K1, kb, kt[i + 1], n, wave);
-        Tile::template load<kFwdK, 4>(V1, vb, kt[i + 1], n, wave);
+        Tile::template load<4>(K1, kb, kt[i + 1], n, wave);
+        Tile::template load<4>(V1, vb, kt[i + 1], n, wave);
       }
       step(K0, V0, kt[i]);
       __syncthreads();
       if (i + 2 < kt.count) {
-        Tile::template load<kFwdK, 4>(K0, kb, kt[i + 2], n, wave);
-        Tile::template load<kFwdK, 4>(V0, vb, kt[i + 2], n, wave);
+        Tile::template load<4>(K0, kb, kt[i + 2], n, wave);
+        Tile::template load<4>(V0, vb, kt[i + 2], n, wave);
       }
       if (i + 1 < kt.count) step(K1, V1, kt[i + 1]);
     }
