@@ -120,8 +120,21 @@ __device__ __forceinline__ int wave_uid() { return uniform(threadIdx.x >> 6); }
 // a row's 64 stands at piece c ^ (r / 4) % 4: both read patterns are free of bank conflicts (16
 // rows at one piece for the row operand, 4 rows at 4 neighbouring pieces for the transpose
 // read), and blocks and rows are reached by constant offsets from two addresses a pattern.
+// The compiler does not always wait for such loads before the LDS they fill is read: every reader
+// waits itself (wait_loads<N>: all but the N youngest vector memory operations of the wave are
+// done, loads among themselves in order), then, where other waves read, the barrier.
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void loads_and_barrier() {
+  wait_loads<0>();
+  __syncthreads();
+}
+
 template <int D, int ROWS>
 struct SwzTile {
   static constexpr int RB = 2 * D, BLOCK = 64 * ROWS, bytes = ROWS * RB;
@@ -180,6 +193,7 @@ struct KeyTiles {
   __device__ __forceinline__ int operator[](int i) const { return (i < nsink ? i : lo + i - nsink) * KT; }
 };
 
+// tokens of sequence b, the same for every lane of the wave
 __device__ __forceinline__ int seq_len(const int* lens, int b, int T) {
   return uniform(lens ? min(max(lens[b], 0), T) : T);
 }

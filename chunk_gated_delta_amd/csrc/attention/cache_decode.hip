@@ -64,8 +64,11 @@ __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, i
   }
 }
 
-template <typename T, int D, int NT, bool BUDGET>
-__global__ __launch_bounds__(kDecThreads) void cache_decode_kernel(CacheArgs a) {
+// ------------------------------------------------------------------ fp32
+// 32 slots of a wave at a time through registers, the v rows on into LDS of the wave's own.
+template <int D, int NT, bool BUDGET>
+__global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs a) {
+  using T = float;
   constexpr int LD = D + Pad<T>::v, PR = D / 8, NV = 32 * PR / 64, LDM = D + 4;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ unsigned long long red[kDecThreads / 64];
@@ -173,33 +176,20 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_kernel(CacheArgs a) 
           x[4 * u + i] = __builtin_amdgcn_exp2f(S[u][i] - mn);
           l[nt] += x[4 * u + i];
         }
-      // the weights are rounded to the operand type for the product with v (the sum l is not)
-      if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) P[nt].v[j] = (bf16)x[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          P[nt].lo[j] = x[j];
-          P[nt].hi[j] = x[4 + j];
-        }
+      for (int j = 0; j < 4; ++j) {
+        P[nt].lo[j] = x[j];
+        P[nt].hi[j] = x[4 + j];
       }
     }
     // V^T operand, its contraction in the order of P: slots 4 lg + j, then 16 + 4 lg + j
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) {
       Frag<T> F;
-      if constexpr (sizeof(T) == 2) {
-        bf16* q = Vs + (4 * lg + (lr >> 2)) * LD + 16 * dt + 4 * (lr & 3);
-        const i16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)q);
-        const i16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q + 16 * LD));
-        F.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
-      } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          F.lo[j] = Vs[(4 * lg + j) * LD + 16 * dt + lr];
-          F.hi[j] = Vs[(16 + 4 * lg + j) * LD + 16 * dt + lr];
-        }
+      for (int j = 0; j < 4; ++j) {
+        F.lo[j] = Vs[(4 * lg + j) * LD + 16 * dt + lr];
+        F.hi[j] = Vs[(16 + 4 * lg + j) * LD + 16 * dt + lr];
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma(O[nt][dt], F, P[nt]);
@@ -263,52 +253,297 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_kernel(CacheArgs a) 
   }
 }
 
-// Joins the ranges of one key head: the output (range 0's workgroup), and for a cache kept by
-// weight the weights of the workgroup's own range of slots.
+// ------------------------------------------------------------------ bf16
+// A wave's 32 slots at a time, brought to LDS by buffer loads that write it directly: the k rows of the
+// next slots are on their way while these are worked on, and so are its v rows, each wave in
+// buffers of its own and without barriers.  Rows of slots that are not live lie past the
+// buffer's end and read as zero.  Layout: blocks of 32 columns, [32][64 bytes], piece c of a row at
+// c ^ f(row), f = row bits 2 and 3 swapped: 16 rows at one piece, and 8 rows at 2 pieces, are
+// free of bank conflicts.
+template <int D>
+struct WaveRows {
+  static constexpr int RB = 2 * D, BLOCK = 2048, bytes = 32 * RB, kLoads = bytes / 1024;   // instructions of a load
+  static __device__ __forceinline__ int swz(int r) { return ((r >> 1) & 2) | ((r >> 3) & 1); }
+  // rows j0 .. j0 + 31 of base, those whose bit of `live` is set (one descriptor: 32 rows)
+  static __device__ __forceinline__ void load(unsigned char* dst, const bf16* base, int j0, unsigned live) {
+    const int lane = lane_id(), rl = lane >> 2;
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16*>(base) + (size_t)j0 * D, 0, bytes, 0x00020000);
+    const int voff = rl * RB + (((lane & 3) ^ swz(rl)) << 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int v = (live >> (16 * h + rl)) & 1 ? voff : bytes;      // (past the end)
+#pragma unroll
+      for (int blk = 0; blk < D / 32; ++blk)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(dst + blk * BLOCK + 1024 * h), 16, v,
+                                                 blk * 64 + 16 * h * RB, 0, 0);
+    }
+  }
+  // rows 16 u .. + 15 as A operand, 32-deep block kk
+  static __device__ __forceinline__ Frag<bf16> row_frag(const unsigned char* src, int u, int kk) {
+    const int lane = lane_id(), r = lane & 15;
+    Frag<bf16> f;
+    f.v = *(lds_bf16x8*)(src + kk * BLOCK + 1024 * u + r * 64 + (((lane >> 4) ^ swz(r)) << 4));
+    return f;
+  }
+  // columns 16 dt .. + 15 as rows of an A operand, contraction over rows 4 g + j, then 16 + 4 g + j
+  static __device__ __forceinline__ Frag<bf16> col_frag(const unsigned char* src, int dt) {
+    const int lane = lane_id(), s = lane & 15, r = 4 * (lane >> 4) + (s >> 2);
+    const unsigned char* p = src + (dt >> 1) * BLOCK + r * 64 +
+                             (((2 * (dt & 1) + ((s & 3) >> 1)) ^ swz(r)) << 4) + 8 * (s & 1);
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 1024));
+    Frag<bf16> f;
+    f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    return f;
+  }
+};
+
+template <int D, int NT, bool BUDGET>
+__global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf16_kernel(CacheArgs a) {
+  using Rows = WaveRows<D>;
+  __shared__ __align__(16) unsigned char Ks[4 * Rows::bytes], Vs[4 * Rows::bytes];
+  __shared__ unsigned long long red[kDecThreads / 64];
+  __shared__ float ml[4][16][2];
+  __shared__ float st[16 * NT][2];
+  const int G = a.Hq / a.Hkv;
+  const int split = uniform(blockIdx.x % a.n_split), bk = uniform(blockIdx.x / a.n_split), b = uniform(bk / a.Hkv);
+  const int lane = lane_id(), wave = wave_uid(), lr = lane & 15, lg = lane >> 4;
+  const int p = uniform(a.pos[b]);
+  bf16* ob = reinterpret_cast<bf16*>(a.o) + (size_t)bk * G * D;
+  if (p < 0) {                                   // no token: the cache stays as it is
+    if (split == 0) {
+      for (int i = threadIdx.x; i < G * D; i += kDecThreads) ob[i] = (bf16)0.f;
+      if (BUDGET && threadIdx.x == 0) a.slot[bk] = -1;
+    }
+    return;
+  }
+  const int at = uniform(BUDGET ? pick_slot(a, bk, p, red) : ring_slot(a, p));
+  if (BUDGET && split == 0 && threadIdx.x == 0) a.slot[bk] = at;
+  const int count = BUDGET ? a.C : min(p, a.C - 1) + 1;          // a ring holds its tokens from slot 0 up
+  const int lo = split * a.split_len, hi = min(min(lo + a.split_len, a.C), count);
+  bf16* ck = reinterpret_cast<bf16*>(a.cache_k) + (size_t)bk * a.C * D;
+  bf16* cv = reinterpret_cast<bf16*>(a.cache_v) + (size_t)bk * a.C * D;
+  const int* held = BUDGET ? a.cache_pos + (size_t)bk * a.C : nullptr;
+  // the new rows go to the cache first, by the workgroup that owns their slot and alone reads it
+  if (at >= lo && at < hi) {
+    if (threadIdx.x < D / 4) {
+      const int i = 8 * (threadIdx.x % (D / 8));
+      const bool is_v = threadIdx.x >= D / 8;
+      const bf16* src = reinterpret_cast<const bf16*>(is_v ? a.v : a.k) + (size_t)bk * D + i;
+      *reinterpret_cast<bf16x8*>((is_v ? cv : ck) + (size_t)at * D + i) = *reinterpret_cast<const bf16x8*>(src);
+    }
+    __syncthreads();
+  }
+  Frag<bf16> Q[NT][D / 32];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int g = min(16 * nt + lr, G - 1);
+#pragma unroll
+    for (int kk = 0; kk < D / 32; ++kk)
+      Q[nt][kk] = load_frag(reinterpret_cast<const bf16*>(a.q) + ((size_t)bk * G + g) * D + 32 * kk + 8 * lg);
+  }
+  const float c = a.scale * kLog2e;
+  f32x4 O[NT][D / 16];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = kNegBig;
+    l[nt] = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt) O[nt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  unsigned char* kw = Ks + wave * Rows::bytes;
+  unsigned char* vw = Vs + wave * Rows::bytes;
+  auto live_of = [&](int j0) -> unsigned {       // live slots of the 32, one bit each
+    const int j = j0 + (lane & 31);
+    bool on = j < hi;
+    if (BUDGET) on = on && (j == at || held[min(j, a.C - 1)] >= 0);
+    return (unsigned)__ballot(on);
+  };
+  const int first = lo + 32 * wave;
+  unsigned live = 0;
+  if (first < hi) {
+    live = live_of(first);
+    Rows::load(kw, ck, first, live);
+    Rows::load(vw, cv, first, live);
+  }
+  for (int j0 = first; j0 < hi; j0 += 128) {
+    const unsigned next = j0 + 128 < hi ? live_of(j0 + 128) : 0;
+    wait_loads<Rows::kLoads>();                  // this k has arrived (its v, issued after it, may not have)
+    f32x4 X[NT][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      Frag<bf16> K[D / 32];
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) K[kk] = Rows::row_frag(kw, u, kk);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        X[nt][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) mma(X[nt][u], K[kk], Q[nt][kk]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (j0 + 128 < hi) Rows::load(kw, ck, j0 + 128, next);
+    Frag<bf16> P[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * u + 4 * lg + i;
+          const float x = ((live >> r) & 1) ? X[nt][u][i] * c : -INFINITY;
+          X[nt][u][i] = x;
+          if (BUDGET && 16 * nt + lr < G && j0 + r < hi)
+            a.score[((size_t)bk * a.C + j0 + r) * G + 16 * nt + lr] = x;
+          mx = fmaxf(mx, x);
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      if (__any(mx > m[nt] + 8.f)) {             // rescale only when a maximum grows by 2^8
+        const float mn = fmaxf(m[nt], mx), alpha = __builtin_amdgcn_exp2f(m[nt] - mn);
+        m[nt] = mn;
+        l[nt] *= alpha;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) O[nt][dt] *= alpha;
+      }
+      // the weights are rounded to bf16 for the product with v (the sum l is not)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = __builtin_amdgcn_exp2f(X[nt][u][i] - m[nt]);
+          l[nt] += x;
+          P[nt].v[4 * u + i] = (bf16)x;
+        }
+    }
+    // this v has arrived (the next k, issued after it, may not have)
+    if (j0 + 128 < hi) wait_loads<Rows::kLoads>();
+    else wait_loads<0>();
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt) {
+      const Frag<bf16> F = Rows::col_frag(vw, dt);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma(O[nt][dt], F, P[nt]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (j0 + 128 < hi) Rows::load(vw, cv, j0 + 128, next);
+    live = next;
+  }
+  // join the waves, 16 heads at a time (4-float pieces of a row swizzled by the head)
+  float* mg = reinterpret_cast<float*>(Ks);                        // [4][16][D]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (16 * nt >= G) break;
+    float lt = l[nt] + __shfl_xor(l[nt], 16);
+    lt += __shfl_xor(lt, 32);
+    __syncthreads();
+    if (lg == 0) {
+      ml[wave][lr][0] = m[nt];
+      ml[wave][lr][1] = lt;
+    }
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt)
+      store4(mg + (wave * 16 + lr) * D + (((4 * dt + lg) ^ lr) << 2), O[nt][dt]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * D / 4; i += kDecThreads) {
+      const int h = i / (D / 4), c4 = i % (D / 4), g = 16 * nt + h;
+      if (g >= G) continue;
+      float M = kNegBig, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[w][h][0]);
+      f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w][h][0] - M);
+        L += f * ml[w][h][1];
+        x += load4f(mg + (w * 16 + h) * D + ((c4 ^ h) << 2)) * f;
+      }
+      if (a.n_split == 1) {
+        const float f = L > 0.f ? 1.f / L : 0.f;
+        store4(ob + (size_t)g * D + 4 * c4, x * f);
+        if (c4 == 0) {
+          st[g][0] = M;
+          st[g][1] = f;
+        }
+      } else {
+        float* dst = a.part + (((size_t)bk * a.n_split + split) * G + g) * (D + 4);
+        store4(dst + 4 + 4 * c4, x);
+        if (c4 == 0) {
+          dst[0] = M;
+          dst[1] = L;
+        }
+      }
+    }
+  }
+  if (BUDGET && a.n_split == 1) {
+    __syncthreads();                             // scores of all waves, and st
+    add_weights(a, bk, p, at, 0, a.C, &st[0][0]);
+  }
+}
+
+// Joins the ranges of one key head: the output (a workgroup per head of the group, its ranges'
+// partial sums read at once), and for a cache kept by weight the weights, a range of slots a workgroup.
+constexpr int kMaxSplit = 64;
 template <typename T, int D, bool BUDGET>
 __global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
   __shared__ float st[64][2];
-  const int G = a.Hq / a.Hkv;
-  const int split = BUDGET ? blockIdx.x % a.n_split : 0, bk = BUDGET ? blockIdx.x / a.n_split : blockIdx.x;
-  const int b = bk / a.Hkv, p = a.pos[b];
+  __shared__ float f[kMaxSplit];
+  const int G = a.Hq / a.Hkv, per = BUDGET ? G + a.n_split : G;
+  const int w = blockIdx.x % per, bk = blockIdx.x / per, p = a.pos[bk / a.Hkv];
   if (p < 0) return;
   const float* part = a.part + (size_t)bk * a.n_split * G * (D + 4);
-  if (threadIdx.x < G) {
-    float M = kNegBig, L = 0.f;
-    for (int s = 0; s < a.n_split; ++s) M = fmaxf(M, part[((size_t)s * G + threadIdx.x) * (D + 4)]);
-    for (int s = 0; s < a.n_split; ++s) {
-      const float* q = part + ((size_t)s * G + threadIdx.x) * (D + 4);
-      L += __builtin_amdgcn_exp2f(q[0] - M) * q[1];
+  auto stats = [&](int g) {                      // lanes of a wave: max and sum of head g over the ranges
+    const int lane = lane_id();
+    const float* q = part + ((size_t)min(lane, a.n_split - 1) * G + g) * (D + 4);
+    const float m = lane < a.n_split ? q[0] : kNegBig;
+    float M = m;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) M = fmaxf(M, __shfl_xor(M, o));
+    const float x = __builtin_amdgcn_exp2f(m - M);
+    float L = lane < a.n_split ? x * q[1] : 0.f;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) L += __shfl_xor(L, o);
+    if (lane == 0) {
+      st[g][0] = M;
+      st[g][1] = L > 0.f ? 1.f / L : 0.f;
     }
-    st[threadIdx.x][0] = M;
-    st[threadIdx.x][1] = L > 0.f ? 1.f / L : 0.f;
-  }
-  __syncthreads();
-  if (split == 0) {
-    T* ob = reinterpret_cast<T*>(a.o) + (size_t)bk * G * D;
-    for (int i = threadIdx.x; i < G * D / 4; i += kDecThreads) {
-      const int g = i / (D / 4), d = 4 * (i % (D / 4));
-      f32x4 x = {0.f, 0.f, 0.f, 0.f};
-      for (int s = 0; s < a.n_split; ++s) {
-        const float* q = part + ((size_t)s * G + g) * (D + 4);
-        x += load4f(q + 4 + d) * __builtin_amdgcn_exp2f(q[0] - st[g][0]);
-      }
-      store4(ob + (size_t)g * D + d, x * st[g][1]);
+    return x;
+  };
+  if (w < G) {
+    if (threadIdx.x < 64) f[threadIdx.x] = stats(w);
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d < D) {
+      float x = 0.f;
+      const float* q = part + (size_t)w * (D + 4) + 4 + d;
+#pragma unroll 8
+      for (int s = 0; s < a.n_split; ++s) x += q[(size_t)s * G * (D + 4)] * f[s];
+      reinterpret_cast<T*>(a.o)[((size_t)bk * G + w) * D + d] = to<T>(x * st[w][1]);
     }
-  }
-  if constexpr (BUDGET) {
-    const int lo = split * a.split_len, hi = min(lo + a.split_len, a.C);
+  } else if constexpr (BUDGET) {
+    for (int g = wave_uid(); g < G; g += kDecThreads / 64) (void)stats(g);
+    __syncthreads();
+    const int lo = (w - G) * a.split_len, hi = min(lo + a.split_len, a.C);
     add_weights(a, bk, p, a.slot[bk], lo, hi, &st[0][0]);
   }
 }
 
 template <typename T, int D, int NT, bool BUDGET>
 static hipError_t launch_nt(const CacheArgs& a, hipStream_t st) {
-  constexpr size_t lds = std::max(sizeof(T) * 4 * 32 * (D + Pad<T>::v), sizeof(float) * 4 * 16 * (D + 4));
-  const int units = a.B * a.Hkv;
-  hipError_t e = launch_kernel<lds>(cache_decode_kernel<T, D, NT, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);
+  const int units = a.B * a.Hkv, G = a.Hq / a.Hkv;
+  hipError_t e;
+  if constexpr (sizeof(T) == 2) {
+    e = launch_kernel<0>(cache_decode_bf16_kernel<D, NT, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);
+  } else {
+    constexpr size_t lds = std::max(sizeof(T) * 4 * 32 * (D + Pad<T>::v), sizeof(float) * 4 * 16 * (D + 4));
+    e = launch_kernel<lds>(cache_decode_f32_kernel<D, NT, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);
+  }
   if (e != hipSuccess || a.n_split == 1) return e;
-  return launch_kernel<0>(cache_join_kernel<T, D, BUDGET>, dim3(BUDGET ? units * a.n_split : units), kDecThreads, a, st);
+  return launch_kernel<0>(cache_join_kernel<T, D, BUDGET>, dim3(units * (BUDGET ? G + a.n_split : G)), kDecThreads, a, st);
 }
 template <typename T, int D, bool BUDGET>
 static hipError_t launch_g(const CacheArgs& a, hipStream_t st) {

@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256) void fill_rows_kernel(FillArgs a) {
     if (BUDGET) {
       p = a.cache_pos[row];
     } else {
-      const int last = seq_len(a.lens, (int)(bk / a.Hkv), a.T) - 1;
+      const int last = (a.lens ? min(max(a.lens[bk / a.Hkv], 0), a.T) : a.T) - 1;   // (lanes of several rows)
       if (j < a.sinks) {
         p = j <= last ? j : -1;
       } else {

@@ -194,10 +194,10 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
     auto sweep = [&](auto&& step) {
       load(K0, V0, 0);
       for (int i = 0; i < kt.count; i += 2) {
-        __syncthreads();
+        loads_and_barrier();
         load(K1, V1, i + 1);
         if (seen(kt[i])) step(K0, V0, kt[i]);
-        __syncthreads();
+        loads_and_barrier();
         load(K0, V0, i + 2);
         if (i + 1 < kt.count && seen(kt[i + 1])) step(K1, V1, kt[i + 1]);
       }
@@ -345,11 +345,11 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
     load(Q0, G0, L0);
     int ct = 0;                            // tile of the next step
     for (int i = 0; i < total; i += 2) {
-      __syncthreads();
+      loads_and_barrier();
       load(Q1, G1, L1);
       step(Q0, G0, L0, t_lo + ct * kDkRows);
       ct = ct + 1 == nt ? 0 : ct + 1;
-      __syncthreads();
+      loads_and_barrier();
       load(Q0, G0, L0);
       if (i + 1 < total) step(Q1, G1, L1, t_lo + ct * kDkRows);
       ct = ct + 1 == nt ? 0 : ct + 1;

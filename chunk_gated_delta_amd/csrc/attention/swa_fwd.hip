@@ -147,13 +147,13 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
       }
     };
     for (int i = 0; i < kt.count; i += 2) {
-      __syncthreads();
+      loads_and_barrier();
       if (i + 1 < kt.count) {
         Tile::template load<4>(K1, kb, kt[i + 1], n, wave);
         Tile::template load<4>(V1, vb, kt[i + 1], n, wave);
       }
       step(K0, V0, kt[i]);
-      __syncthreads();
+      loads_and_barrier();
       if (i + 2 < kt.count) {
         Tile::template load<4>(K0, kb, kt[i + 2], n, wave);
         Tile::template load<4>(V0, vb, kt[i + 2], n, wave);
