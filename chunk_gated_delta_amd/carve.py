@@ -641,46 +641,74 @@ def decode_step(q, k, v, log_g, w, S, b=None, L=64, content=None, o=None):
 def _call(what, dev, *args):
     """One library call on the tensors' device and its current stream; raises on a status."""
     fn = getattr(load_library(), what)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _raise(code, what)
+            code = fn(*args, _raw_stream(index))
+    if code != 0:
+        _raise(code, what)
+
+
+# handle of a device's current stream, without a Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _fit(t, name, shape, dtype, dev):
+    """The address of a tensor that fits; _check raises for one that does not."""
+    if t is None:
+        raise TypeError(f"{name}: a tensor is required")
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _check(t, name, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _fit_opt(t, name, shape, dtype, dev):
+    return None if t is None else _fit(t, name, shape, dtype, dev)
+
+
 def _heads(q, k, ndim):
     """(B, Hq, Hkv, T, D, device, dtype) of q [B,Hq,(T,)D] and k [B,Hkv,(T,)D]."""
     if q.dim() != ndim or k.dim() != ndim:
         raise ValueError(f"q and k must have {ndim} dimensions, got {q.dim()} and {k.dim()}")
-    B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
-    Hkv = k.shape[1]
-    T = q.shape[2] if ndim == 4 else 1
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     if not q.is_cuda:
         raise ValueError(f"q: expected a GPU tensor, got {q.device}")
-    return B, Hq, Hkv, T, D, q.device, q.dtype
+    if ndim == 4:
+        B, Hq, T, D = q.shape
+    else:
+        (B, Hq, D), T = q.shape, 1
+    return B, Hq, k.shape[1], T, D, q.device, q.dtype
 
 
 def _swa_shape(q, k, ndim, window, sinks, scale):
     B, Hq, Hkv, T, D, dev, dt = _heads(q, k, ndim)
     s = carve_swa_shape(B, Hq, Hkv, T, D, window, sinks, D ** -0.5 if scale is None else scale, _dtype_code(q))
-    return s, dev, dt
+    return B, Hq, Hkv, T, D, dev, dt, s, ctypes.byref(s)
 
 
 def _workspace(what, s, dev, workspace):
-    need = getattr(load_library(), what + "_workspace_size")(ctypes.byref(s))
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace is not None and workspace.device != dev:
-        raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return workspace, _addr(workspace), nbytes
+    """(workspace kept alive, its address, its bytes) for a call that needs one."""
+    need = getattr(load_library(), what)(s)
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        have = workspace.numel() * workspace.element_size()
+        if have >= need:
+            return workspace, workspace.data_ptr(), have
+    if not need:
+        return None, None, 0
+    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, workspace.data_ptr(), need
 
 
 def swa_fwd(q, k, v, window, sinks=0, scale=None, lens=None, o=None, lse=None):
@@ -691,36 +719,29 @@ def swa_fwd(q, k, v, window, sinks=0, scale=None, lens=None, o=None, lse=None):
     s < sinks).  scale: factor of q . k, 1/sqrt(D) by default.  lens [B] int32 or None: tokens of
     each sequence of a padded batch; rows behind them give o = 0 and lse = -inf.  Outputs may be
     passed preallocated."""
-    s, dev, dt = _swa_shape(q, k, 4, window, sinks, scale)
-    kv = (s.B, s.Hkv, s.T, s.D)
-    _check(k, "k", kv, dt, dev)
-    _check(v, "v", kv, dt, dev)
-    _check(lens, "lens", (s.B,), torch.int32, dev)
+    B, Hq, Hkv, T, D, dev, dt, s, sp = _swa_shape(q, k, 4, window, sinks, scale)
+    kv, rows = (B, Hkv, T, D), (B, Hq, T)
     if o is None:
         o = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
-    _check(o, "o", q.shape, dt, dev)
-    _check(lse, "lse", q.shape[:3], torch.float32, dev)
-    _call("carve_swa_fwd", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(v), _addr(lens), _addr(o), _addr(lse))
+        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+    _call("carve_swa_fwd", dev, sp, q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev),
+          _fit_opt(lens, "lens", (B,), torch.int32, dev), _fit(o, "o", q.shape, dt, dev),
+          _fit(lse, "lse", rows, torch.float32, dev))
     return o, lse
 
 
 def swa_bwd(q, k, v, o, lse, dO, window, sinks=0, scale=None, lens=None, workspace=None):
     """Backward of swa_fwd from its o and lse: {"dq", "dk", "dv"} for the output gradient dO
     [B,Hq,T,D] (dk, dv summed over the query heads that share the key head)."""
-    s, dev, dt = _swa_shape(q, k, 4, window, sinks, scale)
-    kv = (s.B, s.Hkv, s.T, s.D)
-    _check(k, "k", kv, dt, dev)
-    _check(v, "v", kv, dt, dev)
-    _check(o, "o", q.shape, dt, dev)
-    _check(dO, "dO", q.shape, dt, dev)
-    _check(lse, "lse", q.shape[:3], torch.float32, dev)
-    _check(lens, "lens", (s.B,), torch.int32, dev)
+    B, Hq, Hkv, T, D, dev, dt, s, sp = _swa_shape(q, k, 4, window, sinks, scale)
+    kv = (B, Hkv, T, D)
+    ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev),
+            _fit_opt(lens, "lens", (B,), torch.int32, dev), _fit(o, "o", q.shape, dt, dev),
+            _fit(lse, "lse", (B, Hq, T), torch.float32, dev), _fit(dO, "dO", q.shape, dt, dev))
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
-    workspace, ws, nbytes = _workspace("carve_swa_bwd", s, dev, workspace)
-    _call("carve_swa_bwd", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(v), _addr(lens), _addr(o), _addr(lse),
-          _addr(dO), _addr(g["dq"]), _addr(g["dk"]), _addr(g["dv"]), ws, nbytes)
+    workspace, ws, nbytes = _workspace("carve_swa_bwd_workspace_size", sp, dev, workspace)
+    _call("carve_swa_bwd", dev, sp, *ptrs, g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), ws, nbytes)
     return g
 
 
@@ -733,13 +754,11 @@ def swa_cache(B, Hkv, D, window, sinks=0, dtype=torch.bfloat16, device="cuda"):
 def swa_fill(k, v, cache_k, cache_v, window, sinks=0, lens=None):
     """Writes a prompt's k, v [B,Hkv,T,D] (starting at position 0; lens [B] int32 of T tokens) into
     the ring cache [B,Hkv,sinks+window,D]; slots that hold none of its tokens stay as they are."""
-    s, dev, dt = _swa_shape(k, k, 4, window, sinks, 1.0)
-    _check(v, "v", k.shape, dt, dev)
-    cache = (s.B, s.Hkv, window + sinks, s.D)
-    _check(cache_k, "cache_k", cache, dt, dev)
-    _check(cache_v, "cache_v", cache, dt, dev)
-    _check(lens, "lens", (s.B,), torch.int32, dev)
-    _call("carve_swa_fill", dev, ctypes.byref(s), _addr(k), _addr(v), _addr(lens), _addr(cache_k), _addr(cache_v))
+    B, _, Hkv, T, D, dev, dt, s, sp = _swa_shape(k, k, 4, window, sinks, 1.0)
+    cache = (B, Hkv, window + sinks, D)
+    _call("carve_swa_fill", dev, sp, k.data_ptr(), _fit(v, "v", k.shape, dt, dev),
+          _fit_opt(lens, "lens", (B,), torch.int32, dev), _fit(cache_k, "cache_k", cache, dt, dev),
+          _fit(cache_v, "cache_v", cache, dt, dev))
 
 
 def swa_decode(q, k, v, cache_k, cache_v, pos, window, sinks=0, scale=None, o=None, workspace=None):
@@ -748,20 +767,15 @@ def swa_decode(q, k, v, cache_k, cache_v, pos, window, sinks=0, scale=None, o=No
     q [B,Hq,D], k, v [B,Hkv,D], cache_k, cache_v [B,Hkv,sinks+window,D]; pos [B] int32, on the
     device: tokens of each sequence before this one (negative: no token; o = 0, cache untouched).
     pos is not advanced: one array serves all layers of a step."""
-    s, dev, dt = _swa_shape(q, k, 3, window, sinks, scale)
-    kv = (s.B, s.Hkv, s.D)
-    cache = (s.B, s.Hkv, window + sinks, s.D)
-    _check(k, "k", kv, dt, dev)
-    _check(v, "v", kv, dt, dev)
-    _check(cache_k, "cache_k", cache, dt, dev)
-    _check(cache_v, "cache_v", cache, dt, dev)
-    _check(pos, "pos", (s.B,), torch.int32, dev)
+    B, Hq, Hkv, _, D, dev, dt, s, sp = _swa_shape(q, k, 3, window, sinks, scale)
+    kv, cache = (B, Hkv, D), (B, Hkv, window + sinks, D)
+    ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev),
+            _fit(cache_k, "cache_k", cache, dt, dev), _fit(cache_v, "cache_v", cache, dt, dev),
+            _fit(pos, "pos", (B,), torch.int32, dev))
     if o is None:
         o = torch.empty_like(q)
-    _check(o, "o", q.shape, dt, dev)
-    workspace, ws, nbytes = _workspace("carve_swa_decode", s, dev, workspace)
-    _call("carve_swa_decode", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(v), _addr(cache_k), _addr(cache_v),
-          _addr(pos), _addr(o), ws, nbytes)
+    workspace, ws, nbytes = _workspace("carve_swa_decode_workspace_size", sp, dev, workspace)
+    _call("carve_swa_decode", dev, sp, *ptrs, _fit(o, "o", q.shape, dt, dev), ws, nbytes)
     return o
 
 
@@ -771,16 +785,13 @@ def budget_weights(q, k, lse, window=None, sinks=0, scale=None, lens=None, weigh
     the same window and sinks (window None: all tokens before, as swa_fwd with window >= T)."""
     if window is None:
         window = max(q.shape[2], 1)
-    s, dev, dt = _swa_shape(q, k, 4, window, sinks, scale)
-    _check(k, "k", (s.B, s.Hkv, s.T, s.D), dt, dev)
-    _check(lse, "lse", q.shape[:3], torch.float32, dev)
-    _check(lens, "lens", (s.B,), torch.int32, dev)
+    B, Hq, Hkv, T, D, dev, dt, s, sp = _swa_shape(q, k, 4, window, sinks, scale)
+    ptrs = (q.data_ptr(), _fit(k, "k", (B, Hkv, T, D), dt, dev), _fit(lse, "lse", (B, Hq, T), torch.float32, dev),
+            _fit_opt(lens, "lens", (B,), torch.int32, dev))
     if weights is None:
-        weights = torch.empty((s.B, s.Hkv, s.T), dtype=torch.float32, device=dev)
-    _check(weights, "weights", (s.B, s.Hkv, s.T), torch.float32, dev)
-    workspace, ws, nbytes = _workspace("carve_budget_weights", s, dev, workspace)
-    _call("carve_budget_weights", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(lse), _addr(lens), _addr(weights),
-          ws, nbytes)
+        weights = torch.empty((B, Hkv, T), dtype=torch.float32, device=dev)
+    workspace, ws, nbytes = _workspace("carve_budget_weights_workspace_size", sp, dev, workspace)
+    _call("carve_budget_weights", dev, sp, *ptrs, _fit(weights, "weights", (B, Hkv, T), torch.float32, dev), ws, nbytes)
     return weights
 
 
@@ -792,13 +803,11 @@ def budget_cache(B, Hkv, D, C, dtype=torch.bfloat16, device="cuda"):
             torch.full((B, Hkv, C), -1, dtype=torch.int32, device=device))
 
 
-def _check_cache(cache, B, Hkv, C, D, dt, dev):
+def _fit_cache(cache, B, Hkv, C, D, dt, dev):
     cache_k, cache_v, cache_w, cache_pos = cache
-    _check(cache_k, "cache_k", (B, Hkv, C, D), dt, dev)
-    _check(cache_v, "cache_v", (B, Hkv, C, D), dt, dev)
-    _check(cache_w, "cache_w", (B, Hkv, C), torch.float32, dev)
-    _check(cache_pos, "cache_pos", (B, Hkv, C), torch.int32, dev)
-    return tuple(map(_addr, cache))
+    rows, slots = (B, Hkv, C, D), (B, Hkv, C)
+    return (_fit(cache_k, "cache_k", rows, dt, dev), _fit(cache_v, "cache_v", rows, dt, dev),
+            _fit(cache_w, "cache_w", slots, torch.float32, dev), _fit(cache_pos, "cache_pos", slots, torch.int32, dev))
 
 
 def budget_keep(k, v, weights, C, sinks=0, recent=1, lens=None, cache=None):
@@ -807,13 +816,11 @@ def budget_keep(k, v, weights, C, sinks=0, recent=1, lens=None, cache=None):
     cache_pos) as budget_cache makes it, or `cache` itself, overwritten (rows of empty slots stay)."""
     B, _, Hkv, T, D, dev, dt = _heads(k, k, 4)
     s = carve_budget_shape(B, Hkv, Hkv, T, D, C, sinks, recent, 1.0, _dtype_code(k))
-    _check(v, "v", k.shape, dt, dev)
-    _check(weights, "weights", (B, Hkv, T), torch.float32, dev)
-    _check(lens, "lens", (B,), torch.int32, dev)
     if cache is None:
         cache = budget_cache(B, Hkv, D, C, dt, dev)
-    ptrs = _check_cache(cache, B, Hkv, C, D, dt, dev)
-    _call("carve_budget_keep", dev, ctypes.byref(s), _addr(k), _addr(v), _addr(weights), _addr(lens), *ptrs)
+    _call("carve_budget_keep", dev, ctypes.byref(s), k.data_ptr(), _fit(v, "v", k.shape, dt, dev),
+          _fit(weights, "weights", (B, Hkv, T), torch.float32, dev), _fit_opt(lens, "lens", (B,), torch.int32, dev),
+          *_fit_cache(cache, B, Hkv, C, D, dt, dev))
     return tuple(cache)
 
 
@@ -828,19 +835,16 @@ def budget_decode(q, k, v, cache, pos, sinks=0, recent=1, scale=None, o=None, sl
     B, Hq, Hkv, _, D, dev, dt = _heads(q, k, 3)
     C = cache[0].shape[2]
     s = carve_budget_shape(B, Hq, Hkv, 1, D, C, sinks, recent, D ** -0.5 if scale is None else scale, _dtype_code(q))
-    _check(k, "k", (B, Hkv, D), dt, dev)
-    _check(v, "v", (B, Hkv, D), dt, dev)
-    _check(pos, "pos", (B,), torch.int32, dev)
-    ptrs = _check_cache(cache, B, Hkv, C, D, dt, dev)
+    sp, kv, slots = ctypes.byref(s), (B, Hkv, D), (B, Hkv)
+    ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev),
+            *_fit_cache(cache, B, Hkv, C, D, dt, dev), _fit(pos, "pos", (B,), torch.int32, dev))
     if o is None:
         o = torch.empty_like(q)
     if slot is None:
-        slot = torch.empty((B, Hkv), dtype=torch.int32, device=dev)
-    _check(o, "o", q.shape, dt, dev)
-    _check(slot, "slot", (B, Hkv), torch.int32, dev)
-    workspace, ws, nbytes = _workspace("carve_budget_decode", s, dev, workspace)
-    _call("carve_budget_decode", dev, ctypes.byref(s), _addr(q), _addr(k), _addr(v), *ptrs, _addr(pos), _addr(o),
-          _addr(slot), ws, nbytes)
+        slot = torch.empty(slots, dtype=torch.int32, device=dev)
+    workspace, ws, nbytes = _workspace("carve_budget_decode_workspace_size", sp, dev, workspace)
+    _call("carve_budget_decode", dev, sp, *ptrs, _fit(o, "o", q.shape, dt, dev),
+          _fit(slot, "slot", slots, torch.int32, dev), ws, nbytes)
     return o, slot
 
 

@@ -112,11 +112,20 @@ void weight_plan(const carve_swa_shape* s, int* n_chunk, int* chunk) {
   *n_chunk = ceil_div(s->T, *chunk);
 }
 
-// Slot ranges of a decode call: one per key head when there are enough heads for the 256
-// compute units twice over, else ranges of whole 128-slot steps.
-void split_plan(int units, int C, int* n_split, int* split_len) {
+int row_bytes(int D, carve_dtype dtype) { return D * (dtype == CARVE_BF16 ? 2 : 4); }
+
+// Slot ranges of a decode call and waves of a workgroup.  From 512 key heads on, a workgroup of 4
+// waves each (two a compute unit); from 256 on, and where a key head's rows are few enough that
+// one compute unit reads them in less time than the second launch that joins ranges takes,
+// a workgroup of 8.  Else ranges of whole 128-slot steps, for two workgroups a compute unit.
+constexpr size_t kOneUnitBytes = 640 << 10;
+void split_plan(int units, int C, int row_bytes, int* n_split, int* split_len, int* waves) {
   int n = 1;
-  if (units < 512) n = std::min({ceil_div(512, units), ceil_div(C, 128), 64});
+  *waves = units < 512 ? 8 : 4;
+  if (units < 256 && (size_t)C * 2 * row_bytes > kOneUnitBytes) {
+    n = std::min({ceil_div(512, units), ceil_div(C, 128), 64});
+    *waves = 4;
+  }
   *split_len = ceil_div(ceil_div(C, n), 128) * 128;
   *n_split = ceil_div(C, *split_len);
 }
@@ -216,8 +225,8 @@ carve_status carve_swa_fill(const carve_swa_shape* s, const void* k, const void*
 
 size_t carve_swa_decode_workspace_size(const carve_swa_shape* s) {
   if (check_swa(s) != CARVE_OK || s->T != 1 || empty(s) || s->Hq / s->Hkv > kMaxGroup) return 0;
-  int n, len;
-  split_plan(s->B * s->Hkv, s->window + s->sinks, &n, &len);
+  int n, len, waves;
+  split_plan(s->B * s->Hkv, s->window + s->sinks, row_bytes(s->D, s->dtype), &n, &len, &waves);
   const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n);
   return bytes ? bytes + 256 : 0;
 }
@@ -251,7 +260,7 @@ carve_status carve_swa_decode(const carve_swa_shape* s, const void* q, const voi
   a.cache_v = cache_v;
   a.pos = pos;
   a.o = o;
-  split_plan(a.B * a.Hkv, a.C, &a.n_split, &a.split_len);
+  split_plan(a.B * a.Hkv, a.C, row_bytes(s->D, s->dtype), &a.n_split, &a.split_len, &a.waves);
   const size_t need = part_bytes(a.B * a.Hkv, a.Hq / a.Hkv, a.D, a.n_split);
   if (need && (!workspace || workspace_bytes < need + 256)) return CARVE_ERR_WORKSPACE;
   a.part = reinterpret_cast<float*>(up256(reinterpret_cast<uintptr_t>(workspace)));
@@ -330,8 +339,8 @@ carve_status carve_budget_keep(const carve_budget_shape* s, const void* k, const
 
 size_t carve_budget_decode_workspace_size(const carve_budget_shape* s) {
   if (check_budget(s) != CARVE_OK || s->T != 1 || s->B == 0 || s->Hq == 0 || s->Hq / s->Hkv > kMaxGroup) return 0;
-  int n, len;
-  split_plan(s->B * s->Hkv, s->C, &n, &len);
+  int n, len, waves;
+  split_plan(s->B * s->Hkv, s->C, row_bytes(s->D, s->dtype), &n, &len, &waves);
   return part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n) + (size_t)s->B * s->Hq * s->C * sizeof(float) + 256;
 }
 
@@ -367,7 +376,7 @@ carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, con
   a.pos = pos;
   a.o = o;
   a.slot = slot;
-  split_plan(a.B * a.Hkv, a.C, &a.n_split, &a.split_len);
+  split_plan(a.B * a.Hkv, a.C, row_bytes(s->D, s->dtype), &a.n_split, &a.split_len, &a.waves);
   const size_t need = carve_budget_decode_workspace_size(s);
   if (!workspace || workspace_bytes < need) return CARVE_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(up256(reinterpret_cast<uintptr_t>(workspace)));

@@ -65,6 +65,7 @@ struct CacheArgs {
   void* o;                    // [B,Hq,D]
   int* slot;                  // [B,Hkv]
   int n_split, split_len;     // slots of a workgroup
+  int waves;                  // of a workgroup, 4 or 8 (bf16, at most 16 heads a group)
   float* part;                // [B*Hkv][n_split][G][2 + D]: max, sum, sum of p v
   float* score;               // [B*Hkv][C][G] scores (log2 domain), budget cache only
 };

@@ -21,11 +21,12 @@ __device__ __forceinline__ unsigned weight_order(float w) {
   const unsigned u = __builtin_bit_cast(unsigned, w + 0.f);
   return w != w ? 0xffffffffu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+template <int NW>
 __device__ __forceinline__ int pick_slot(const CacheArgs& a, int bk, int p, unsigned long long* red) {
   const float* w = a.cache_w + (size_t)bk * a.C;
   const int* held = a.cache_pos + (size_t)bk * a.C;
   unsigned long long best = ~0ull;
-  for (int j = threadIdx.x; j < a.C; j += kDecThreads) {
+  for (int j = threadIdx.x; j < a.C; j += 64 * NW) {
     const int h = held[j];
     const int cls = h == p ? 0 : h < 0 ? 1 : (h >= a.sinks && h <= p - a.recent) ? 2 : 3;
     const unsigned o = cls < 2 ? 0u : weight_order(w[j]);
@@ -40,7 +41,7 @@ __device__ __forceinline__ int pick_slot(const CacheArgs& a, int bk, int p, unsi
   if (lane_id() == 0) red[wave_id()] = best;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kDecThreads / 64; ++i) best = red[i] < best ? red[i] : best;
+  for (int i = 0; i < NW; ++i) best = red[i] < best ? red[i] : best;
   return (int)(best & ((1u << 30) - 1));
 }
 
@@ -50,9 +51,10 @@ __device__ __forceinline__ int ring_slot(const CacheArgs& a, int p) {
 
 // Adds the token's weights to the cache's: slots lo .. hi - 1, with max and sum of every head
 // (log2 domain) in st[head] = {m, 1 / l}.
+template <int NW>
 __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st) {
   const int G = a.Hq / a.Hkv;
-  for (int j = lo + threadIdx.x; j < hi; j += kDecThreads) {
+  for (int j = lo + threadIdx.x; j < hi; j += 64 * NW) {
     const size_t i = (size_t)bk * a.C + j;
     const bool mine = j == at;
     if (!mine && a.cache_pos[i] < 0) continue;
@@ -86,7 +88,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
     }
     return;
   }
-  const int at = BUDGET ? pick_slot(a, bk, p, red) : ring_slot(a, p);
+  const int at = BUDGET ? pick_slot<4>(a, bk, p, red) : ring_slot(a, p);
   if (BUDGET && split == 0 && threadIdx.x == 0) a.slot[bk] = at;
   const int count = BUDGET ? a.C : min(p, a.C - 1) + 1;          // a ring holds its tokens from slot 0 up
   const int lo = split * a.split_len, hi = min(min(lo + a.split_len, a.C), count);
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
   }
   if (BUDGET && a.n_split == 1) {
     __syncthreads();                             // scores of all waves, and st
-    add_weights(a, bk, p, at, 0, a.C, &st[0][0]);
+    add_weights<4>(a, bk, p, at, 0, a.C, &st[0][0]);
   }
 }
 
@@ -299,12 +301,13 @@ struct WaveRows {
   }
 };
 
-template <int D, int NT, bool BUDGET>
-__global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf16_kernel(CacheArgs a) {
+template <int D, int NT, int NW, bool BUDGET>
+__global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_kernel(CacheArgs a) {
   using Rows = WaveRows<D>;
-  __shared__ __align__(16) unsigned char Ks[4 * Rows::bytes], Vs[4 * Rows::bytes];
-  __shared__ unsigned long long red[kDecThreads / 64];
-  __shared__ float ml[4][16][2];
+  constexpr int STEP = 32 * NW;
+  __shared__ __align__(16) unsigned char Ks[NW * Rows::bytes], Vs[NW * Rows::bytes];
+  __shared__ unsigned long long red[NW];
+  __shared__ float ml[NW][16][2];
   __shared__ float st[16 * NT][2];
   const int G = a.Hq / a.Hkv;
   const int split = uniform(blockIdx.x % a.n_split), bk = uniform(blockIdx.x / a.n_split), b = uniform(bk / a.Hkv);
@@ -313,12 +316,12 @@ __global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf1
   bf16* ob = reinterpret_cast<bf16*>(a.o) + (size_t)bk * G * D;
   if (p < 0) {                                   // no token: the cache stays as it is
     if (split == 0) {
-      for (int i = threadIdx.x; i < G * D; i += kDecThreads) ob[i] = (bf16)0.f;
+      for (int i = threadIdx.x; i < G * D; i += 64 * NW) ob[i] = (bf16)0.f;
       if (BUDGET && threadIdx.x == 0) a.slot[bk] = -1;
     }
     return;
   }
-  const int at = uniform(BUDGET ? pick_slot(a, bk, p, red) : ring_slot(a, p));
+  const int at = uniform(BUDGET ? pick_slot<NW>(a, bk, p, red) : ring_slot(a, p));
   if (BUDGET && split == 0 && threadIdx.x == 0) a.slot[bk] = at;
   const int count = BUDGET ? a.C : min(p, a.C - 1) + 1;          // a ring holds its tokens from slot 0 up
   const int lo = split * a.split_len, hi = min(min(lo + a.split_len, a.C), count);
@@ -368,8 +371,8 @@ __global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf1
     Rows::load(kw, ck, first, live);
     Rows::load(vw, cv, first, live);
   }
-  for (int j0 = first; j0 < hi; j0 += 128) {
-    const unsigned next = j0 + 128 < hi ? live_of(j0 + 128) : 0;
+  for (int j0 = first; j0 < hi; j0 += STEP) {
+    const unsigned next = j0 + STEP < hi ? live_of(j0 + STEP) : 0;
     wait_loads<Rows::kLoads>();                  // this k has arrived (its v, issued after it, may not have)
     f32x4 X[NT][2];
 #pragma unroll
@@ -385,7 +388,7 @@ __global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf1
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (j0 + 128 < hi) Rows::load(kw, ck, j0 + 128, next);
+    if (j0 + STEP < hi) Rows::load(kw, ck, j0 + STEP, next);
     Frag<bf16> P[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -421,7 +424,7 @@ __global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf1
         }
     }
     // this v has arrived (the next k, issued after it, may not have)
-    if (j0 + 128 < hi) wait_loads<Rows::kLoads>();
+    if (j0 + STEP < hi) wait_loads<Rows::kLoads>();
     else wait_loads<0>();
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) {
@@ -430,11 +433,11 @@ __global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf1
       for (int nt = 0; nt < NT; ++nt) mma(O[nt][dt], F, P[nt]);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (j0 + 128 < hi) Rows::load(vw, cv, j0 + 128, next);
+    if (j0 + STEP < hi) Rows::load(vw, cv, j0 + STEP, next);
     live = next;
   }
   // join the waves, 16 heads at a time (4-float pieces of a row swizzled by the head)
-  float* mg = reinterpret_cast<float*>(Ks);                        // [4][16][D]
+  float* mg = reinterpret_cast<float*>(Ks);                        // [NW][16][D]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if (16 * nt >= G) break;
@@ -449,15 +452,15 @@ __global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf1
     for (int dt = 0; dt < D / 16; ++dt)
       store4(mg + (wave * 16 + lr) * D + (((4 * dt + lg) ^ lr) << 2), O[nt][dt]);
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * D / 4; i += kDecThreads) {
+    for (int i = threadIdx.x; i < 16 * D / 4; i += 64 * NW) {
       const int h = i / (D / 4), c4 = i % (D / 4), g = 16 * nt + h;
       if (g >= G) continue;
       float M = kNegBig, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[w][h][0]);
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w][h][0]);
       f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const float f = __builtin_amdgcn_exp2f(ml[w][h][0] - M);
         L += f * ml[w][h][1];
         x += load4f(mg + (w * 16 + h) * D + ((c4 ^ h) << 2)) * f;
@@ -481,7 +484,7 @@ __global__ __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1) void cache_decode_bf1
   }
   if (BUDGET && a.n_split == 1) {
     __syncthreads();                             // scores of all waves, and st
-    add_weights(a, bk, p, at, 0, a.C, &st[0][0]);
+    add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0]);
   }
 }
 
@@ -528,7 +531,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
     for (int g = wave_uid(); g < G; g += kDecThreads / 64) (void)stats(g);
     __syncthreads();
     const int lo = (w - G) * a.split_len, hi = min(lo + a.split_len, a.C);
-    add_weights(a, bk, p, a.slot[bk], lo, hi, &st[0][0]);
+    add_weights<4>(a, bk, p, a.slot[bk], lo, hi, &st[0][0]);
   }
 }
 
@@ -537,7 +540,10 @@ static hipError_t launch_nt(const CacheArgs& a, hipStream_t st) {
   const int units = a.B * a.Hkv, G = a.Hq / a.Hkv;
   hipError_t e;
   if constexpr (sizeof(T) == 2) {
-    e = launch_kernel<0>(cache_decode_bf16_kernel<D, NT, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);
+    if (NT == 1 && a.waves == 8)
+      e = launch_kernel<0>(cache_decode_bf16_kernel<D, 1, 8, BUDGET>, dim3(units * a.n_split), 512, a, st);
+    else
+      e = launch_kernel<0>(cache_decode_bf16_kernel<D, NT, 4, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);
   } else {
     constexpr size_t lds = std::max(sizeof(T) * 4 * 32 * (D + Pad<T>::v), sizeof(float) * 4 * 16 * (D + 4));
     e = launch_kernel<lds>(cache_decode_f32_kernel<D, NT, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);
