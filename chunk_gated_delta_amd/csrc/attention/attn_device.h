@@ -198,11 +198,19 @@ __device__ __forceinline__ int seq_len(const int* lens, int b, int T) {
   return uniform(lens ? min(max(lens[b], 0), T) : T);
 }
 
-// Workgroups are dispatched round-robin over the 8 XCDs: consecutive units of work, which
-// share keys, go to one XCD and its L2.
+// Workgroups are dispatched round-robin over the 8 XCDs, each with its own L2.  Where every
+// unit of work is about as long (a window well inside the sequence), consecutive units, which share
+// keys, go to one XCD; else (units from long to short) an XCD takes every eighth group of units.
 __device__ __forceinline__ int xcd_unit(int total) {
   const int id = blockIdx.x, per = total / 8;
   return id < 8 * per ? (id % 8) * per + id / 8 : id;
+}
+__device__ __forceinline__ int xcd_unit_spread(int total, int group) {
+  const int id = blockIdx.x, even = total / (8 * group) * (8 * group);
+  return id < even ? ((id / 8) / group * 8 + id % 8) * group + (id / 8) % group : id;
+}
+__device__ __forceinline__ int attn_unit(int total, int group, int window, int T) {
+  return window <= T / 2 ? xcd_unit(total) : xcd_unit_spread(total, group);
 }
 
 // Launch with `lds` bytes of dynamic LDS (above 64 KB the limit has to be raised first).

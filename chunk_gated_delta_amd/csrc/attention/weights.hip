@@ -8,26 +8,138 @@
 
 namespace carve {
 
-constexpr int kWtK = 128, kWtQ = 32;
+constexpr int kWtK = 128;
 
-template <typename T, int D>
-__global__ __launch_bounds__(256) void weight_kernel(WeightArgs a) {
+// A unit of work: keys s0 .. + 127 of a key head and the tokens t_lo .. t_hi - 1 (a range that
+// may see them; t_lo >= t_hi: none).
+struct WeightUnit {
+  int b, bk, n, ch, s0, t_lo, t_hi;
+};
+__device__ __forceinline__ WeightUnit weight_unit(const WeightArgs& a) {
+  const int NK = (a.T + kWtK - 1) / kWtK;
+  const int unit = attn_unit(a.B * a.Hkv * NK * a.n_chunk, 1, a.window, a.T);
+  WeightUnit u;
+  u.s0 = uniform(unit % NK) * kWtK;
+  u.ch = uniform((unit / NK) % a.n_chunk);
+  u.bk = uniform(unit / (NK * a.n_chunk));
+  u.b = uniform(u.bk / a.Hkv);
+  u.n = seq_len(a.lens, u.b, a.T);
+  u.t_lo = uniform(max(u.ch * a.chunk, u.s0));
+  u.t_hi = uniform((int)min((long long)u.n, (long long)(u.ch + 1) * a.chunk));
+  // behind the window of the tile only sinks are seen
+  if (u.s0 >= a.sinks) u.t_hi = uniform((int)min((long long)u.t_hi, (long long)u.s0 + kWtK - 1 + a.window));
+  return u;
+}
+__device__ __forceinline__ void weight_store(const WeightArgs& a, const WeightUnit& u, int s, float sum) {
+  sum += __shfl_xor(sum, 32);
+  if ((lane_id() >> 5) == 0 && s < a.T) {
+    float* dst = a.n_chunk > 1 ? a.part + ((size_t)u.ch * a.B * a.Hkv + u.bk) * a.T : a.out + (size_t)u.bk * a.T;
+    dst[s] = s < u.n ? sum : 0.f;
+  }
+}
+
+// ------------------------------------------------------------------ bf16
+// Tiles of 64 tokens in two swizzled LDS buffers filled by direct loads; their lse goes through a
+// register one tile ahead.  Little state a wave (k and one sum), so four waves a SIMD hide
+// the exponentials, which bound this kernel (16 of them, a quarter rate each, beside 8 products).
+constexpr int kWtRows = 64;
+
+template <int D>
+__global__ __launch_bounds__(256, 4) void weight_bf16_kernel(WeightArgs a) {
+  using Tile = SwzTile<D, kWtRows>;
+  constexpr int KK = D / 16;
+  __shared__ __align__(16) unsigned char Q0[Tile::bytes], Q1[Tile::bytes];
+  __shared__ __align__(16) float L0[kWtRows], L1[kWtRows];
+  const WeightUnit un = weight_unit(a);
+  const int G = a.Hq / a.Hkv, n = un.n, t_lo = un.t_lo, t_hi = un.t_hi;
+  const int lane = lane_id(), wave = wave_uid(), half = lane >> 5;
+  const int sw = un.s0 + 32 * wave, s = sw + (lane & 31);
+  float sum = 0.f;
+  if (t_lo < t_hi) {
+    Frag<bf16> K[KK];
+    const size_t at = ((size_t)un.bk * a.T + min(s, n - 1)) * D + 8 * half;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) K[kk] = load_frag(reinterpret_cast<const bf16*>(a.k) + at + 16 * kk);
+    const float c = a.scale * kLog2e;
+    const int nt = (t_hi - t_lo + kWtRows - 1) / kWtRows, total = nt * G, rb = Tile::row_base();
+    const int row0 = un.b * a.Hq + (un.bk % a.Hkv) * G;
+    int lg = 0, lt = 0;                    // head and tile of the next load
+    float lse = 0.f;
+    auto load = [&](unsigned char* Qs) {
+      if (lg >= G) return;
+      const size_t row = (size_t)(row0 + lg) * a.T;
+      const int tt = t_lo + lt * kWtRows;
+      if (wave == 0) {
+        // past the end, or no visible weight: p = exp2(. - inf) = 0
+        const float x = tt + lane < t_hi ? a.lse[row + tt + lane] : -INFINITY;
+        lse = x == -INFINITY ? INFINITY : x * kLog2e;
+      }
+      Tile::template load<4>(Qs, reinterpret_cast<const bf16*>(a.q) + row * D, tt, t_hi, wave);
+      if (++lt == nt) {
+        lt = 0;
+        ++lg;
+      }
+    };
+    auto step = [&](const unsigned char* Qs, const float* Ls, int tile0) {
+#pragma unroll
+      for (int u = 0; u < kWtRows / 32; ++u) {
+        const int tt = tile0 + 32 * u;
+        if (!(sw > tt + 31 || (sw >= a.sinks && tt - (sw + 31) >= a.window))) {
+          f32x16 S = zero16();
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk) mma32(S, Tile::row_frag(Qs, rb, 32 * u, kk), K[kk]);
+          const bool full = sw + 31 <= tt && (tt + 31 - sw < a.window || sw + 32 <= a.sinks);
+          if (!full) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int t = tt + acc_row(r, half);
+              const bool see = (s <= t) & ((t - s < a.window) | (s < a.sinks));
+              S[r] = see ? S[r] : -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 32 * u + 8 * q + 4 * half);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(S[4 * q + e] * c - ls[e]);
+          }
+        }
+      }
+    };
+    load(Q0);
+    if (wave == 0) L0[lane] = lse;
+    int ct = 0;                            // tile of the next step
+    for (int i = 0; i < total; i += 2) {
+      loads_and_barrier();
+      load(Q1);
+      step(Q0, L0, t_lo + ct * kWtRows);
+      if (wave == 0) L1[lane] = lse;
+      ct = ct + 1 == nt ? 0 : ct + 1;
+      loads_and_barrier();
+      load(Q0);
+      if (i + 1 < total) step(Q1, L1, t_lo + ct * kWtRows);
+      if (wave == 0) L0[lane] = lse;
+      ct = ct + 1 == nt ? 0 : ct + 1;
+    }
+  }
+  weight_store(a, un, s, sum);
+}
+
+// ------------------------------------------------------------------ fp32
+constexpr int kWtQ = 32;
+
+template <int D>
+__global__ __launch_bounds__(256) void weight_f32_kernel(WeightArgs a) {
+  using T = float;
   using St = RowStage<T, kWtQ, D, 256>;
   constexpr int LD = St::LD;
   extern __shared__ __align__(16) unsigned char smem[];
   T* Qs = reinterpret_cast<T*>(smem);
   float* Ls = reinterpret_cast<float*>(Qs + kWtQ * LD);
-  const int G = a.Hq / a.Hkv, NK = (a.T + kWtK - 1) / kWtK;
-  const int unit = xcd_unit(a.B * a.Hkv * NK * a.n_chunk);
-  const int kt = unit % NK, ch = (unit / NK) % a.n_chunk, bk = unit / (NK * a.n_chunk);
-  const int b = bk / a.Hkv;
-  const int n = seq_len(a.lens, b, a.T);
-  const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
-  const int s0 = kt * kWtK, sw = s0 + 32 * wave, s = sw + (lane & 31);
-  const int t_lo = max(ch * a.chunk, s0) / kWtQ * kWtQ;
-  int t_hi = (int)min((long long)n, (long long)(ch + 1) * a.chunk);
-  // behind the window of the tile only sinks are seen
-  if (s0 >= a.sinks) t_hi = (int)min((long long)t_hi, (long long)s0 + kWtK - 1 + a.window);
+  const WeightUnit un = weight_unit(a);
+  const int G = a.Hq / a.Hkv, n = un.n, t_lo = un.t_lo, t_hi = un.t_hi, b = un.b, bk = un.bk;
+  const int lane = lane_id(), wave = wave_uid(), half = lane >> 5;
+  const int sw = un.s0 + 32 * wave, s = sw + (lane & 31);
   float sum = 0.f;
   if (t_lo < t_hi) {
     Frag<T> K[D / 16];
@@ -76,11 +188,7 @@ __global__ __launch_bounds__(256) void weight_kernel(WeightArgs a) {
       }
     }
   }
-  sum += __shfl_xor(sum, 32);
-  if (half == 0 && s < a.T) {
-    float* dst = a.n_chunk > 1 ? a.part + ((size_t)ch * a.B * a.Hkv + bk) * a.T : a.out + (size_t)bk * a.T;
-    dst[s] = s < n ? sum : 0.f;
-  }
+  weight_store(a, un, s, sum);
 }
 
 __global__ __launch_bounds__(256) void weight_sum_kernel(WeightArgs a) {
@@ -94,9 +202,14 @@ __global__ __launch_bounds__(256) void weight_sum_kernel(WeightArgs a) {
 
 template <typename T, int D>
 static hipError_t launch(const WeightArgs& a, hipStream_t st) {
-  constexpr size_t lds = sizeof(T) * kWtQ * RowStage<T, kWtQ, D, 256>::LD + sizeof(float) * kWtQ;
-  const int NK = (a.T + kWtK - 1) / kWtK;
-  hipError_t e = launch_kernel<lds>(weight_kernel<T, D>, dim3(a.B * a.Hkv * NK * a.n_chunk), 256, a, st);
+  const dim3 grid(a.B * a.Hkv * ((a.T + kWtK - 1) / kWtK) * a.n_chunk);
+  hipError_t e;
+  if constexpr (sizeof(T) == 2) {
+    e = launch_kernel<0>(weight_bf16_kernel<D>, grid, 256, a, st);
+  } else {
+    constexpr size_t lds = sizeof(T) * kWtQ * RowStage<T, kWtQ, D, 256>::LD + sizeof(float) * kWtQ;
+    e = launch_kernel<lds>(weight_f32_kernel<D>, grid, 256, a, st);
+  }
   if (e != hipSuccess || a.n_chunk == 1) return e;
   const size_t N = (size_t)a.B * a.Hkv * a.T;
   return launch_kernel<0>(weight_sum_kernel, dim3((unsigned)((N + 255) / 256)), 256, a, st);
