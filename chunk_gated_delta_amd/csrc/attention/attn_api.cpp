@@ -333,7 +333,7 @@ carve_status carve_budget_keep(const carve_budget_shape* s, const void* k, const
   a.cache_w = cache_w;
   a.cache_pos = cache_pos;
   const hipError_t e = carve::launch_keep_select(a, (hipStream_t)stream);
-  if (e != hipSuccess || s->T == 0) return hip_status(e);
+  if (e != hipSuccess) return hip_status(e);
   return hip_status(carve::launch_fill_rows(a, (hipStream_t)stream));
 }
 

@@ -77,11 +77,11 @@ struct FillArgs {
   int dtype;
   const void* k;              // [B,Hkv,T,D]
   const void* v;
-  const float* weights;       // [B,Hkv,T] (budget cache; null: ring cache)
+  const float* weights;       // [B,Hkv,T]
   const int* lens;
   void* cache_k;
   void* cache_v;
-  float* cache_w;
+  float* cache_w;             // null: ring cache
   int* cache_pos;
 };
 

@@ -34,36 +34,80 @@ __device__ __forceinline__ int block_scan(int x, int* red, int& total) {
   return x + before;
 }
 
-// Positions kept of one (sequence, key head): a workgroup.  Tokens 0 .. lo - 1 and hi .. n - 1
-// stay; of lo .. hi - 1 the m heaviest, the lowest positions of equal weights.  The m-th largest
-// weight is found by digits of its ordered bits (11, 11, 10) with a histogram each, then
-// the positions are written in order by a running count.
+// lanes below this one whose bit is set
+__device__ __forceinline__ int bits_below(unsigned long long b) {
+  return __builtin_amdgcn_mbcnt_hi((unsigned)(b >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)b, 0));
+}
+
+// Positions kept of one (sequence, key head): a workgroup of 16 waves.  Tokens 0 .. lo - 1 and
+// hi .. n - 1 stay; of lo .. hi - 1 the m heaviest, the lowest positions of equal weights.  The
+// m-th largest weight is found by digits of its ordered bits (11, 11, 10) with a histogram each;
+// then every wave counts what stays of its stretch of tokens, and writes it behind the waves
+// before it.  A wave's stretch is kept in registers as ordered bits, VPT a lane (VPT = 0: sequences
+// past 32 x 1024 tokens, read again in every pass).  The one compute unit's instruction rate
+// bounds it, so tokens that are not candidates carry the key 0, below every weight's, and are told
+// apart by nothing else.
+template <int VPT>
 __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
-  __shared__ int hist[2048];
-  __shared__ int red[kSelThreads / 64];
+  constexpr int NW = kSelThreads / 64;
+  // four copies of the histogram, a quarter of the lanes each: weights crowd into few bins, and
+  // lanes that add to one address take turns
+  __shared__ __align__(16) int hist[4 * 2048];
+  __shared__ int red[NW];
+  __shared__ int count[NW][2];
   __shared__ unsigned found[2];
-  const int bk = blockIdx.x, tid = threadIdx.x;
+  const int bk = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wave = wave_uid();
   const int n = seq_len(a.lens, bk / a.Hkv, a.T);
   const float* w = a.weights + (size_t)bk * a.T;
-  float* cw = a.cache_w + (size_t)bk * a.C;
   int* cp = a.cache_pos + (size_t)bk * a.C;
   const int lo = min(a.sinks, n), hi = max(lo, n - a.recent);
   const int cand = hi - lo, m = min(cand, a.C - (lo + n - hi));
-  unsigned prefix = 0, mask = 0;
-  int need = m;                            // of the weights equal to the digits so far
+  const int steps = (n + kSelThreads - 1) / kSelThreads;         // of 64 tokens a wave
+  const int j_wave = wave * steps * 64 + lane;                   // token of step i: + 64 i
+  auto key_of = [&](int j, float v) { return j >= lo && j < hi ? heavy_order(v) : 0u; };
+  unsigned x[VPT > 0 ? VPT : 1];
+  if constexpr (VPT > 0) {
+    float v[VPT];                          // loads without branches, all in flight together
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) v[i] = n > 0 ? w[min(j_wave + 64 * i, n - 1)] : 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) x[i] = i < steps ? key_of(j_wave + 64 * i, v[i]) : 0u;
+  }
+  // fn(token, key) over the wave's tokens, in order
+  auto each = [&](auto&& fn) {
+    if constexpr (VPT > 0) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) fn(j_wave + 64 * i, x[i]);
+    } else {
+      for (int i = 0; i < steps; ++i) {
+        const int j = j_wave + 64 * i;
+        fn(j, key_of(j, w[min(j, n - 1)]));
+      }
+    }
+  };
+  // the threshold: keys above it stay, and the first `need` equal to it
+  unsigned prefix = m == cand ? 0u : 0xffffffffu;
+  int need = 0;
   if (m < cand && m > 0) {
+    unsigned mask = 0;
+    prefix = 0;
+    need = m;
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-      hist[tid] = 0;
-      hist[tid + 1024] = 0;
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      i32x4* h4 = reinterpret_cast<i32x4*>(hist);
+      h4[tid] = i32x4{0, 0, 0, 0};
+      h4[tid + 1024] = i32x4{0, 0, 0, 0};
       __syncthreads();
-      for (int j = lo + tid; j < hi; j += kSelThreads) {
-        const unsigned key = heavy_order(w[j]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
-      }
+      each([&](int, unsigned key) {
+        if (key != 0u && (key & mask) == prefix) atomicAdd(&hist[((key >> shift) & (bins - 1)) * 4 + (lane & 3)], 1);
+      });
       __syncthreads();
       // bins from the top: thread t has bins - 1 - 2 t and the one below
-      const int b1 = bins - 1 - 2 * tid, h1 = b1 >= 0 ? hist[b1] : 0, h0 = b1 >= 1 ? hist[b1 - 1] : 0;
+      const int b1 = bins - 1 - 2 * tid;
+      auto of = [&](int b) { return b < 0 ? 0 : h4[b][0] + h4[b][1] + h4[b][2] + h4[b][3]; };
+      const int h1 = of(b1), h0 = of(b1 - 1);
       int total;
       const int upto = block_scan(h1 + h0, red, total), above = upto - h1 - h0;
       if (above < need && need <= upto) {
@@ -78,42 +122,42 @@ __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
       __syncthreads();
     }
   }
-  // need = how many weights equal to the threshold `prefix` stay
   int kept = 0, ties = 0;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    bool keep = false, tie = false;
-    float x = 0.f;
-    if (j < n) {
-      x = w[j];
-      if (j < lo || j >= hi || m == cand) {
-        keep = true;
-      } else if (m > 0) {
-        const unsigned key = heavy_order(x);
-        keep = key > prefix;
-        tie = key == prefix;
-      }
-    }
-    int total;
-    const int sum = block_scan((keep ? 1 : 0) | (tie ? 1 << 16 : 0), red, total);
-    const int tied = ties + (sum >> 16);                        // ties up to and with this token
-    const int at = kept + (sum & 0xffff) + min(tied, need) - 1;
-    if ((keep || (tie && tied <= need)) && at < a.C) {
-      cp[at] = j;
-      cw[at] = x;
-    }
-    kept += total & 0xffff;
-    ties += total >> 16;
+  each([&](int, unsigned key) {
+    kept += __popcll(__ballot(key > prefix));
+    ties += __popcll(__ballot(key == prefix));
+  });
+  if (lane == 0) {
+    count[wave][0] = kept;
+    count[wave][1] = ties;
   }
-  const int end = m == cand ? kept : kept + min(ties, need);
-  for (int j = end + tid; j < a.C; j += kSelThreads) {
-    cp[j] = -1;
-    cw[j] = 0.f;
+  __syncthreads();
+  int base = lo, tied = 0, end = lo, all_ties = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    base += i < wave ? count[i][0] : 0;
+    tied += i < wave ? count[i][1] : 0;
+    end += count[i][0];
+    all_ties += count[i][1];
   }
+  end += min(all_ties, need);
+  if (kept + ties > 0)
+    each([&](int j, unsigned key) {
+      const unsigned long long keeps = __ballot(key > prefix), equal = __ballot(key == prefix);
+      const int t = tied + bits_below(equal);                    // equal weights before this one
+      const int at = base + bits_below(keeps) + min(t, need);
+      if ((key > prefix || (key == prefix && t < need)) && at < a.C) cp[at] = j;
+      base += __popcll(keeps);
+      tied += __popcll(equal);
+    });
+  // the first and the recent tokens, and the empty slots
+  for (int j = tid; j < lo; j += kSelThreads) cp[j] = j;
+  for (int j = hi + tid; j < n; j += kSelThreads) cp[end + j - hi] = j;
+  for (int j = end + n - hi + tid; j < a.C; j += kSelThreads) cp[j] = -1;
 }
 
-// Copies the kept rows: 16 bytes a thread.  A slot of the ring holds the last token of its
-// residue; a slot that holds no token is left as it was.
+// Copies the kept rows, 16 bytes a thread, and their weights.  A slot of the ring holds the last
+// token of its residue; the row of a slot that holds no token is left as it was.
 template <int ROW16, bool BUDGET>
 __global__ __launch_bounds__(256) void fill_rows_kernel(FillArgs a) {
   const size_t rows = (size_t)a.B * a.Hkv * a.C, total = rows * ROW16;
@@ -124,6 +168,7 @@ __global__ __launch_bounds__(256) void fill_rows_kernel(FillArgs a) {
     int p;
     if (BUDGET) {
       p = a.cache_pos[row];
+      if (i % ROW16 == 0) a.cache_w[row] = p < 0 ? 0.f : a.weights[bk * a.T + p];
     } else {
       const int last = (a.lens ? min(max(a.lens[bk / a.Hkv], 0), a.T) : a.T) - 1;   // (lanes of several rows)
       if (j < a.sinks) {
@@ -143,14 +188,18 @@ __global__ __launch_bounds__(256) void fill_rows_kernel(FillArgs a) {
 }
 
 hipError_t launch_keep_select(const FillArgs& a, hipStream_t st) {
-  return launch_kernel<0>(keep_select_kernel, dim3(a.B * a.Hkv), kSelThreads, a, st);
+  const dim3 grid(a.B * a.Hkv);
+  if (a.T <= 4 * kSelThreads) return launch_kernel<0>(keep_select_kernel<4>, grid, kSelThreads, a, st);
+  if (a.T <= 12 * kSelThreads) return launch_kernel<0>(keep_select_kernel<12>, grid, kSelThreads, a, st);
+  if (a.T <= 32 * kSelThreads) return launch_kernel<0>(keep_select_kernel<32>, grid, kSelThreads, a, st);
+  return launch_kernel<0>(keep_select_kernel<0>, grid, kSelThreads, a, st);
 }
 
 template <int ROW16>
 static hipError_t fill_rows(const FillArgs& a, hipStream_t st) {
   const size_t total = (size_t)a.B * a.Hkv * a.C * ROW16;
   const unsigned grid = (unsigned)std::min<size_t>((total + 255) / 256, 1u << 14);
-  return a.weights ? launch_kernel<0>(fill_rows_kernel<ROW16, true>, dim3(grid), 256, a, st)
+  return a.cache_w ? launch_kernel<0>(fill_rows_kernel<ROW16, true>, dim3(grid), 256, a, st)
                    : launch_kernel<0>(fill_rows_kernel<ROW16, false>, dim3(grid), 256, a, st);
 }
 hipError_t launch_fill_rows(const FillArgs& a, hipStream_t st) {

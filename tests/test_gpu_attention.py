@@ -285,8 +285,9 @@ def keep_ref(w, n, C, sinks, recent):
 
 @pytest.mark.parametrize("kind", ["spread", "ties", "special"])
 @pytest.mark.parametrize("T,C,sinks,recent,lens", [
-    (1, 4, 1, 1, None), (10, 16, 2, 3, [10, 0]), (100, 33, 4, 8, [100, 61]), (1500, 200, 0, 1, [1500, 3]),
-    (5000, 1024, 7, 100, [5000, 1200]), (64, 12, 4, 8, [64, 64]), (3000, 2999, 1, 5, None)])
+    (0, 3, 1, 1, None), (1, 4, 1, 1, None), (10, 16, 2, 3, [10, 0]), (100, 33, 4, 8, [100, 61]), (1500, 200, 0, 1, [1500, 3]),
+    (5000, 1024, 7, 100, [5000, 1200]), (64, 12, 4, 8, [64, 64]), (3000, 2999, 1, 5, None),
+    (40000, 3001, 4, 50, [40000, 33333]), (50, 12, 4, 8, None)])
 def test_keep(T, C, sinks, recent, lens, kind):
     B, Hkv, D = 2, 2, 64
     k, v = normal((B, Hkv, T, D), "bf16", 81), normal((B, Hkv, T, D), "bf16", 82)
