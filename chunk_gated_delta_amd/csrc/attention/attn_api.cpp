@@ -62,7 +62,7 @@ void mask_of(const carve_swa_shape* s, int* window, int* sinks) {
 
 // Backward: ranges of the tokens behind the window of the first key tile, so that a tile with
 // sinks is not one workgroup's walk over the whole sequence; at most about 64 (tile, range)
-// pairs a key head, each of at least one window (or 512 tokens).
+// pairs a key head, of 256 tokens or more (short, so that they fill the gaps of the last round).
 struct SwaPlan {
   int window, sinks, n_sink_tiles, n_far, far_len;
   size_t delta_bytes, part_bytes;
@@ -75,7 +75,7 @@ SwaPlan swa_plan(const carve_swa_shape* s) {
   if (p.sinks > 0 && far > 0) {
     p.n_sink_tiles = ceil_div(p.sinks, carve::kSwaKeyTile);
     const int most = std::max(1, 64 / p.n_sink_tiles);
-    const int want = std::min(most, ceil_div(far, std::max(512, p.window + carve::kSwaKeyTile)));
+    const int want = std::min(most, ceil_div(far, 256));
     p.far_len = ceil_div(ceil_div(far, want), 32) * 32;
     p.n_far = ceil_div(far, p.far_len);
   }

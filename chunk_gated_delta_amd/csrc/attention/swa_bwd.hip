@@ -75,8 +75,10 @@ __device__ __forceinline__ void store_key_grads(const SwaArgs& a, const KeyUnit&
   if (u.part >= 0) {
     float* dst = a.part + ((((size_t)u.bk * a.n_sink_tiles + u.kt) * (1 + a.n_far) + u.part) * 2 * KT + 32 * kb +
                            (lane_id() & 31)) * D;
-    store_column<float, D>(dst, dK, a.scale);
-    store_column<float, D>(dst + (size_t)KT * D, dV, 1.f);
+    if (u.part == 0 || s < a.sinks) {      // (a far range adds to sinks only)
+      store_column<float, D>(dst, dK, a.scale);
+      store_column<float, D>(dst + (size_t)KT * D, dV, 1.f);
+    }
   } else if (s < a.T) {
     if (s >= u.n) {
 #pragma unroll
@@ -154,33 +156,32 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
     const float lse2 = log2_lse(a.lse[row + min(t, n - 1)]);
     const int rb = Tile::row_base(), cb = Tile::col_base();
 
-    // weights p and dp = dO . v of 64 keys; what is not seen has p = 0
-    auto scores = [&](const unsigned char* Ks, const unsigned char* Vs, int s0, f32x16(&S)[2], f32x16(&dP)[2]) {
+    // weights p and dp = dO . v of 32 keys; what is not seen has p = 0.  That is decided before the
+    // products, so that they and the exponentials stand in one stretch of code without branches.
+    auto scores = [&](const unsigned char* Ks, const unsigned char* Vs, int u, const bool(&see)[16], f32x16& S, f32x16& dP) {
+      S = zero16();
+      dP = zero16();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        S[u] = zero16();
-        dP[u] = zero16();
+      for (int kk = 0; kk < KK; ++kk) mma32(S, Tile::row_frag(Ks, rb, 32 * u, kk), Q[kk]);
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) mma32(S[u], Tile::row_frag(Ks, rb, 32 * u, kk), Q[kk]);
+      for (int kk = 0; kk < KK; ++kk) mma32(dP, Tile::row_frag(Vs, rb, 32 * u, kk), dO[kk]);
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) mma32(dP[u], Tile::row_frag(Vs, rb, 32 * u, kk), dO[kk]);
+      for (int r = 0; r < 16; ++r) {
+        const float p = __builtin_amdgcn_exp2f(S[r] * c - lse2);
+        S[r] = see[r] ? p : 0.f;
       }
-      const bool full = s0 + kDqK - 1 <= tw && (tw + 31 - s0 < a.window || s0 + kDqK <= a.sinks);
+    };
+    auto sight = [&](int su, bool(&see)[16]) {
+      const bool full = su + 31 <= tw && (tw + 31 - su < a.window || su + 32 <= a.sinks);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) see[r] = true;
       if (!full) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int s = s0 + 32 * u + acc_row(r, half);
-            const bool see = (s <= t) & ((t - s < a.window) | (s < a.sinks));
-            S[u][r] = see ? S[u][r] : -INFINITY;
-            dP[u][r] = see ? dP[u][r] : delta;
-          }
+        for (int r = 0; r < 16; ++r) {
+          const int s = su + acc_row(r, half);
+          see[r] = (s <= t) & ((t - s < a.window) | (s < a.sinks));
+        }
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[u][r] = __builtin_amdgcn_exp2f(S[u][r] * c - lse2);
     };
     auto seen = [&](int s0) {
       return !(s0 > tw + 31 || (s0 >= a.sinks && tw - (s0 + kDqK - 1) >= a.window));
@@ -205,12 +206,15 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
     if (a.window + a.sinks <= kExactKeys) {
       float sum = 0.f;
       sweep([&](const unsigned char* Ks, const unsigned char* Vs, int s0) {
-        f32x16 S[2], dP[2];
-        scores(Ks, Vs, s0, S, dP);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          bool see[16];
+          f32x16 S, dP;
+          sight(s0 + 32 * u, see);
+          scores(Ks, Vs, u, see, S, dP);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) sum += S[u][r] * (dP[u][r] - delta);   // a correction of the rounded one
+          for (int r = 0; r < 16; ++r) sum += S[r] * (dP[r] - delta);   // a correction of the rounded one
+        }
       });
       delta += sum + __shfl_xor(sum, 32);
       __syncthreads();                               // the second sweep loads over the last tile
@@ -220,17 +224,19 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
       a.lse2[row + t] = lse2;
     }
     sweep([&](const unsigned char* Ks, const unsigned char* Vs, int s0) {
-      f32x16 S[2], dP[2];
-      scores(Ks, Vs, s0, S, dP);
-      // ds rounded to bf16 for its product with k
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        bool see[16];
+        f32x16 S, dP;
+        sight(s0 + 32 * u, see);
+        scores(Ks, Vs, u, see, S, dP);
+        // ds rounded to bf16 for its product with k
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[u][r] *= dP[u][r] - delta;
+        for (int r = 0; r < 16; ++r) S[r] *= dP[r] - delta;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           Frag<bf16> F;
-          acc_frag(S[u], x, F);
+          acc_frag(S, x, F);
 #pragma unroll
           for (int dt = 0; dt < DT; ++dt) mma32(dQ[dt], Tile::col_frag(Ks, cb, dt, 32 * u + 16 * x), F);
         }
@@ -304,28 +310,32 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
     auto step = [&](const unsigned char* Qs, const unsigned char* Gs, const float* Ls, int tile0) {
       const int tt = tile0 + 32 * th;
       if (!(sw > tt + 31 || (sw >= a.sinks && tt - (sw + 31) >= a.window))) {
+        // what is seen, decided before the products: they and the exponentials then stand in one
+        // stretch of code without branches, where the products run beside the vector work
+        const bool full = sw + 31 <= tt && (tt + 31 - sw < a.window || sw + 32 <= a.sinks);
+        bool see[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) see[r] = true;
+        if (!full) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int t = tt + acc_row(r, half);
+            see[r] = (s <= t) & ((t - s < a.window) | (s < a.sinks));
+          }
+        }
         f32x16 S = zero16(), dP = zero16();
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) mma32(S, Tile::row_frag(Qs, rt, 0, kk), K[kk]);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) mma32(dP, Tile::row_frag(Gs, rt, 0, kk), V[kk]);
-        const bool full = sw + 31 <= tt && (tt + 31 - sw < a.window || sw + 32 <= a.sinks);
-        if (!full) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int t = tt + acc_row(r, half);
-            const bool see = (s <= t) & ((t - s < a.window) | (s < a.sinks));
-            S[r] = see ? S[r] : -INFINITY;
-            dP[r] = see ? dP[r] : 0.f;
-          }
-        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 32 * th + 8 * q + 4 * half);
           const f32x4 de = *reinterpret_cast<const f32x4*>(Ls + kDkRows + 32 * th + 8 * q + 4 * half);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            S[4 * q + e] = __builtin_amdgcn_exp2f(S[4 * q + e] * c - ls[e]);
+            const float p = __builtin_amdgcn_exp2f(S[4 * q + e] * c - ls[e]);
+            S[4 * q + e] = see[4 * q + e] ? p : 0.f;
             dP[4 * q + e] = S[4 * q + e] * (dP[4 * q + e] - de[e]);
           }
         }
@@ -563,8 +573,10 @@ __global__ __launch_bounds__(256) void swa_sink_kernel(SwaArgs a) {
     const int which = i / (KT * PR), r = (i / PR) % KT, s = kt * KT + r;
     if (s >= a.T) continue;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    const int last = s < a.sinks ? a.n_far : 0;
     if (s < n)
-      for (int f = 0; f <= a.n_far; ++f) x += load4f(src + (size_t)f * 2 * KT * D + (size_t)i * 4);
+#pragma unroll 4
+      for (int f = 0; f <= last; ++f) x += load4f(src + (size_t)f * 2 * KT * D + (size_t)i * 4);
     T* dst = reinterpret_cast<T*>(which ? a.dv : a.dk);
     store4(dst + ((size_t)bk * a.T + s) * D + 4 * (i % PR), x);
   }
