@@ -137,7 +137,8 @@ __device__ __forceinline__ void loads_and_barrier() {
 
 template <int D, int ROWS>
 struct SwzTile {
-  static constexpr int RB = 2 * D, BLOCK = 64 * ROWS, bytes = ROWS * RB;
+  static constexpr int RB = 2 * D, BLOCK = 128 * ROWS, bytes = ROWS * RB;
+  static __device__ __forceinline__ int swz(int r) { return (((r >> 1) & 1) << 2) | ((r >> 2) & 3); }
   // rows r0 .. r0 + ROWS - 1 of base [n][D] by NW waves
   template <int NW>
   static __device__ __forceinline__ void load(unsigned char* tile, const bf16* base, int r0, int n, int wave) {
@@ -146,35 +147,36 @@ struct SwzTile {
     const int lane = lane_id(), rows = uniform(max(0, min(n - r0, ROWS)));
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16*>(base) + (size_t)r0 * D, 0, rows * RB, 0x00020000);
-    const int rl = lane >> 2, voff = rl * RB + (((lane & 3) ^ ((rl >> 2) & 3)) << 4);
-    const int blk = wave * PER / IPB, row0 = wave * PER % IPB * 16;
+    const int rl = lane >> 3, blk = wave * PER / IPB, row0 = wave * PER % IPB * 8;
+    const int voff = rl * RB + (((lane & 7) ^ swz(rl)) << 4), odd = row0 & 8;
 #pragma unroll
-    for (int u = 0; u < PER; ++u)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(tile + blk * BLOCK + (row0 + 16 * u) * 64), 16, voff,
-                                               blk * 64 + (row0 + 16 * u) * RB, 0, 0);
+    for (int u = 0; u < PER; ++u)            // (swz of rows 8 .. 15: ^ 2)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(tile + blk * BLOCK + (row0 + 8 * u) * 128), 16,
+                                               voff ^ (((u & 1) ^ (odd ? 1 : 0)) << 5), blk * 128 + (row0 + 8 * u) * RB, 0, 0);
   }
-  // byte offset of the lane's row operand (odd contraction blocks: ^ 32)
+  // byte offset of the lane's row operand (contraction block kk: ^ (kk % 4) * 32)
   static __device__ __forceinline__ int row_base() {
     const int lane = lane_id(), r = lane & 31;
-    return r * 64 + (((lane >> 5) ^ ((r >> 2) & 3)) << 4);
+    return r * 128 + (((lane >> 5) ^ swz(r)) << 4);
   }
   // rows r0 .. r0 + 31, 16-deep block kk
   static __device__ __forceinline__ Frag<bf16> row_frag(const unsigned char* tile, int base, int r0, int kk) {
     Frag<bf16> f;
-    f.v = *(lds_bf16x8*)(tile + (kk >> 1) * BLOCK + r0 * 64 + (base ^ ((kk & 1) << 5)));
+    f.v = *(lds_bf16x8*)(tile + (kk >> 2) * BLOCK + r0 * 128 + (base ^ ((kk & 3) << 5)));
     return f;
   }
-  // byte offset of the lane's transpose read (rows + 8: ^ 32, + 512)
+  // byte offset of the lane's transpose read (columns 32 dt: ^ (dt % 2) * 64; rows + 8: ^ 32, + 1024)
   static __device__ __forceinline__ int col_base() {
     const int lane = lane_id(), s = lane & 15, g = lane >> 4, r = 4 * (g >> 1) + (s >> 2);
-    return r * 64 + (((2 * (g & 1) + ((s & 3) >> 1)) ^ ((r >> 2) & 3)) << 4) + 8 * (s & 1);
+    return r * 128 + (((2 * (g & 1) + ((s & 3) >> 1)) ^ swz(r)) << 4) + 8 * (s & 1);
   }
   // columns 32 dt .. + 31 as rows of an A operand, contraction over rows k0 + 8 (j / 4) + 4 (l / 32) + j % 4
   // (k0 a multiple of 16)
   static __device__ __forceinline__ Frag<bf16> col_frag(const unsigned char* tile, int base, int dt, int k0) {
-    const unsigned char* p = tile + dt * BLOCK + k0 * 64;
-    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + base));
-    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 512 + (base ^ 32)));
+    const unsigned char* p = tile + (dt >> 1) * BLOCK + k0 * 128;
+    const int b = base ^ ((dt & 1) << 6);
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + b));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 1024 + (b ^ 32)));
     Frag<bf16> f;
     f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     return f;

@@ -287,7 +287,7 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
     }
     const float c = a.scale * kLog2e;
     const int nt = (t_hi - t_lo + kDkRows - 1) / kDkRows, total = nt * G;
-    const int rt = Tile::row_base() + 2048 * th, ct0 = Tile::col_base() + 2048 * th;   // (32 rows of a block)
+    const int rt = Tile::row_base() + 4096 * th, ct0 = Tile::col_base() + 4096 * th;   // (32 rows of a block)
     const int row0 = (un.b * a.Hq + (un.bk % a.Hkv) * G);
     int lg = 0, lt = 0;                    // head and tile of the next load
     auto load = [&](unsigned char* Qs, unsigned char* Gs, float* Ls) {
