@@ -183,6 +183,14 @@ struct SwzTile {
   }
 };
 
+// x of the lane 32 away
+__device__ __forceinline__ float other_half(float x) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (lane_id() & 32) ? r[0] : r[1]);
+}
+
 // Key tiles that a tile of tokens t0 .. t1 - 1 sees, in the order sinks, then window.
 template <int KT>
 struct KeyTiles {

@@ -46,11 +46,11 @@ __device__ __forceinline__ void fwd_store(const SwaArgs& a, const FwdUnit& u, in
 // buffers: the next tile's loads go straight to LDS while this one is worked on, one barrier a tile.
 // The accumulators are rescaled only when a token's maximum grows by more than 2^8 (weights
 // up to 2^8 keep their relative precision in bf16 and fp32).
-constexpr int kFwdK = 64;
+constexpr int kFwdK = 64, kFwdKeys = 32;
 
 template <int D, int NQ>
-__global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
-  using Tile = SwzTile<D, kFwdK>;
+__global__ __launch_bounds__(256, 3) void swa_fwd_bf16_kernel(SwaArgs a) {
+  using Tile = SwzTile<D, kFwdKeys>;
   constexpr int QW = 32 * NQ, QT = 4 * QW, KK = D / 16, DT = D / 32;
   __shared__ __align__(16) unsigned char K0[Tile::bytes], K1[Tile::bytes];
   __shared__ __align__(16) unsigned char V0[Tile::bytes], V1[Tile::bytes];
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
     l[q] = 0.f;
   }
   if (t0 < n) {
-    const KeyTiles<kFwdK> kt(t0, min(t0 + QT, n), a.window, a.sinks);
+    const KeyTiles<kFwdKeys> kt(t0, min(t0 + QT, n), a.window, a.sinks);
     Tile::template load<4>(K0, kb, kt[0], n, wave);
     Tile::template load<4>(V0, vb, kt[0], n, wave);
     Frag<bf16> Q[NQ][KK];
@@ -87,9 +87,9 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
     // one tile of 64 keys from s0 against the wave's 32 tokens from ts
     auto block = [&](const unsigned char* Ks, const unsigned char* Vs, int s0, int ts, bool masked, const Frag<bf16>(&Qf)[KK],
                      f32x16(&Of)[DT], float& mf, float& lf) {
-      f32x16 S[2];
+      f32x16 S[kFwdKeys / 32];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kFwdKeys / 32; ++u) {
         S[u] = zero16();
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) mma32(S[u], Tile::row_frag(Ks, rb, 32 * u, kk), Qf[kk]);
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
       if (masked) {
         const int t = ts + (lane & 31);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kFwdKeys / 32; ++u)
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int s = s0 + 32 * u + acc_row(r, half);
@@ -107,10 +107,10 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
       }
       float mx = S[0][0];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < kFwdKeys / 32; ++u)
 #pragma unroll
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, S[u][r]);
-      mx = fmaxf(mx, __shfl_xor(mx, 32)) * c;
+      mx = fmaxf(mx, other_half(mx)) * c;
       if (__any(mx > mf + 8.f)) {
         const float mn = fmaxf(mf, mx), alpha = __builtin_amdgcn_exp2f(mf - mn);
         mf = mn;
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
         for (int dt = 0; dt < DT; ++dt) Of[dt] *= alpha;
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < kFwdKeys / 32; ++u)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           S[u][r] = __builtin_amdgcn_exp2f(S[u][r] * c - mf);
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
         }
       // the weights are rounded to bf16 for the product with v (their sum is not)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < kFwdKeys / 32; ++u)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           Frag<bf16> P;
@@ -141,8 +141,8 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
       for (int q = 0; q < NQ; ++q) {
         const int ts = tw + 32 * q;
         // nothing of the tile is seen / all of it is seen by all of the 32 tokens
-        if (s0 > ts + 31 || (s0 >= a.sinks && ts - (s0 + kFwdK - 1) >= a.window)) continue;
-        const bool full = s0 + kFwdK - 1 <= ts && (ts + 31 - s0 < a.window || s0 + kFwdK <= a.sinks);
+        if (s0 > ts + 31 || (s0 >= a.sinks && ts - (s0 + kFwdKeys - 1) >= a.window)) continue;
+        const bool full = s0 + kFwdKeys - 1 <= ts && (ts + 31 - s0 < a.window || s0 + kFwdKeys <= a.sinks);
         block(Ks, Vs, s0, ts, !full, Q[q], O[q], m[q], l[q]);
       }
     };
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(256, 2) void swa_fwd_bf16_kernel(SwaArgs a) {
   }
 #pragma unroll
   for (int q = 0; q < NQ; ++q)
-    fwd_store<bf16, D>(a, un, tw + 32 * q + (lane & 31), O[q], m[q], l[q] + __shfl_xor(l[q], 32));
+    fwd_store<bf16, D>(a, un, tw + 32 * q + (lane & 31), O[q], m[q], l[q] + other_half(l[q]));
 }
 
 // ------------------------------------------------------------------ fp32
