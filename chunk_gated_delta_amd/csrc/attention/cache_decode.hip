@@ -54,15 +54,29 @@ __device__ __forceinline__ int ring_slot(const CacheArgs& a, int p) {
 template <int NW>
 __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st) {
   const int G = a.Hq / a.Hkv;
-  for (int j = lo + threadIdx.x; j < hi; j += 64 * NW) {
-    const size_t i = (size_t)bk * a.C + j;
-    const bool mine = j == at;
-    if (!mine && a.cache_pos[i] < 0) continue;
-    const float* s = a.score + i * G;
-    float x = 0.f;
-    for (int g = 0; g < G; ++g) x += __builtin_amdgcn_exp2f(s[g] - st[2 * g]) * st[2 * g + 1];
-    a.cache_w[i] = mine ? x : a.cache_w[i] + x;
-    if (mine) a.cache_pos[i] = p;
+  const size_t row = (size_t)bk * a.C;
+  constexpr int STEP = 64 * NW, U = 4;           // slots a thread takes at a time, their loads in flight together
+  for (int j0 = lo + threadIdx.x; j0 < hi; j0 += U * STEP) {
+    float x[U], w[U];
+    int held[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = min(j0 + u * STEP, hi - 1);
+      held[u] = a.cache_pos[row + j];
+      w[u] = a.cache_w[row + j];
+      x[u] = 0.f;
+    }
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[u] += __builtin_amdgcn_exp2f(a.score[(row + min(j0 + u * STEP, hi - 1)) * G + g] - st[2 * g]) * st[2 * g + 1];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * STEP;
+      if (j < hi && (j == at || held[u] >= 0)) a.cache_w[row + j] = j == at ? x[u] : w[u] + x[u];
+      if (j < hi && j == at) a.cache_pos[row + j] = p;
+    }
   }
 }
 
@@ -321,13 +335,30 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
     }
     return;
   }
-  const int at = uniform(BUDGET ? pick_slot<NW>(a, bk, p, red) : ring_slot(a, p));
-  if (BUDGET && split == 0 && threadIdx.x == 0) a.slot[bk] = at;
   const int count = BUDGET ? a.C : min(p, a.C - 1) + 1;          // a ring holds its tokens from slot 0 up
   const int lo = split * a.split_len, hi = min(min(lo + a.split_len, a.C), count);
   bf16* ck = reinterpret_cast<bf16*>(a.cache_k) + (size_t)bk * a.C * D;
   bf16* cv = reinterpret_cast<bf16*>(a.cache_v) + (size_t)bk * a.C * D;
   const int* held = BUDGET ? a.cache_pos + (size_t)bk * a.C : nullptr;
+  unsigned char* kw = Ks + wave * Rows::bytes;
+  unsigned char* vw = Vs + wave * Rows::bytes;
+  const int first = lo + 32 * wave;
+  // live slots of the 32 from j0, one bit each (`at`: the new token's, live whatever it held)
+  auto live_of = [&](int j0, int at) -> unsigned {
+    const int j = j0 + (lane & 31);
+    bool on = j < hi;
+    if (BUDGET) on = on && (j == at || held[min(j, a.C - 1)] >= 0);
+    return (unsigned)__ballot(on);
+  };
+  unsigned live = 0;
+  auto fetch_first = [&](int at) {
+    live = live_of(first, at);
+    Rows::load(kw, ck, first, live);
+    Rows::load(vw, cv, first, live);
+  };
+  if (BUDGET && first < hi) fetch_first(-1);     // on their way while the slot is looked for
+  const int at = uniform(BUDGET ? pick_slot<NW>(a, bk, p, red) : ring_slot(a, p));
+  if (BUDGET && split == 0 && threadIdx.x == 0) a.slot[bk] = at;
   // the new rows go to the cache first, by the workgroup that owns their slot and alone reads it
   if (at >= lo && at < hi) {
     if (threadIdx.x < D / 4) {
@@ -338,6 +369,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
     }
     __syncthreads();
   }
+  if (first < hi && (!BUDGET || (at >= first && at < first + 32))) fetch_first(at);
   Frag<bf16> Q[NT][D / 32];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -356,23 +388,8 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) O[nt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  unsigned char* kw = Ks + wave * Rows::bytes;
-  unsigned char* vw = Vs + wave * Rows::bytes;
-  auto live_of = [&](int j0) -> unsigned {       // live slots of the 32, one bit each
-    const int j = j0 + (lane & 31);
-    bool on = j < hi;
-    if (BUDGET) on = on && (j == at || held[min(j, a.C - 1)] >= 0);
-    return (unsigned)__ballot(on);
-  };
-  const int first = lo + 32 * wave;
-  unsigned live = 0;
-  if (first < hi) {
-    live = live_of(first);
-    Rows::load(kw, ck, first, live);
-    Rows::load(vw, cv, first, live);
-  }
   for (int j0 = first; j0 < hi; j0 += STEP) {
-    const unsigned next = j0 + STEP < hi ? live_of(j0 + STEP) : 0;
+    const unsigned next = j0 + STEP < hi ? live_of(j0 + STEP, at) : 0;
     wait_loads<Rows::kLoads>();                  // this k has arrived (its v, issued after it, may not have)
     f32x4 X[NT][2];
 #pragma unroll
