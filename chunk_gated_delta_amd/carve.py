@@ -688,7 +688,15 @@ def _heads(q, k, ndim):
     return B, Hq, k.shape[1], T, D, q.device, q.dtype
 
 
+def _whole(**numbers):
+    """Whole numbers that a C int holds (ctypes would cut them short without a word)."""
+    for name, x in numbers.items():
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{name} = {x} is past 32 bits")
+
+
 def _swa_shape(q, k, ndim, window, sinks, scale):
+    _whole(window=window, sinks=sinks)
     B, Hq, Hkv, T, D, dev, dt = _heads(q, k, ndim)
     s = carve_swa_shape(B, Hq, Hkv, T, D, window, sinks, D ** -0.5 if scale is None else scale, _dtype_code(q))
     return B, Hq, Hkv, T, D, dev, dt, s, ctypes.byref(s)
@@ -814,6 +822,7 @@ def budget_keep(k, v, weights, C, sinks=0, recent=1, lens=None, cache=None):
     """The cache of C slots of a prompt (starting at position 0): the first `sinks` tokens, the last
     `recent`, and the heaviest of the others, in order of position; (cache_k, cache_v, cache_w,
     cache_pos) as budget_cache makes it, or `cache` itself, overwritten (rows of empty slots stay)."""
+    _whole(C=C, sinks=sinks, recent=recent)
     B, _, Hkv, T, D, dev, dt = _heads(k, k, 4)
     s = carve_budget_shape(B, Hkv, Hkv, T, D, C, sinks, recent, 1.0, _dtype_code(k))
     if cache is None:
@@ -832,6 +841,7 @@ def budget_decode(q, k, v, cache, pos, sinks=0, recent=1, scale=None, o=None, sl
     The token takes an empty slot, or that of the least weight among tokens neither in the first
     `sinks` nor the last `recent` positions (the new one counted); every live slot's weight grows
     by its attention weight of this token."""
+    _whole(sinks=sinks, recent=recent)
     B, Hq, Hkv, _, D, dev, dt = _heads(q, k, 3)
     C = cache[0].shape[2]
     s = carve_budget_shape(B, Hq, Hkv, 1, D, C, sinks, recent, D ** -0.5 if scale is None else scale, _dtype_code(q))

@@ -178,7 +178,7 @@ carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* 
       !all_aligned({lens, lse}, 4))
     return CARVE_ERR_INVALID_ARG;
   const SwaPlan p = swa_plan(s);
-  if ((long long)s->B * s->Hq * (ceil_div(s->T, 128) + (long long)p.n_sink_tiles * p.n_far) > kMaxUnits)
+  if ((long long)s->B * s->Hq * (ceil_div(s->T, carve::kSwaKeyTile) + (long long)p.n_sink_tiles * p.n_far) > kMaxUnits)
     return CARVE_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < 2 * p.delta_bytes + p.part_bytes + 256) return CARVE_ERR_WORKSPACE;
   carve::SwaArgs a = swa_args(s, q, k, v, lens);

@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
         x += load4f(mg + (w * 16 + h) * LDM + d) * f;
       }
       if (a.n_split == 1) {
-        const float f = L > 0.f ? 1.f / L : 0.f;
+        const float f = L != 0.f ? 1.f / L : 0.f;
         store4(ob + (size_t)g * D + d, x * f);
         if (d == 0) {
           st[g][0] = M;
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
         x += load4f(mg + (w * 16 + h) * D + ((c4 ^ h) << 2)) * f;
       }
       if (a.n_split == 1) {
-        const float f = L > 0.f ? 1.f / L : 0.f;
+        const float f = L != 0.f ? 1.f / L : 0.f;
         store4(ob + (size_t)g * D + 4 * c4, x * f);
         if (c4 == 0) {
           st[g][0] = M;
@@ -529,7 +529,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
     for (int o = 1; o < 64; o <<= 1) L += __shfl_xor(L, o);
     if (lane == 0) {
       st[g][0] = M;
-      st[g][1] = L > 0.f ? 1.f / L : 0.f;
+      st[g][1] = L != 0.f ? 1.f / L : 0.f;
     }
     return x;
   };

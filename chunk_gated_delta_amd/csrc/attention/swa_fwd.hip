@@ -32,7 +32,7 @@ template <typename T, int D>
 __device__ __forceinline__ void fwd_store(const SwaArgs& a, const FwdUnit& u, int t, f32x16 (&O)[D / 32], float m, float l) {
   if (t >= a.T) return;
   const size_t row = (size_t)(u.b * a.Hq + u.hq) * a.T + t;
-  const bool live = t < u.n && l > 0.f;
+  const bool live = t < u.n && l != 0.f;        // (a sum that is not a number stays one)
   if (!live) {
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt) O[dt] = zero16();

@@ -123,3 +123,7 @@ def test_binding_refuses(lib):
         carve.swa_fwd(q.transpose(1, 2), k, v, window=4)
     with pytest.raises(ValueError, match="dimensions"):
         carve.swa_decode(q, k, v, None, None, None, window=4)
+    with pytest.raises(ValueError, match="32 bits"):
+        carve.swa_fwd(q, k, v, window=(1 << 32) + 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        carve.budget_keep(k, v, torch.zeros(2, 2, 8), 1 << 33)

@@ -166,9 +166,77 @@ def test_autograd_in_a_hybrid_block():
     assert vl.grad.shape == vl.shape and torch.isfinite(vl.grad.float()).all() and vl.grad.any()
 
 
+def test_not_a_number_stays_with_its_token():
+    """A query that is not a number gives a row that is not, and only that row."""
+    for dt in DT:
+        q, k, v, _ = inputs(1, 2, 1, 200, 64, dt, seed=33)
+        want, lse = carve.swa_fwd(q, k, v, window=50, sinks=2)
+        q[0, 1, 77, 5] = math.nan
+        o, lse2 = carve.swa_fwd(q, k, v, window=50, sinks=2)
+        assert torch.isnan(o[0, 1, 77].float()).all() and torch.isnan(lse2[0, 1, 77])
+        rest = torch.ones(1, 2, 200, dtype=torch.bool, device="cuda")
+        rest[0, 1, 77] = False
+        assert torch.equal(o[rest], want[rest]) and torch.equal(lse2[rest], lse[rest])
+        ck, cv = carve.swa_cache(1, 1, 64, 50, 2, dtype=DT[dt])
+        o = carve.swa_decode(q[:, :, 77].contiguous(), k[:, :, 0].contiguous(), v[:, :, 0].contiguous(), ck, cv, ints([3]), 50, 2)
+        assert torch.isnan(o[0, 1].float()).all() and torch.isfinite(o[0, 0].float()).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_training_step_in_a_graph(dt):
+    """Forward and backward captured and replayed with other inputs, against eager calls."""
+    q, k, v, dO = inputs(2, 4, 2, 400, 128, dt, seed=35)
+    at = dict(window=60, sinks=3, lens=ints([400, 222]))
+
+    def step():
+        o, lse = carve.swa_fwd(q, k, v, **at)
+        g = carve.swa_bwd(q, k, v, o, lse, dO, **at)
+        return [o, lse, g["dq"], g["dk"], g["dv"]]
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for i in range(4):
+        for j, x in enumerate((q, k, v, dO)):
+            x.copy_(normal(x.shape, dt, 500 + 4 * i + j))
+        g.replay()
+        want = step()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y), i
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_two_streams_at_once(dt):
+    """Two training steps on two streams at the same time give what they give one after the other."""
+    sets = [inputs(2, 8, 2, 900, 64, dt, seed=37 + 10 * i) for i in range(2)]
+    at = dict(window=90, sinks=5)
+
+    def step(q, k, v, dO):
+        o, lse = carve.swa_fwd(q, k, v, **at)
+        g = carve.swa_bwd(q, k, v, o, lse, dO, **at)
+        return [o, g["dq"], g["dk"], g["dv"]]
+
+    want = [step(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = []
+        for st, x in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(step(*x))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+
+
 # ------------------------------------------------------------------ ring cache
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("Hq,Hkv,D,window,sinks,lens", [
+    (2, 1, 64, 1500, 4, [1600, 900, 1503]), (24, 2, 128, 700, 0, [700, 699, 2000]),
     (4, 2, 64, 24, 3, [50, 0, 10]), (16, 1, 128, 7, 0, [5, 30, 1]), (6, 2, 64, 130, 64, [70, 300, 64]),
     (40, 1, 64, 50, 1, [20, 3, 90]), (3, 3, 128, 1, 0, [1, 2, 9]), (128, 2, 128, 200, 4, [0, 410, 199])])
 def test_ring_cache_follows_the_sequence(Hq, Hkv, D, window, sinks, lens, dt):
