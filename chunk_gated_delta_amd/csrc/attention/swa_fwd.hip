@@ -42,133 +42,108 @@ __device__ __forceinline__ void fwd_store(const SwaArgs& a, const FwdUnit& u, in
 }
 
 // ------------------------------------------------------------------ bf16
-// Workgroup = 4 waves x 32 NQ tokens of one query head, key tiles of 64 rows in two pairs of LDS
-// buffers: the next tile's loads go straight to LDS while this one is worked on, one barrier a tile.
-// The accumulators are rescaled only when a token's maximum grows by more than 2^8 (weights
+// Workgroup = 4 waves x 32 tokens of one query head, key tiles of 32 rows in two pairs of LDS
+// buffers: the next tile's loads go straight to LDS while this one is worked on, one barrier a
+// tile.  The accumulators are rescaled only when a token's maximum grows by more than 2^8 (weights
 // up to 2^8 keep their relative precision in bf16 and fp32).
-constexpr int kFwdK = 64, kFwdKeys = 32;
+// Bound by the products and the vector work beside them (per 32 x 32 scores at D = 128: 16 products of
+// 32 cycles; 16 exponentials of 16 and some 100 other vector instructions of 4).  32 tokens a wave
+// and 32 keys a tile keep it at 162 registers, three waves a SIMD: tiles of 64 keys (two waves)
+// took 580 us where this takes 531, 64 tokens a wave spilled (1,261 us), and the next tile's
+// scores formed among this one's exponentials in one wave gained nothing over a second wave.
+// B1, 16 heads on 4, T = 32,768, window 2,048, 4 sinks, D = 128: 531 us, 1.00 PFLOP/s of visible
+// pairs (a library product of 8,192^3 reaches 1.20 on the same card).
+constexpr int kFwdQ = 128, kFwdKeys = 32;
 
-template <int D, int NQ>
+template <int D>
 __global__ __launch_bounds__(256, 3) void swa_fwd_bf16_kernel(SwaArgs a) {
   using Tile = SwzTile<D, kFwdKeys>;
-  constexpr int QW = 32 * NQ, QT = 4 * QW, KK = D / 16, DT = D / 32;
+  constexpr int KK = D / 16, DT = D / 32;
   __shared__ __align__(16) unsigned char K0[Tile::bytes], K1[Tile::bytes];
   __shared__ __align__(16) unsigned char V0[Tile::bytes], V1[Tile::bytes];
-  const FwdUnit un = fwd_unit(a, QT);
+  const FwdUnit un = fwd_unit(a, kFwdQ);
   const int n = un.n, t0 = un.t0, lane = lane_id(), wave = wave_uid(), half = lane >> 5;
-  const int tw = t0 + QW * wave;
+  const int tw = t0 + 32 * wave, t = tw + (lane & 31);
   const bf16* kb = reinterpret_cast<const bf16*>(a.k) + (size_t)un.bk * a.T * D;
   const bf16* vb = reinterpret_cast<const bf16*>(a.v) + (size_t)un.bk * a.T * D;
 
-  f32x16 O[NQ][DT];
-  float m[NQ], l[NQ];
+  f32x16 O[DT];
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) O[q][dt] = zero16();
-    m[q] = kNegBig;
-    l[q] = 0.f;
-  }
+  for (int dt = 0; dt < DT; ++dt) O[dt] = zero16();
+  float m = kNegBig, l = 0.f;
   if (t0 < n) {
-    const KeyTiles<kFwdKeys> kt(t0, min(t0 + QT, n), a.window, a.sinks);
-    Tile::template load<4>(K0, kb, kt[0], n, wave);
-    Tile::template load<4>(V0, vb, kt[0], n, wave);
-    Frag<bf16> Q[NQ][KK];
+    const KeyTiles<kFwdKeys> kt(t0, min(t0 + kFwdQ, n), a.window, a.sinks);
+    auto load = [&](unsigned char* Ks, unsigned char* Vs, int i) {
+      if (i < kt.count) {
+        Tile::template load<4>(Ks, kb, kt[i], n, wave);
+        Tile::template load<4>(Vs, vb, kt[i], n, wave);
+      }
+    };
+    load(K0, V0, 0);
+    Frag<bf16> Q[KK];
+    const bf16* qr = reinterpret_cast<const bf16*>(a.q) +
+                     ((size_t)(un.b * a.Hq + un.hq) * a.T + min(t, n - 1)) * D + 8 * half;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const bf16* qr = reinterpret_cast<const bf16*>(a.q) +
-                       ((size_t)(un.b * a.Hq + un.hq) * a.T + min(tw + 32 * q + (lane & 31), n - 1)) * D + 8 * half;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) Q[q][kk] = load_frag(qr + 16 * kk);
-    }
+    for (int kk = 0; kk < KK; ++kk) Q[kk] = load_frag(qr + 16 * kk);
     const float c = a.scale * kLog2e;
     const int rb = Tile::row_base(), cb = Tile::col_base();
 
-    // one tile of 64 keys from s0 against the wave's 32 tokens from ts
-    auto block = [&](const unsigned char* Ks, const unsigned char* Vs, int s0, int ts, bool masked, const Frag<bf16>(&Qf)[KK],
-                     f32x16(&Of)[DT], float& mf, float& lf) {
-      f32x16 S[kFwdKeys / 32];
+    auto step = [&](const unsigned char* Ks, const unsigned char* Vs, int s0) {
+      // nothing of the tile is seen by any of the wave's tokens
+      if (s0 > tw + 31 || (s0 >= a.sinks && tw - (s0 + kFwdKeys - 1) >= a.window)) return;
+      f32x16 S = zero16();
 #pragma unroll
-      for (int u = 0; u < kFwdKeys / 32; ++u) {
-        S[u] = zero16();
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) mma32(S[u], Tile::row_frag(Ks, rb, 32 * u, kk), Qf[kk]);
-      }
-      if (masked) {
-        const int t = ts + (lane & 31);
-#pragma unroll
-        for (int u = 0; u < kFwdKeys / 32; ++u)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int s = s0 + 32 * u + acc_row(r, half);
-            const bool see = (s <= t) & ((t - s < a.window) | (s < a.sinks));
-            S[u][r] = see ? S[u][r] : -INFINITY;
-          }
-      }
-      float mx = S[0][0];
-#pragma unroll
-      for (int u = 0; u < kFwdKeys / 32; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, S[u][r]);
-      mx = fmaxf(mx, other_half(mx)) * c;
-      if (__any(mx > mf + 8.f)) {
-        const float mn = fmaxf(mf, mx), alpha = __builtin_amdgcn_exp2f(mf - mn);
-        mf = mn;
-        lf *= alpha;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) Of[dt] *= alpha;
-      }
-#pragma unroll
-      for (int u = 0; u < kFwdKeys / 32; ++u)
+      for (int kk = 0; kk < KK; ++kk) mma32(S, Tile::row_frag(Ks, rb, 0, kk), Q[kk]);
+      const bool full = s0 + kFwdKeys - 1 <= tw && (tw + 31 - s0 < a.window || s0 + kFwdKeys <= a.sinks);
+      if (!full) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          S[u][r] = __builtin_amdgcn_exp2f(S[u][r] * c - mf);
-          lf += S[u][r];
+          const int s = s0 + acc_row(r, half);
+          const bool see = (s <= t) & ((t - s < a.window) | (s < a.sinks));
+          S[r] = see ? S[r] : -INFINITY;
         }
+      }
+      float mx = S[0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) mx = fmaxf(mx, S[r]);
+      mx = fmaxf(mx, other_half(mx)) * c;
+      if (__any(mx > m + 8.f)) {
+        const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= alpha;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) O[dt] *= alpha;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        S[r] = __builtin_amdgcn_exp2f(S[r] * c - m);
+        l += S[r];
+      }
       // the weights are rounded to bf16 for the product with v (their sum is not)
 #pragma unroll
-      for (int u = 0; u < kFwdKeys / 32; ++u)
+      for (int x = 0; x < 2; ++x) {
+        Frag<bf16> P;
+        acc_frag(S, x, P);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          Frag<bf16> P;
-          acc_frag(S[u], x, P);
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt) mma32(Of[dt], Tile::col_frag(Vs, cb, dt, 32 * u + 16 * x), P);
-        }
-    };
-    auto step = [&](const unsigned char* Ks, const unsigned char* Vs, int s0) {
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int ts = tw + 32 * q;
-        // nothing of the tile is seen / all of it is seen by all of the 32 tokens
-        if (s0 > ts + 31 || (s0 >= a.sinks && ts - (s0 + kFwdKeys - 1) >= a.window)) continue;
-        const bool full = s0 + kFwdKeys - 1 <= ts && (ts + 31 - s0 < a.window || s0 + kFwdKeys <= a.sinks);
-        block(Ks, Vs, s0, ts, !full, Q[q], O[q], m[q], l[q]);
+        for (int dt = 0; dt < DT; ++dt) mma32(O[dt], Tile::col_frag(Vs, cb, dt, 16 * x), P);
       }
     };
     for (int i = 0; i < kt.count; i += 2) {
       loads_and_barrier();
-      if (i + 1 < kt.count) {
-        Tile::template load<4>(K1, kb, kt[i + 1], n, wave);
-        Tile::template load<4>(V1, vb, kt[i + 1], n, wave);
-      }
+      load(K1, V1, i + 1);
       step(K0, V0, kt[i]);
       loads_and_barrier();
-      if (i + 2 < kt.count) {
-        Tile::template load<4>(K0, kb, kt[i + 2], n, wave);
-        Tile::template load<4>(V0, vb, kt[i + 2], n, wave);
-      }
+      load(K0, V0, i + 2);
       if (i + 1 < kt.count) step(K1, V1, kt[i + 1]);
     }
   }
-#pragma unroll
-  for (int q = 0; q < NQ; ++q)
-    fwd_store<bf16, D>(a, un, tw + 32 * q + (lane & 31), O[q], m[q], l[q] + other_half(l[q]));
+  fwd_store<bf16, D>(a, un, t, O, m, l + other_half(l));
 }
 
 // ------------------------------------------------------------------ fp32
-// As above with one tile in LDS (padded rows, staged through registers) and a product per 32 keys.
-constexpr int kFwdQ = 128;
+// As above with one tile of 64 keys in LDS (padded rows, staged through registers).  Bound by the fp32
+// products, a sixteenth of the bf16 rate.
+constexpr int kFwdK = 64;
 
 template <int D>
 __global__ __launch_bounds__(256) void swa_fwd_f32_kernel(SwaArgs a) {
@@ -252,9 +227,9 @@ __global__ __launch_bounds__(256) void swa_fwd_f32_kernel(SwaArgs a) {
   fwd_store<T, D>(a, un, t, O, m, l);
 }
 
-template <int D, int NQ>
+template <int D>
 static hipError_t launch_bf16(const SwaArgs& a, hipStream_t st) {
-  return launch_kernel<0>(swa_fwd_bf16_kernel<D, NQ>, dim3(a.B * a.Hq * ((a.T + 128 * NQ - 1) / (128 * NQ))), 256, a, st);
+  return launch_kernel<0>(swa_fwd_bf16_kernel<D>, dim3(a.B * a.Hq * ((a.T + kFwdQ - 1) / kFwdQ)), 256, a, st);
 }
 template <int D>
 static hipError_t launch_f32(const SwaArgs& a, hipStream_t st) {
@@ -263,7 +238,7 @@ static hipError_t launch_f32(const SwaArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_swa_fwd(const SwaArgs& a, hipStream_t st) {
-  if (a.dtype) return a.D == 128 ? launch_bf16<128, 1>(a, st) : launch_bf16<64, 1>(a, st);
+  if (a.dtype) return a.D == 128 ? launch_bf16<128>(a, st) : launch_bf16<64>(a, st);
   return a.D == 128 ? launch_f32<128>(a, st) : launch_f32<64>(a, st);
 }
 
