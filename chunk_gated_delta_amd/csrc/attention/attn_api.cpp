@@ -144,6 +144,12 @@ carve_status check_budget(const carve_budget_shape* s) {
   return CARVE_OK;
 }
 
+// whether a budget cache's scores of this step stay in LDS
+bool near_scores(const carve_budget_shape* s, int n_split, int waves) {
+  const long long G = s->Hq / s->Hkv;
+  return s->dtype == CARVE_BF16 && n_split == 1 && waves == 8 && G <= 16 && G * s->C <= carve::kNearScores;
+}
+
 }  // namespace
 
 extern "C" {
@@ -341,7 +347,9 @@ size_t carve_budget_decode_workspace_size(const carve_budget_shape* s) {
   if (check_budget(s) != CARVE_OK || s->T != 1 || s->B == 0 || s->Hq == 0 || s->Hq / s->Hkv > kMaxGroup) return 0;
   int n, len, waves;
   split_plan(s->B * s->Hkv, s->C, row_bytes(s->D, s->dtype), &n, &len, &waves);
-  return part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n) + (size_t)s->B * s->Hq * s->C * sizeof(float) + 256;
+  const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n) +
+                       (near_scores(s, n, waves) ? 0 : (size_t)s->B * s->Hq * s->C * sizeof(float));
+  return bytes ? bytes + 256 : 0;
 }
 
 carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, const void* k, const void* v,
@@ -378,10 +386,12 @@ carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, con
   a.slot = slot;
   split_plan(a.B * a.Hkv, a.C, row_bytes(s->D, s->dtype), &a.n_split, &a.split_len, &a.waves);
   const size_t need = carve_budget_decode_workspace_size(s);
-  if (!workspace || workspace_bytes < need) return CARVE_ERR_WORKSPACE;
+  if (need && (!workspace || workspace_bytes < need)) return CARVE_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(up256(reinterpret_cast<uintptr_t>(workspace)));
   a.part = reinterpret_cast<float*>(ws);
-  a.score = reinterpret_cast<float*>(ws + part_bytes(a.B * a.Hkv, a.Hq / a.Hkv, a.D, a.n_split));
+  a.score = near_scores(s, a.n_split, a.waves)
+                ? nullptr
+                : reinterpret_cast<float*>(ws + part_bytes(a.B * a.Hkv, a.Hq / a.Hkv, a.D, a.n_split));
   return hip_status(carve::launch_cache_decode(a, (hipStream_t)stream));
 }
 

@@ -50,9 +50,10 @@ __device__ __forceinline__ int ring_slot(const CacheArgs& a, int p) {
 }
 
 // Adds the token's weights to the cache's: slots lo .. hi - 1, with max and sum of every head
-// (log2 domain) in st[head] = {m, 1 / l}.
+// (log2 domain) in st[head] = {m, 1 / l}, scores [C][G] of the key head in `score`.
 template <int NW>
-__device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st) {
+__device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st,
+                                            const float* score) {
   const int G = a.Hq / a.Hkv;
   const size_t row = (size_t)bk * a.C;
   constexpr int STEP = 64 * NW, U = 4;           // slots a thread takes at a time, their loads in flight together
@@ -69,7 +70,7 @@ __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, i
     for (int g = 0; g < G; ++g) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        x[u] += __builtin_amdgcn_exp2f(a.score[(row + min(j0 + u * STEP, hi - 1)) * G + g] - st[2 * g]) * st[2 * g + 1];
+        x[u] += __builtin_amdgcn_exp2f(score[(size_t)min(j0 + u * STEP, hi - 1) * G + g] - st[2 * g]) * st[2 * g + 1];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -265,7 +266,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
   }
   if (BUDGET && a.n_split == 1) {
     __syncthreads();                             // scores of all waves, and st
-    add_weights<4>(a, bk, p, at, 0, a.C, &st[0][0]);
+    add_weights<4>(a, bk, p, at, 0, a.C, &st[0][0], a.score + (size_t)bk * a.C * G);
   }
 }
 
@@ -323,6 +324,9 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
   __shared__ unsigned long long red[NW];
   __shared__ float ml[NW][16][2];
   __shared__ float st[16 * NT][2];
+  // a small cache's scores stay in LDS (the workgroup is its compute unit's only one anyway)
+  constexpr bool SMALL = BUDGET && NW == 8;
+  __shared__ float near_score[SMALL ? kNearScores : 1];
   const int G = a.Hq / a.Hkv;
   const int split = uniform(blockIdx.x % a.n_split), bk = uniform(blockIdx.x / a.n_split), b = uniform(bk / a.Hkv);
   const int lane = lane_id(), wave = wave_uid(), lr = lane & 15, lg = lane >> 4;
@@ -379,6 +383,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
       Q[nt][kk] = load_frag(reinterpret_cast<const bf16*>(a.q) + ((size_t)bk * G + g) * D + 32 * kk + 8 * lg);
   }
   const float c = a.scale * kLog2e;
+  const bool near = SMALL && a.score == nullptr;
   f32x4 O[NT][D / 16];
   float m[NT], l[NT];
 #pragma unroll
@@ -417,8 +422,10 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
           const int r = 16 * u + 4 * lg + i;
           const float x = ((live >> r) & 1) ? X[nt][u][i] * c : -INFINITY;
           X[nt][u][i] = x;
-          if (BUDGET && 16 * nt + lr < G && j0 + r < hi)
-            a.score[((size_t)bk * a.C + j0 + r) * G + 16 * nt + lr] = x;
+          if (BUDGET && 16 * nt + lr < G && j0 + r < hi) {
+            if (SMALL && near) near_score[(j0 + r) * G + 16 * nt + lr] = x;
+            else a.score[((size_t)bk * a.C + j0 + r) * G + 16 * nt + lr] = x;
+          }
           mx = fmaxf(mx, x);
         }
       mx = fmaxf(mx, __shfl_xor(mx, 16));
@@ -501,7 +508,8 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
   }
   if (BUDGET && a.n_split == 1) {
     __syncthreads();                             // scores of all waves, and st
-    add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0]);
+    if (SMALL && near) add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], near_score);
+    else add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], a.score + (size_t)bk * a.C * G);
   }
 }
 
@@ -548,7 +556,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
     for (int g = wave_uid(); g < G; g += kDecThreads / 64) (void)stats(g);
     __syncthreads();
     const int lo = (w - G) * a.split_len, hi = min(lo + a.split_len, a.C);
-    add_weights<4>(a, bk, p, a.slot[bk], lo, hi, &st[0][0]);
+    add_weights<4>(a, bk, p, a.slot[bk], lo, hi, &st[0][0], a.score + (size_t)bk * a.C * G);
   }
 }
 

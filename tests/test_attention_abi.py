@@ -105,6 +105,8 @@ def test_sizes(lib):
     assert size("carve_swa_bwd", swa(D=96)) == 0
     # scores of every slot and query head
     assert size("carve_budget_decode", budget(B=256, Hq=16, Hkv=4, C=100, recent=8)) >= 256 * 16 * 100 * 4
+    # a small cache of few sequences needs none
+    assert size("carve_budget_decode", budget(B=1, Hq=16, Hkv=4, C=1024, recent=8)) == 0
     # sinks behind the window cost partial sums only where tokens are behind the window
     near = size("carve_swa_bwd", swa(T=100, window=100, sinks=4))
     assert near == size("carve_swa_bwd", swa(T=100, window=100, sinks=0))
