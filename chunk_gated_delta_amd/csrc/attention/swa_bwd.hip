@@ -7,6 +7,9 @@
 // with its sums in registers in a fixed order, and no atomics: one over the keys of a tile
 // of tokens (dq, and delta for the other pass), one over the tokens of a tile of keys.
 // That is seven products of a visible pair where one pass with shared sums has five.
+// Bound by the products and the vector work beside them, and in the second pass by waits that its
+// 256 registers a wave leave uncovered (matrix cores busy 0.48, vector units 0.37 and 0.30).
+// B4, 16 heads on 4, T = 4,096, window 1,024, 4 sinks, D = 128: dq 217 us, dk/dv 280 us, sinks 5 us.
 #include <algorithm>
 
 #include "attn_device.h"
@@ -256,7 +259,7 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
 // ------------------------------------------------------------------ bf16: dk, dv
 // Workgroup = 64 keys: waves 0, 1 take 32 keys each with the first 32 tokens of every tile, waves 2,
 // 3 the same keys with the last 32 (their sums are added at the end), so that a unit of work is
-// half as long as with 32 keys a wave.  Tiles of 64 tokens (q, dO, lse, delta) in two sets of LDS buffers.  Rows at and past t_hi read as
+// half as long as with 128 keys (695 -> 374 us at the size above: two rounds of units, not a short third).  Tiles of 64 tokens (q, dO, lse, delta) in two sets of LDS buffers.  Rows at and past t_hi read as
 // zero throughout: p = 1 there, but dO = 0 and ds = 1 (0 - 0), so they add nothing.
 constexpr int kDkRows = 64;
 

@@ -1,7 +1,7 @@
 """Drive the CARVE kernels for an external profiler (rocprofv3).
 
     python -m chunk_gated_delta_amd.profile_step [--steps 5] [--warmup 2]
-                                                  [--pass fwd+bwd|fwd|long|content|content_bwd|decode]
+                                                  [--pass fwd+bwd|fwd|long|content|content_bwd|decode|attention]
                                                   [--copy-mib 0]
                                                   [--decode-batch 256]
 
@@ -10,7 +10,9 @@ synthetic seeded inputs) through the same entry points as bench.py: the training
 (fwd_save + bwd_saved), the plain forward, the content-aware forward or its backward (given the forward's
 per-period records), the
 long-context forward (B1 H16 T32768, --pass long), or recurrent decode
-steps (one token per sequence and head at batch --decode-batch).  With
+steps (one token per sequence and head at batch --decode-batch), or the attention layers beside them (--pass
+attention: the windowed training step at the same batch, heads and length, its prompt's weights, the cache
+kept by them, and one token on the ring cache and on that cache at batch --decode-batch).  With
 --copy-mib N it also runs a plain elementwise kernel that reads N MiB and writes N MiB
 (torch.neg), the reference against which HBM byte counters are scaled.  Prints one
 progress line per phase.
@@ -25,7 +27,7 @@ def main(argv=None):
     p.add_argument("--steps", type=int, default=5)
     p.add_argument("--warmup", type=int, default=2)
     p.add_argument("--pass", dest="passes", default="fwd+bwd",
-                   choices=["fwd+bwd", "fwd", "long", "content", "content_bwd", "decode"])
+                   choices=["fwd+bwd", "fwd", "long", "content", "content_bwd", "decode", "attention"])
     p.add_argument("--decode-batch", type=int, default=256)
     p.add_argument("--copy-mib", type=int, default=0)
     args = p.parse_args(argv)
@@ -40,6 +42,8 @@ def main(argv=None):
                    else "long_ctx_fwd" if args.passes == "long" else "head1p3b_fwd"]
     if args.passes == "decode":
         return decode(args, wl, dev)
+    if args.passes == "attention":
+        return attention(args, wl, dev)
     inp = make_inputs(wl, with_dO=args.passes in ("fwd+bwd", "content_bwd"))
 
     def bf16(name):
@@ -92,6 +96,38 @@ def main(argv=None):
         torch.cuda.synchronize()
         print(f"[profile_step] reference kernel: torch.neg over {args.copy_mib} MiB in, "
               f"{args.copy_mib} MiB out, 3 calls", flush=True)
+    return 0
+
+
+def attention(args, wl, dev):
+    """The attention operators at the workload's batch, heads (four query heads a key head), length and
+    width: window T / 4, four sinks, caches of T / 2 slots."""
+    import torch
+    from chunk_gated_delta_amd import carve
+    B, Hq, T, D, Bd = wl.B, wl.H, wl.T, wl.Dk, args.decode_batch
+    Hkv, window, sinks, C = Hq // 4, T // 4, 4, T // 2
+    gen = torch.Generator(device=dev).manual_seed(1007)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device=dev).bfloat16()
+
+    q, dO, k, v = normal(B, Hq, T, D), normal(B, Hq, T, D), normal(B, Hkv, T, D), normal(B, Hkv, T, D)
+    q1, k1, v1 = normal(Bd, Hq, D), normal(Bd, Hkv, D), normal(Bd, Hkv, D)
+    ring = normal(Bd, Hkv, window + sinks, D), normal(Bd, Hkv, window + sinks, D)
+    pos = torch.full((Bd,), T, dtype=torch.int32, device=dev)
+    cache = (normal(Bd, Hkv, C, D), normal(Bd, Hkv, C, D), torch.rand(Bd, Hkv, C, generator=gen, device=dev),
+             torch.arange(C, dtype=torch.int32, device=dev).repeat(Bd, Hkv, 1))
+    print(f"[profile_step] attention inputs ready: B{B} Hq{Hq} Hkv{Hkv} T{T} d{D} window {window}, "
+          f"decode batch {Bd}, {C} slots", flush=True)
+    for _ in range(args.warmup + args.steps):
+        o, lse = carve.swa_fwd(q, k, v, window, sinks=sinks)
+        carve.swa_bwd(q, k, v, o, lse, dO, window, sinks=sinks)
+        _, lse = carve.swa_fwd(q, k, v, T)
+        carve.budget_keep(k, v, carve.budget_weights(q, k, lse), C, sinks=sinks, recent=C // 4)
+        carve.swa_decode(q1, k1, v1, *ring, pos, window, sinks=sinks)
+        carve.budget_decode(q1, k1, v1, cache, pos, sinks=sinks, recent=C // 4)
+    torch.cuda.synchronize()
+    print(f"[profile_step] attention: {args.warmup} warm-up + {args.steps} steps", flush=True)
     return 0
 
 
