@@ -147,7 +147,7 @@ carve_status check_budget(const carve_budget_shape* s) {
 // whether a budget cache's scores of this step stay in LDS
 bool near_scores(const carve_budget_shape* s, int n_split, int waves) {
   const long long G = s->Hq / s->Hkv;
-  return s->dtype == CARVE_BF16 && n_split == 1 && waves == 8 && G <= 16 && G * s->C <= carve::kNearScores;
+  return s->dtype == CARVE_BF16 && n_split == 1 && waves == 8 && G <= 16 && G * carve::score_row(s->C) <= carve::kNearScores;
 }
 
 }  // namespace
@@ -348,7 +348,7 @@ size_t carve_budget_decode_workspace_size(const carve_budget_shape* s) {
   int n, len, waves;
   split_plan(s->B * s->Hkv, s->C, row_bytes(s->D, s->dtype), &n, &len, &waves);
   const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n) +
-                       (near_scores(s, n, waves) ? 0 : (size_t)s->B * s->Hq * s->C * sizeof(float));
+                       (near_scores(s, n, waves) ? 0 : (size_t)s->B * s->Hq * carve::score_row(s->C) * sizeof(float));
   return bytes ? bytes + 256 : 0;
 }
 

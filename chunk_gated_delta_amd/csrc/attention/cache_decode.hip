@@ -50,7 +50,7 @@ __device__ __forceinline__ int ring_slot(const CacheArgs& a, int p) {
 }
 
 // Adds the token's weights to the cache's: slots lo .. hi - 1, with max and sum of every head
-// (log2 domain) in st[head] = {m, 1 / l}, scores [C][G] of the key head in `score`.
+// (log2 domain) in st[head] = {m, 1 / l}, scores [G][score_row(C)] of the key head in `score`.
 template <int NW>
 __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st,
                                             const float* score) {
@@ -70,7 +70,7 @@ __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, i
     for (int g = 0; g < G; ++g) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        x[u] += __builtin_amdgcn_exp2f(score[(size_t)min(j0 + u * STEP, hi - 1) * G + g] - st[2 * g]) * st[2 * g + 1];
+        x[u] += __builtin_amdgcn_exp2f(score[(size_t)g * score_row(a.C) + min(j0 + u * STEP, hi - 1)] - st[2 * g]) * st[2 * g + 1];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
           const int r = 16 * u + 4 * lg + i;
           S[u][i] = ((live >> r) & 1) ? S[u][i] * c : -INFINITY;
           if (BUDGET && 16 * nt + lr < G && j0 + r < hi)
-            a.score[((size_t)bk * a.C + j0 + r) * G + 16 * nt + lr] = S[u][i];
+            a.score[((size_t)bk * G + 16 * nt + lr) * score_row(a.C) + j0 + r] = S[u][i];
           mx = fmaxf(mx, S[u][i]);
         }
       }
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
   }
   if (BUDGET && a.n_split == 1) {
     __syncthreads();                             // scores of all waves, and st
-    add_weights<4>(a, bk, p, at, 0, a.C, &st[0][0], a.score + (size_t)bk * a.C * G);
+    add_weights<4>(a, bk, p, at, 0, a.C, &st[0][0], a.score + (size_t)bk * G * score_row(a.C));
   }
 }
 
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
   __shared__ float st[16 * NT][2];
   // a small cache's scores stay in LDS (the workgroup is its compute unit's only one anyway)
   constexpr bool SMALL = BUDGET && NW == 8;
-  __shared__ float near_score[SMALL ? kNearScores : 1];
+  __shared__ __align__(16) float near_score[SMALL ? kNearScores : 4];
   const int G = a.Hq / a.Hkv;
   const int split = uniform(blockIdx.x % a.n_split), bk = uniform(blockIdx.x / a.n_split), b = uniform(bk / a.Hkv);
   const int lane = lane_id(), wave = wave_uid(), lr = lane & 15, lg = lane >> 4;
@@ -396,8 +396,14 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) O[nt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
+  // the positions of the slots after next, asked for a step early: waiting for them at their use
+  // would also wait for the rows that were asked for before them
+  auto position = [&](int j0) { return BUDGET ? held[min(j0 + (lane & 31), a.C - 1)] : 0; };
+  int ahead = position(first + STEP);
   for (int j0 = first; j0 < hi; j0 += STEP) {
-    const unsigned next = j0 + STEP < hi ? live_of(j0 + STEP, at) : 0;
+    const int jn = j0 + STEP + (lane & 31);
+    const unsigned next = (unsigned)__ballot(jn < hi && (!BUDGET || jn == at || ahead >= 0));
+    ahead = position(j0 + 2 * STEP);
     wait_loads<Rows::kLoads>();                  // this k has arrived (its v, issued after it, may not have)
     f32x4 X[NT][2];
 #pragma unroll
@@ -413,7 +419,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (j0 + STEP < hi) Rows::load(kw, ck, j0 + STEP, next);
+    Rows::load(kw, ck, j0 + STEP, next);         // (behind the last slots: no rows)
     Frag<bf16> P[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -425,12 +431,18 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
           const int r = 16 * u + 4 * lg + i;
           const float x = ((live >> r) & 1) ? X[nt][u][i] * c : -INFINITY;
           X[nt][u][i] = x;
-          if (BUDGET && 16 * nt + lr < G && j0 + r < hi) {
-            if (SMALL && near) near_score[(j0 + r) * G + 16 * nt + lr] = x;
-            else a.score[((size_t)bk * a.C + j0 + r) * G + 16 * nt + lr] = x;
-          }
           mx = fmaxf(mx, x);
         }
+      // four slots of a head at a time (past the last slot into the row's padding)
+      if (BUDGET && 16 * nt + lr < G) {
+        const size_t row = (size_t)(16 * nt + lr) * score_row(a.C) + j0 + 4 * lg;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (j0 + 16 * u + 4 * lg < hi) {
+            if (SMALL && near) store4(near_score + row + 16 * u, X[nt][u]);
+            else store4(a.score + (size_t)bk * G * score_row(a.C) + row + 16 * u, X[nt][u]);
+          }
+      }
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       if (__any(mx > m[nt] + 8.f)) {             // rescale only when a maximum grows by 2^8
@@ -450,9 +462,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
           P[nt].v[4 * u + i] = (bf16)x;
         }
     }
-    // this v has arrived (the next k, issued after it, may not have)
-    if (j0 + STEP < hi) wait_loads<Rows::kLoads>();
-    else wait_loads<0>();
+    wait_loads<Rows::kLoads>();                  // this v has arrived (the next k, issued after it, may not have)
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) {
       const Frag<bf16> F = Rows::col_frag(vw, dt);
@@ -460,9 +470,10 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
       for (int nt = 0; nt < NT; ++nt) mma(O[nt][dt], F, P[nt]);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (j0 + STEP < hi) Rows::load(vw, cv, j0 + STEP, next);
+    Rows::load(vw, cv, j0 + STEP, next);
     live = next;
   }
+  wait_loads<0>();                               // nothing writes LDS any more
   // join the waves, 16 heads at a time (4-float pieces of a row swizzled by the head)
   float* mg = reinterpret_cast<float*>(Ks);                        // [NW][16][D]
 #pragma unroll
@@ -512,7 +523,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
   if (BUDGET && a.n_split == 1) {
     __syncthreads();                             // scores of all waves, and st
     if (SMALL && near) add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], near_score);
-    else add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], a.score + (size_t)bk * a.C * G);
+    else add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], a.score + (size_t)bk * G * score_row(a.C));
   }
 }
 
@@ -559,7 +570,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
     for (int g = wave_uid(); g < G; g += kDecThreads / 64) (void)stats(g);
     __syncthreads();
     const int lo = (w - G) * a.split_len, hi = min(lo + a.split_len, a.C);
-    add_weights<4>(a, bk, p, a.slot[bk], lo, hi, &st[0][0], a.score + (size_t)bk * a.C * G);
+    add_weights<4>(a, bk, p, a.slot[bk], lo, hi, &st[0][0], a.score + (size_t)bk * G * score_row(a.C));
   }
 }
 
