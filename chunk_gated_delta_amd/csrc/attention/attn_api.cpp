@@ -104,12 +104,22 @@ carve::SwaArgs swa_args(const carve_swa_shape* s, const void* q, const void* k, 
 }
 
 // Token ranges of the weight pass: enough workgroups to fill the chip several times over (the
-// later keys are seen by few tokens, so the ranges are uneven), of at least 256 tokens.
-void weight_plan(const carve_swa_shape* s, int* n_chunk, int* chunk) {
+// later keys are seen by few tokens, so the ranges are uneven), of at least 128 tokens.  In fp32,
+// whose products take sixteen times as long, ranges from 64 tokens and, while compute units
+// are idle, the heads of a group apart (4 rows of 11 tokens, 32 heads on 4: 28 -> 13 us, where
+// the sum's launch costs 3; in bf16 it would cost more than it gives).
+struct WeightPlan {
+  int n_chunk, chunk, n_head;
+};
+WeightPlan weight_plan(const carve_swa_shape* s) {
+  const bool f32 = s->dtype == CARVE_F32;
   const long long units = (long long)s->B * s->Hkv * ceil_div(s->T, 128);
-  const int want = (int)std::max(1ll, std::min<long long>(4096 / std::max(1ll, units), ceil_div(s->T, 256)));
-  *chunk = ceil_div(ceil_div(s->T, want), 32) * 32;
-  *n_chunk = ceil_div(s->T, *chunk);
+  const int want = (int)std::max(1ll, std::min<long long>(4096 / std::max(1ll, units), ceil_div(s->T, f32 ? 64 : 128)));
+  WeightPlan p;
+  p.chunk = ceil_div(ceil_div(s->T, want), 32) * 32;
+  p.n_chunk = ceil_div(s->T, p.chunk);
+  p.n_head = f32 ? (int)std::max(1ll, std::min<long long>(s->Hq / s->Hkv, 256 / (units * p.n_chunk))) : 1;
+  return p;
 }
 
 int row_bytes(int D, carve_dtype dtype) { return D * (dtype == CARVE_BF16 ? 2 : 4); }
@@ -275,8 +285,8 @@ carve_status carve_swa_decode(const carve_swa_shape* s, const void* q, const voi
 
 size_t carve_budget_weights_workspace_size(const carve_swa_shape* s) {
   if (check_swa(s) != CARVE_OK || empty(s)) return 0;
-  int n, chunk;
-  weight_plan(s, &n, &chunk);
+  const WeightPlan p = weight_plan(s);
+  const int n = p.n_chunk * p.n_head;
   return n > 1 ? (size_t)n * s->B * s->Hkv * s->T * sizeof(float) + 256 : 0;
 }
 
@@ -303,8 +313,11 @@ carve_status carve_budget_weights(const carve_swa_shape* s, const void* q, const
   a.lse = lse;
   a.lens = lens;
   a.out = weights;
-  weight_plan(s, &a.n_chunk, &a.chunk);
-  if ((long long)a.B * a.Hkv * ceil_div(a.T, 128) * a.n_chunk > kMaxUnits) return CARVE_ERR_UNSUPPORTED;
+  const WeightPlan p = weight_plan(s);
+  a.n_chunk = p.n_chunk;
+  a.chunk = p.chunk;
+  a.n_head = p.n_head;
+  if ((long long)a.B * a.Hkv * ceil_div(a.T, 128) * a.n_chunk * a.n_head > kMaxUnits) return CARVE_ERR_UNSUPPORTED;
   const size_t need = carve_budget_weights_workspace_size(s);
   if (need && (!workspace || workspace_bytes < need)) return CARVE_ERR_WORKSPACE;
   a.part = reinterpret_cast<float*>(up256(reinterpret_cast<uintptr_t>(workspace)));

@@ -44,8 +44,9 @@ struct WeightArgs {
   const float* lse;           // [B,Hq,T]
   const int* lens;
   float* out;                 // [B,Hkv,T]
-  float* part;                // [n_chunk][B*Hkv][T] (n_chunk > 1)
+  float* part;                // [n_chunk * n_head][B*Hkv][T] (more than one)
   int n_chunk, chunk;         // query tokens of a workgroup
+  int n_head;                 // parts of a group's heads
 };
 
 // One new token per sequence against a cache of C slots.

@@ -10,22 +10,26 @@ namespace carve {
 
 constexpr int kWtK = 128;
 
-// A unit of work: keys s0 .. + 127 of a key head and the tokens t_lo .. t_hi - 1 (a range that
-// may see them; t_lo >= t_hi: none).
+// A unit of work: keys s0 .. + 127 of a key head, the tokens t_lo .. t_hi - 1 (a range that may see
+// them; t_lo >= t_hi: none) and the heads h_lo .. h_hi - 1 of the group.
 struct WeightUnit {
-  int b, bk, n, ch, s0, t_lo, t_hi;
+  int b, bk, n, part, s0, t_lo, t_hi, h_lo, h_hi;
 };
 __device__ __forceinline__ WeightUnit weight_unit(const WeightArgs& a) {
   const int NK = (a.T + kWtK - 1) / kWtK;
-  const int unit = attn_unit(a.B * a.Hkv * NK * a.n_chunk, 1, a.window, a.T);
+  const int parts = a.n_chunk * a.n_head;
+  const int unit = attn_unit(a.B * a.Hkv * NK * parts, 1, a.window, a.T);
   WeightUnit u;
   u.s0 = uniform(unit % NK) * kWtK;
-  u.ch = uniform((unit / NK) % a.n_chunk);
-  u.bk = uniform(unit / (NK * a.n_chunk));
+  u.part = uniform((unit / NK) % parts);
+  u.bk = uniform(unit / (NK * parts));
+  const int ch = u.part / a.n_head, G = a.Hq / a.Hkv, per = (G + a.n_head - 1) / a.n_head;
+  u.h_lo = uniform(u.part % a.n_head * per);
+  u.h_hi = min(G, u.h_lo + per);
   u.b = uniform(u.bk / a.Hkv);
   u.n = seq_len(a.lens, u.b, a.T);
-  u.t_lo = uniform(max(u.ch * a.chunk, u.s0));
-  u.t_hi = uniform((int)min((long long)u.n, (long long)(u.ch + 1) * a.chunk));
+  u.t_lo = uniform(max(ch * a.chunk, u.s0));
+  u.t_hi = uniform((int)min((long long)u.n, (long long)(ch + 1) * a.chunk));
   // behind the window of the tile only sinks are seen
   if (u.s0 >= a.sinks) u.t_hi = uniform((int)min((long long)u.t_hi, (long long)u.s0 + kWtK - 1 + a.window));
   return u;
@@ -33,7 +37,7 @@ __device__ __forceinline__ WeightUnit weight_unit(const WeightArgs& a) {
 __device__ __forceinline__ void weight_store(const WeightArgs& a, const WeightUnit& u, int s, float sum) {
   sum += __shfl_xor(sum, 32);
   if ((lane_id() >> 5) == 0 && s < a.T) {
-    float* dst = a.n_chunk > 1 ? a.part + ((size_t)u.ch * a.B * a.Hkv + u.bk) * a.T : a.out + (size_t)u.bk * a.T;
+    float* dst = a.n_chunk * a.n_head > 1 ? a.part + ((size_t)u.part * a.B * a.Hkv + u.bk) * a.T : a.out + (size_t)u.bk * a.T;
     dst[s] = s < u.n ? sum : 0.f;
   }
 }
@@ -57,18 +61,18 @@ __global__ __launch_bounds__(256, 4) void weight_bf16_kernel(WeightArgs a) {
   const int lane = lane_id(), wave = wave_uid(), half = lane >> 5;
   const int sw = un.s0 + 32 * wave, s = sw + (lane & 31);
   float sum = 0.f;
-  if (t_lo < t_hi) {
+  if (t_lo < t_hi && un.h_lo < un.h_hi) {
     Frag<bf16> K[KK];
     const size_t at = ((size_t)un.bk * a.T + min(s, n - 1)) * D + 8 * half;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) K[kk] = load_frag(reinterpret_cast<const bf16*>(a.k) + at + 16 * kk);
     const float c = a.scale * kLog2e;
-    const int nt = (t_hi - t_lo + kWtRows - 1) / kWtRows, total = nt * G, rb = Tile::row_base();
+    const int nt = (t_hi - t_lo + kWtRows - 1) / kWtRows, total = nt * (un.h_hi - un.h_lo), rb = Tile::row_base();
     const int row0 = un.b * a.Hq + (un.bk % a.Hkv) * G;
-    int lg = 0, lt = 0;                    // head and tile of the next load
+    int lg = un.h_lo, lt = 0;              // head and tile of the next load
     float lse = 0.f;
     auto load = [&](unsigned char* Qs) {
-      if (lg >= G) return;
+      if (lg >= un.h_hi) return;
       const size_t row = (size_t)(row0 + lg) * a.T;
       const int tt = t_lo + lt * kWtRows;
       if (wave == 0) {
@@ -143,17 +147,17 @@ __global__ __launch_bounds__(256) void weight_f32_kernel(WeightArgs a) {
   const int lane = lane_id(), wave = wave_uid(), half = lane >> 5;
   const int sw = un.s0 + 32 * wave, s = sw + (lane & 31);
   float sum = 0.f;
-  if (t_lo < t_hi) {
+  if (t_lo < t_hi && un.h_lo < un.h_hi) {
     Frag<T> K[D / 16];
     const size_t at = ((size_t)bk * a.T + min(s, n - 1)) * D + 8 * half;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) K[kk] = load_frag(reinterpret_cast<const T*>(a.k) + at + 16 * kk);
     const float c = a.scale * kLog2e;
-    const int nt = (t_hi - t_lo + kWtQ - 1) / kWtQ, total = nt * G;
+    const int nt = (t_hi - t_lo + kWtQ - 1) / kWtQ, total = nt * (un.h_hi - un.h_lo);
     St qst;
     float lst = 0.f;
     auto load = [&](int i) {
-      const int hq = (bk % a.Hkv) * G + i / nt, tt = t_lo + (i % nt) * kWtQ;
+      const int hq = (bk % a.Hkv) * G + un.h_lo + i / nt, tt = t_lo + (i % nt) * kWtQ;
       const size_t row = (size_t)(b * a.Hq + hq) * a.T;
       qst.load(reinterpret_cast<const T*>(a.q) + row * D, tt, t_hi);
       if (threadIdx.x < kWtQ) {
@@ -198,13 +202,13 @@ __global__ __launch_bounds__(256) void weight_sum_kernel(WeightArgs a) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= N) return;
   float x = 0.f;
-  for (int c = 0; c < a.n_chunk; ++c) x += a.part[c * N + i];
+  for (int c = 0; c < a.n_chunk * a.n_head; ++c) x += a.part[c * N + i];
   a.out[i] = x;
 }
 
 template <typename T, int D>
 static hipError_t launch(const WeightArgs& a, hipStream_t st) {
-  const dim3 grid(a.B * a.Hkv * ((a.T + kWtK - 1) / kWtK) * a.n_chunk);
+  const dim3 grid(a.B * a.Hkv * ((a.T + kWtK - 1) / kWtK) * a.n_chunk * a.n_head);
   hipError_t e;
   if constexpr (sizeof(T) == 2) {
     e = launch_kernel<0>(weight_bf16_kernel<D>, grid, 256, a, st);
@@ -212,7 +216,7 @@ static hipError_t launch(const WeightArgs& a, hipStream_t st) {
     constexpr size_t lds = sizeof(T) * kWtQ * RowStage<T, kWtQ, D, 256>::LD + sizeof(float) * kWtQ;
     e = launch_kernel<lds>(weight_f32_kernel<D>, grid, 256, a, st);
   }
-  if (e != hipSuccess || a.n_chunk == 1) return e;
+  if (e != hipSuccess || a.n_chunk * a.n_head == 1) return e;
   const size_t N = (size_t)a.B * a.Hkv * a.T;
   return launch_kernel<0>(weight_sum_kernel, dim3((unsigned)((N + 255) / 256)), 256, a, st);
 }

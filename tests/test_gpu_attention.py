@@ -329,7 +329,7 @@ def test_decode_in_a_graph_follows_the_positions():
 # ------------------------------------------------------------------ cache kept by weight
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("B,Hq,Hkv,T,D,window,sinks,lens", [
-    (1, 1, 1, 1, 64, None, 0, None), (2, 6, 2, 77, 128, None, 0, [77, 0]), (1, 4, 4, 129, 64, 30, 3, None),
+    (1, 1, 1, 1, 64, None, 0, None), (2, 6, 2, 77, 128, None, 0, [77, 0]), (1, 14, 2, 11, 128, None, 0, None), (1, 4, 4, 129, 64, 30, 3, None),
     (2, 4, 1, 1030, 64, None, 0, [1030, 515]), (1, 2, 1, 900, 128, 100, 140, None)])
 def test_weights(B, Hq, Hkv, T, D, window, sinks, lens, dt):
     q, k, v, _ = inputs(B, Hq, Hkv, T, D, dt, seed=71)
