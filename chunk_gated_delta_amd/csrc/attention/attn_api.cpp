@@ -62,10 +62,12 @@ void mask_of(const carve_swa_shape* s, int* window, int* sinks) {
 
 // Backward: ranges of the tokens behind the window of the first key tile, so that a tile with
 // sinks is not one workgroup's walk over the whole sequence; at most about 64 (tile, range)
-// pairs a key head, of 256 tokens or more (short, so that they fill the gaps of the last round).
+// pairs a key head, of 256 tokens or more (64 in fp32): short, so that they fill the gaps of the last round.  While key tiles are
+// fewer than the 256 compute units, the heads that share a key head are also taken apart.
 struct SwaPlan {
-  int window, sinks, n_sink_tiles, n_far, far_len;
-  size_t delta_bytes, part_bytes;
+  int window, sinks, n_sink_tiles, n_far, far_len, n_head_part;
+  size_t delta_bytes, part_bytes, head_bytes;
+  size_t bytes() const { return 2 * delta_bytes + part_bytes + head_bytes + 256; }
 };
 SwaPlan swa_plan(const carve_swa_shape* s) {
   SwaPlan p;
@@ -75,13 +77,16 @@ SwaPlan swa_plan(const carve_swa_shape* s) {
   if (p.sinks > 0 && far > 0) {
     p.n_sink_tiles = ceil_div(p.sinks, carve::kSwaKeyTile);
     const int most = std::max(1, 64 / p.n_sink_tiles);
-    const int want = std::min(most, ceil_div(far, 256));
+    const int want = std::min(most, ceil_div(far, s->dtype == CARVE_F32 ? 64 : 256));
     p.far_len = ceil_div(ceil_div(far, want), 32) * 32;
     p.n_far = ceil_div(far, p.far_len);
   }
   p.delta_bytes = up256((size_t)s->B * s->Hq * s->T * sizeof(float));
-  p.part_bytes = (size_t)s->B * s->Hkv * p.n_sink_tiles * (p.n_far ? 1 + p.n_far : 0) * 2 * carve::kSwaKeyTile * s->D *
-                 sizeof(float);
+  const size_t one = 2 * carve::kSwaKeyTile * s->D * sizeof(float);
+  p.part_bytes = up256((size_t)s->B * s->Hkv * p.n_sink_tiles * (p.n_far ? 1 + p.n_far : 0) * one);
+  const long long tiles = (long long)s->B * s->Hkv * ceil_div(s->T, carve::kSwaKeyTile);
+  p.n_head_part = (int)std::max(1ll, std::min<long long>(s->Hq / s->Hkv, 256 / tiles));
+  p.head_bytes = p.n_head_part > 1 ? (size_t)tiles * p.n_head_part * one : 0;
   return p;
 }
 
@@ -181,7 +186,7 @@ carve_status carve_swa_fwd(const carve_swa_shape* s, const void* q, const void* 
 size_t carve_swa_bwd_workspace_size(const carve_swa_shape* s) {
   if (check_swa(s) != CARVE_OK || empty(s)) return 0;
   const SwaPlan p = swa_plan(s);
-  return 2 * p.delta_bytes + p.part_bytes + 256;
+  return p.bytes();
 }
 
 carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* k, const void* v, const int* lens,
@@ -194,9 +199,9 @@ carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* 
       !all_aligned({lens, lse}, 4))
     return CARVE_ERR_INVALID_ARG;
   const SwaPlan p = swa_plan(s);
-  if ((long long)s->B * s->Hq * (ceil_div(s->T, carve::kSwaKeyTile) + (long long)p.n_sink_tiles * p.n_far) > kMaxUnits)
+  if ((long long)s->B * s->Hq * ((long long)ceil_div(s->T, carve::kSwaKeyTile) * p.n_head_part + (long long)p.n_sink_tiles * p.n_far) > kMaxUnits)
     return CARVE_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < 2 * p.delta_bytes + p.part_bytes + 256) return CARVE_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < p.bytes()) return CARVE_ERR_WORKSPACE;
   carve::SwaArgs a = swa_args(s, q, k, v, lens);
   a.o = const_cast<void*>(o);
   a.lse = const_cast<float*>(lse);
@@ -208,6 +213,8 @@ carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* 
   a.delta = reinterpret_cast<float*>(ws);
   a.lse2 = reinterpret_cast<float*>(ws + p.delta_bytes);
   a.part = reinterpret_cast<float*>(ws + 2 * p.delta_bytes);
+  a.head_part = reinterpret_cast<float*>(ws + 2 * p.delta_bytes + p.part_bytes);
+  a.n_head_part = p.n_head_part;
   a.n_sink_tiles = p.n_sink_tiles;
   a.n_far = p.n_far;
   a.far_len = p.far_len;

@@ -30,6 +30,9 @@ struct SwaArgs {
   // key tiles, [B*Hkv][n_sink_tiles][1 + n_far][2][kSwaKeyTile][D] fp32
   float* part;
   int n_sink_tiles, n_far, far_len;
+  // few key tiles: the heads of a group in n_head_part parts, [B*Hkv][tiles][n_head_part][2][kSwaKeyTile][D]
+  float* head_part;
+  int n_head_part;
 };
 constexpr int kSwaKeyTile = 64;        // keys of a workgroup of the dk / dv pass
 

@@ -48,37 +48,48 @@ __device__ __forceinline__ float log2_lse(float lse) { return lse == -INFINITY ?
 // group.  The tokens behind the window of a tile that holds sinks see only the sinks: they are cut
 // into n_far ranges with workgroups of their own, whose sums, like the tile's, go to `part`
 // and are added by swa_sink_kernel.
+// Where tiles are few (a.n_head_part > 1), the heads of a group are cut into parts as well; then every
+// tile's sums go to `head_part`, and the same kernel adds them.
 struct KeyUnit {
-  int b, bk, n, kt, s0, t_lo, t_hi, part;     // part: index of the partial sum, -1 = final
+  int b, bk, n, kt, s0, t_lo, t_hi, h_lo, h_hi;
+  bool far;
+  float* part;                                // partial sums [2][kSwaKeyTile][D], null = final
 };
 __device__ __forceinline__ KeyUnit key_unit(const SwaArgs& a) {
   constexpr int KT = kSwaKeyTile;
-  const int NK = (a.T + KT - 1) / KT, per = NK + a.n_sink_tiles * a.n_far;
+  const int NK = (a.T + KT - 1) / KT, HP = a.n_head_part, G = a.Hq / a.Hkv, per = NK * HP + a.n_sink_tiles * a.n_far;
   const int unit = attn_unit(a.B * a.Hkv * per, 1, a.window, a.T);
   KeyUnit u;
   u.bk = uniform(unit / per);
   u.b = uniform(u.bk / a.Hkv);
   u.n = seq_len(a.lens, u.b, a.T);
   const int w = uniform(unit % per);
-  const bool far = w >= NK;
-  u.kt = uniform(far ? (w - NK) / a.n_far : w);
-  const int fi = uniform(far ? (w - NK) % a.n_far : 0);
+  u.far = w >= NK * HP;
+  u.kt = uniform(u.far ? (w - NK * HP) / a.n_far : w / HP);
+  const int fi = uniform(u.far ? (w - NK * HP) % a.n_far : 0), hp = uniform(u.far ? 0 : w % HP);
+  const int heads = (G + HP - 1) / HP;
+  u.h_lo = u.far ? 0 : hp * heads;
+  u.h_hi = u.far ? G : min(G, u.h_lo + heads);
   u.s0 = u.kt * KT;
   const long long band = (long long)u.s0 + KT - 1 + a.window;     // first token that sees no key of the tile
-  const long long lo = far ? band + (long long)fi * a.far_len : u.s0, hi = far ? lo + a.far_len : band;
+  const long long lo = u.far ? band + (long long)fi * a.far_len : u.s0, hi = u.far ? lo + a.far_len : band;
   u.t_lo = uniform((int)min((long long)u.n, lo));
   u.t_hi = uniform((int)min((long long)u.n, hi));
-  u.part = u.kt < a.n_sink_tiles && a.n_far > 0 ? (far ? 1 + fi : 0) : -1;
+  u.part = nullptr;
+  constexpr size_t one = 2 * KT;
+  if (u.far || (HP == 1 && u.kt < a.n_sink_tiles && a.n_far > 0))
+    u.part = a.part + (((size_t)u.bk * a.n_sink_tiles + u.kt) * (1 + a.n_far) + (u.far ? 1 + fi : 0)) * one * a.D;
+  else if (HP > 1)
+    u.part = a.head_part + (((size_t)u.bk * NK + u.kt) * HP + hp) * one * a.D;
   return u;
 }
 template <typename T, int D>
 __device__ __forceinline__ void store_key_grads(const SwaArgs& a, const KeyUnit& u, int s, int kb, f32x16 (&dK)[D / 32],
                                                 f32x16 (&dV)[D / 32]) {
   constexpr int KT = kSwaKeyTile;
-  if (u.part >= 0) {
-    float* dst = a.part + ((((size_t)u.bk * a.n_sink_tiles + u.kt) * (1 + a.n_far) + u.part) * 2 * KT + 32 * kb +
-                           (lane_id() & 31)) * D;
-    if (u.part == 0 || s < a.sinks) {      // (a far range adds to sinks only)
+  if (u.part) {
+    float* dst = u.part + (32 * kb + (lane_id() & 31)) * D;
+    if (!u.far || s < a.sinks) {              // (a far range adds to sinks only)
       store_column<float, D>(dst, dK, a.scale);
       store_column<float, D>(dst + (size_t)KT * D, dV, 1.f);
     }
@@ -281,7 +292,7 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
     dK[dt] = zero16();
     dV[dt] = zero16();
   }
-  if (t_lo < t_hi && s0 < n) {
+  if (t_lo < t_hi && s0 < n && un.h_lo < un.h_hi) {
     Frag<bf16> K[KK], V[KK];
     const size_t at = ((size_t)un.bk * a.T + min(s, n - 1)) * D + 8 * half;
 #pragma unroll
@@ -290,12 +301,12 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
       V[kk] = load_frag(reinterpret_cast<const bf16*>(a.v) + at + 16 * kk);
     }
     const float c = a.scale * kLog2e;
-    const int nt = (t_hi - t_lo + kDkRows - 1) / kDkRows, total = nt * G;
+    const int nt = (t_hi - t_lo + kDkRows - 1) / kDkRows, total = nt * (un.h_hi - un.h_lo);
     const int rt = Tile::row_base() + 4096 * th, ct0 = Tile::col_base() + 4096 * th;   // (32 rows of a block)
     const int row0 = (un.b * a.Hq + (un.bk % a.Hkv) * G);
-    int lg = 0, lt = 0;                    // head and tile of the next load
+    int lg = un.h_lo, lt = 0;              // head and tile of the next load
     auto load = [&](unsigned char* Qs, unsigned char* Gs, float* Ls) {
-      if (lg >= G) return;
+      if (lg >= un.h_hi) return;
       const size_t row = (size_t)(row0 + lg) * a.T;
       const int tt = t_lo + lt * kDkRows;
       Tile::template load<4>(Qs, reinterpret_cast<const bf16*>(a.q) + row * D, tt, t_hi, wave);
@@ -487,7 +498,7 @@ __global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
     dK[dt] = zero16();
     dV[dt] = zero16();
   }
-  if (t_lo < t_hi && s0 < n) {
+  if (t_lo < t_hi && s0 < n && un.h_lo < un.h_hi) {
     Frag<T> K[D / 16], V[D / 16];
     const size_t at = ((size_t)bk * a.T + min(s, n - 1)) * D + 8 * half;
 #pragma unroll
@@ -496,11 +507,11 @@ __global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
       V[kk] = load_frag(reinterpret_cast<const T*>(a.v) + at + 16 * kk);
     }
     const float c = a.scale * kLog2e;
-    const int nt = (t_hi - t_lo + kDkQ - 1) / kDkQ, total = nt * G;
+    const int nt = (t_hi - t_lo + kDkQ - 1) / kDkQ, total = nt * (un.h_hi - un.h_lo);
     St qst, gst;
     float lst = 0.f, dst = 0.f;
     auto load = [&](int i) {
-      const int hq = (bk % a.Hkv) * G + i / nt, tt = t_lo + (i % nt) * kDkQ;
+      const int hq = (bk % a.Hkv) * G + un.h_lo + i / nt, tt = t_lo + (i % nt) * kDkQ;
       const size_t row = (size_t)(b * a.Hq + hq) * a.T;
       qst.load(reinterpret_cast<const T*>(a.q) + row * D, tt, t_hi);
       gst.load(reinterpret_cast<const T*>(a.dO) + row * D, tt, t_hi);
@@ -566,21 +577,29 @@ __global__ __launch_bounds__(256) void swa_dkdv_f32_kernel(SwaArgs a) {
   if (!th) store_key_grads<T, D>(a, un, s, kb, dK, dV);
 }
 
-// dk, dv of the tiles that hold sinks: the sums of the tile's window and far ranges, in order.
+// dk, dv of the tiles whose sums are in parts, added in order: the parts of the heads (or the tile's one
+// sum), then, for sinks, the far ranges.  `tiles` of a key head, from the first.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void swa_sink_kernel(SwaArgs a) {
   constexpr int KT = kSwaKeyTile, PR = D / 4;
-  const int kt = blockIdx.x % a.n_sink_tiles, bk = blockIdx.x / a.n_sink_tiles;
+  constexpr size_t one = 2 * KT * D;
+  const int NK = (a.T + KT - 1) / KT, HP = a.n_head_part, tiles = HP > 1 ? NK : a.n_sink_tiles;
+  const int kt = blockIdx.x % tiles, bk = blockIdx.x / tiles;
   const int n = seq_len(a.lens, bk / a.Hkv, a.T);
-  const float* src = a.part + ((size_t)bk * a.n_sink_tiles + kt) * (1 + a.n_far) * 2 * KT * D;
+  const bool sink = kt < a.n_sink_tiles && a.n_far > 0;
+  const float* far = a.part + ((size_t)bk * a.n_sink_tiles + kt) * (1 + a.n_far) * one;
+  const float* src = HP > 1 ? a.head_part + ((size_t)bk * NK + kt) * HP * one : far;
   for (int i = blockIdx.y * 256 + threadIdx.x; i < 2 * KT * PR; i += 256 * gridDim.y) {
     const int which = i / (KT * PR), r = (i / PR) % KT, s = kt * KT + r;
     if (s >= a.T) continue;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    const int last = s < a.sinks ? a.n_far : 0;
-    if (s < n)
+    const int last = sink && s < a.sinks ? a.n_far : 0;
+    if (s < n) {
 #pragma unroll 4
-      for (int f = 0; f <= last; ++f) x += load4f(src + (size_t)f * 2 * KT * D + (size_t)i * 4);
+      for (int f = 0; f < HP; ++f) x += load4f(src + (size_t)f * one + (size_t)i * 4);
+#pragma unroll 4
+      for (int f = 1; f <= last; ++f) x += load4f(far + (size_t)f * one + (size_t)i * 4);
+    }
     T* dst = reinterpret_cast<T*>(which ? a.dv : a.dk);
     store4(dst + ((size_t)bk * a.T + s) * D + 4 * (i % PR), x);
   }
@@ -589,7 +608,8 @@ __global__ __launch_bounds__(256) void swa_sink_kernel(SwaArgs a) {
 template <typename T, int D>
 static hipError_t launch(const SwaArgs& a, hipStream_t st) {
   const dim3 grid_q(a.B * a.Hq * ((a.T + kDqQ - 1) / kDqQ));
-  const dim3 grid_k(a.B * a.Hkv * ((a.T + kSwaKeyTile - 1) / kSwaKeyTile + a.n_sink_tiles * a.n_far));
+  const int NK = (a.T + kSwaKeyTile - 1) / kSwaKeyTile;
+  const dim3 grid_k(a.B * a.Hkv * (NK * a.n_head_part + a.n_sink_tiles * a.n_far));
   hipError_t e;
   if constexpr (sizeof(T) == 2) {
     e = launch_kernel<0>(swa_dq_bf16_kernel<D>, grid_q, 256, a, st);
@@ -600,8 +620,9 @@ static hipError_t launch(const SwaArgs& a, hipStream_t st) {
     e = launch_kernel<lds_q>(swa_dq_f32_kernel<D>, grid_q, 256, a, st);
     if (e == hipSuccess) e = launch_kernel<lds_k>(swa_dkdv_f32_kernel<D>, grid_k, 256, a, st);
   }
-  if (e != hipSuccess || a.n_sink_tiles * a.n_far == 0) return e;
-  return launch_kernel<0>(swa_sink_kernel<T, D>, dim3(a.B * a.Hkv * a.n_sink_tiles, 8), 256, a, st);
+  const int tiles = a.n_head_part > 1 ? NK : a.n_sink_tiles * (a.n_far > 0);
+  if (e != hipSuccess || tiles == 0) return e;
+  return launch_kernel<0>(swa_sink_kernel<T, D>, dim3(a.B * a.Hkv * tiles, 8), 256, a, st);
 }
 
 hipError_t launch_swa_bwd(const SwaArgs& a, hipStream_t st) {
