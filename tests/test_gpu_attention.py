@@ -233,6 +233,96 @@ def test_two_streams_at_once(dt):
                 assert torch.equal(x, y)
 
 
+def test_autograd_shapes_of_gradients():
+    """An output gradient that is a broadcast number, gradients asked for in part, and a captured
+    forward and backward without leaves of an eager graph alive."""
+    q, k, v, _ = inputs(2, 4, 2, 90, 64, "bf16", seed=39)
+    leaves = [x.detach().clone().requires_grad_() for x in (q, k, v)]
+    swa_attention(*leaves, window=20, sinks=1).float().sum().backward()
+    o, lse = carve.swa_fwd(q, k, v, window=20, sinks=1)
+    g = carve.swa_bwd(q, k, v, o, lse, torch.ones_like(o), window=20, sinks=1)
+    for x, name in zip(leaves, ("dq", "dk", "dv")):
+        assert torch.equal(x.grad, g[name])
+    kk = k.detach().clone().requires_grad_()
+    only, = torch.autograd.grad(swa_attention(q, kk, v, window=20, sinks=1).float().sum(), kk)
+    assert torch.equal(only, g["dk"])
+    del leaves, kk
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        x = [y.detach().clone().requires_grad_() for y in (q, k, v)]
+        for _ in range(2):
+            torch.autograd.grad(swa_attention(*x, window=20, sinks=1), x, torch.ones_like(q))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(swa_attention(*x, window=20, sinks=1), x, torch.ones_like(q))
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for y, name in zip(got, ("dq", "dk", "dv")):
+            assert torch.equal(y, g[name])
+
+
+def test_most_heads():
+    """The largest accepted number of sequences and heads, a few tokens each: sampled rows."""
+    B, T, D = 65535, 3, 64
+    gen = torch.Generator(device="cuda").manual_seed(45)
+    q, k, v, dO = (torch.randn(B, 1, T, D, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    o, lse = carve.swa_fwd(q, k, v, window=2, sinks=1)
+    g = carve.swa_bwd(q, k, v, o, lse, dO, window=2, sinks=1)
+    w = carve.budget_weights(q, k, lse, window=2, sinks=1)
+    at = torch.tensor([0, 1, 32767, 32768, 65534], device="cuda")
+    want = ref.swa(q[at], k[at], v[at], 2, 1, None, None, dO[at])
+    for name, x in (("o", o), ("lse", lse), ("dq", g["dq"]), ("dk", g["dk"]), ("dv", g["dv"])):
+        ref.within(x[at], want[name], name)
+    ref.within(w[at], ref.weights(q[at], k[at], 2, 1, None, None), "weights")
+    cache = carve.budget_keep(k, v, w, 2, sinks=1, recent=1)
+    assert (cache[3][:, 0, 0] == 0).all() and (cache[3][:, 0, 1] == 2).all()
+    assert torch.equal(cache[0][:, :, 1], k[:, :, 2])
+    q1, k1, v1 = (x[:, :, 0].contiguous() for x in (q, k, v))
+    pos = torch.full((B,), 3, dtype=torch.int32, device="cuda")
+    o1, slot = carve.budget_decode(q1, k1, v1, cache, pos, sinks=1, recent=1)
+    assert (slot == 1).all() and torch.equal(cache[0][:, :, 1], k1)
+    for b in at.tolist():
+        x = ref.rows(q1[b, 0], cache[0][b, 0], cache[1][b, 0], torch.ones(2, dtype=torch.bool, device="cuda"), D ** -0.5)
+        ref.within(o1[b, 0], x[:2], f"row {b}")
+
+
+def test_longest_sequence():
+    """2^20 tokens of one head: the last tokens against the definition, the sinks' gradients (which
+    come from every token) through sum dq q = sum dk k, both sides sum ds s: each element off by at
+    most half a step u twice (as a result, and in ds), so the sums by 2 u (sum |dq q| + sum |dk k|)."""
+    T, D, window, sinks = 1 << 20, 64, 40, 3
+    gen = torch.Generator(device="cuda").manual_seed(47)
+    q, k, v, dO = (torch.randn(1, 1, T, D, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    o, lse = carve.swa_fwd(q, k, v, window=window, sinks=sinks)
+    g = carve.swa_bwd(q, k, v, o, lse, dO, window=window, sinks=sinks)
+    n = 200                                    # tokens that the last n see: the sinks and the n + window last
+    at = torch.cat([torch.arange(sinks, device="cuda"), torch.arange(T - n - window, T, device="cuda")])
+    qq, kk, vv = q[:, :, at].contiguous(), k[:, :, at].contiguous(), v[:, :, at].contiguous()
+    want = ref.swa(qq, kk, vv, window, sinks, None, None, dO[:, :, at].contiguous())
+    for name, x in (("o", o), ("lse", lse), ("dq", g["dq"])):
+        ref.within(x[:, :, T - n:], tuple(y[:, :, -n:] for y in want[name]), name)
+    for name in ("dk", "dv"):
+        ref.within(g[name][:, :, T - n:], tuple(y[:, :, -n:] for y in want[name]), name)
+    a, b = g["dq"].double() * q.double(), g["dk"].double() * k.double()
+    room = 2 * ref.half_step(q.dtype) * float(a.abs().sum() + b.abs().sum())
+    assert abs(float(a.sum() - b.sum())) <= room
+    # the sinks' own share of it is far above what a lost range of tokens could hide in
+    s = (q[0, 0].double() @ k[0, 0, :sinks].double().T) * D ** -0.5
+    p = torch.exp(s - lse[0, 0, :, None].double())
+    t = torch.arange(T, device="cuda")[:, None]
+    p = torch.where(t >= torch.arange(sinks, device="cuda"), p, 0.0)
+    dv = p.T @ dO[0, 0].double()
+    off = (g["dv"][0, 0, :sinks].double() - dv).abs()
+    A = float((q[0, 0].double().abs() @ k[0, 0, :sinks].double().abs().T).max()) * D ** -0.5
+    # a weight's error with lse as the kernel's; a range of at most T / 64 + 64 tokens summed, then 65 ranges
+    e = ref.F32 * (2 * (2 * (D + 4) * A + 64 + 16) + T // 64 + 64 + 65)
+    bound = ref.half_step(q.dtype) * dv.abs() + (ref.half_step(q.dtype) + e) * (p.T @ dO[0, 0].double().abs())
+    assert (off <= bound).all()
+
+
 # ------------------------------------------------------------------ ring cache
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("Hq,Hkv,D,window,sinks,lens", [
