@@ -9,7 +9,8 @@
 // That is seven products of a visible pair where one pass with shared sums has five.
 // Bound by the products and the vector work beside them, and in the second pass by waits that its
 // 256 registers a wave leave uncovered (matrix cores busy 0.48, vector units 0.37 and 0.30).
-// B4, 16 heads on 4, T = 4,096, window 1,024, 4 sinks, D = 128: dq 217 us, dk/dv 280 us, sinks 5 us.
+// B4, 16 heads on 4, T = 4,096, window 1,024, 4 sinks, D = 128: dq 214 us, dk/dv 268 us, sinks 5 us
+// (0.61 ms with the forward pass, 0.69 PFLOP/s of 14 D flops a visible pair).
 #include <algorithm>
 
 #include "attn_device.h"
