@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
   __shared__ __align__(16) int hist[4 * 2048];
   __shared__ int red[NW];
   __shared__ int count[NW][2];
-  __shared__ unsigned found[2];
+  __shared__ unsigned found[3];
   const int bk = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wave = wave_uid();
   const int n = seq_len(a.lens, bk / a.Hkv, a.T);
   const float* w = a.weights + (size_t)bk * a.T;
@@ -68,11 +68,20 @@ __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
   auto key_of = [&](int j, float v) { return j >= lo && j < hi ? heavy_order(v) : 0u; };
   unsigned x[VPT > 0 ? VPT : 1];
   if constexpr (VPT > 0) {
-    float v[VPT];                          // loads without branches, all in flight together
+    // loads without branches, all in flight together; past the last token they give zero
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(w), 0, n * 4, 0x00020000);
+    unsigned v[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) v[i] = n > 0 ? w[min(j_wave + 64 * i, n - 1)] : 0.f;
+    for (int i = 0; i < VPT; ++i)
+      v[i] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, j_wave * 4 + (i % 16) * 256, (i / 16) * 4096, 0);
+    const int j0 = wave * steps * 64;
+    if (steps == VPT && j0 >= lo && j0 + 64 * VPT <= hi) {       // candidates alone
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) x[i] = i < steps ? key_of(j_wave + 64 * i, v[i]) : 0u;
+      for (int i = 0; i < VPT; ++i) x[i] = heavy_order(__builtin_bit_cast(float, v[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) x[i] = i < steps ? key_of(j_wave + 64 * i, __builtin_bit_cast(float, v[i])) : 0u;
+    }
   }
   // fn(token, key) over the wave's tokens, in order
   auto each = [&](auto&& fn) {
@@ -86,23 +95,26 @@ __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
       }
     }
   };
-  // the threshold: keys above it stay, and the first `need` equal to it
-  unsigned prefix = m == cand ? 0u : 0xffffffffu;
+  // the threshold: keys above it stay; of those equal to it the first `need`, and if that is all of
+  // them it is lowered by one step, so that nothing more asks for equal keys
+  unsigned limit = m == cand ? 0u : 0xffffffffu;
   int need = 0;
   if (m < cand && m > 0) {
-    unsigned mask = 0;
-    prefix = 0;
+    unsigned prefix = 0;
+    int same = 0;
     need = m;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    // The digit of `BITS` bits above the lowest SHIFT of the keys that agree with prefix above it.
+    // Keys 0 share no first digit with a candidate (-inf, the lowest, has the key 0x007fffff).
+    auto digit = [&](auto shift_c, auto bits_c) {
+      constexpr int SHIFT = decltype(shift_c)::value, BITS = decltype(bits_c)::value, bins = 1 << BITS;
       typedef int i32x4 __attribute__((ext_vector_type(4)));
       i32x4* h4 = reinterpret_cast<i32x4*>(hist);
       h4[tid] = i32x4{0, 0, 0, 0};
       h4[tid + 1024] = i32x4{0, 0, 0, 0};
       __syncthreads();
       each([&](int, unsigned key) {
-        if (key != 0u && (key & mask) == prefix) atomicAdd(&hist[((key >> shift) & (bins - 1)) * 4 + (lane & 3)], 1);
+        const unsigned rest = key ^ prefix;
+        if (SHIFT + BITS == 32 ? key != 0u : rest < 1u << ((SHIFT + BITS) & 31)) atomicAdd(&hist[(rest >> SHIFT) * 4 + (lane & 3)], 1);
       });
       __syncthreads();
       // bins from the top: thread t has bins - 1 - 2 t and the one below
@@ -115,42 +127,54 @@ __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
         const bool top = need <= above + h1;
         found[0] = (unsigned)(top ? b1 : b1 - 1);
         found[1] = (unsigned)(need - (top ? above : above + h1));
+        found[2] = (unsigned)(top ? h1 : h0);
       }
       __syncthreads();
-      prefix |= found[0] << shift;
-      mask |= (unsigned)(bins - 1) << shift;
-      need = (int)found[1];
-      __syncthreads();
+      prefix |= uniform(found[0]) << SHIFT;
+      need = uniform((int)found[1]);
+      same = uniform((int)found[2]);
+    };
+    digit(std::integral_constant<int, 21>{}, std::integral_constant<int, 11>{});
+    digit(std::integral_constant<int, 10>{}, std::integral_constant<int, 11>{});
+    digit(std::integral_constant<int, 0>{}, std::integral_constant<int, 10>{});
+    limit = prefix;
+    if (need == same) {
+      limit = prefix - 1;
+      need = 0;
     }
   }
   int kept = 0, ties = 0;
-  each([&](int, unsigned key) {
-    kept += __popcll(__ballot(key > prefix));
-    ties += __popcll(__ballot(key == prefix));
-  });
+  each([&](int, unsigned key) { kept += __popcll(__ballot(key > limit)); });
+  if (need > 0) each([&](int, unsigned key) { ties += __popcll(__ballot(key == limit)); });
   if (lane == 0) {
     count[wave][0] = kept;
     count[wave][1] = ties;
   }
   __syncthreads();
-  int base = lo, tied = 0, end = lo, all_ties = 0;
+  int base = lo, tied = 0, end = lo + need;
 #pragma unroll
   for (int i = 0; i < NW; ++i) {
     base += i < wave ? count[i][0] : 0;
     tied += i < wave ? count[i][1] : 0;
     end += count[i][0];
-    all_ties += count[i][1];
   }
-  end += min(all_ties, need);
-  if (kept + ties > 0)
+  base = uniform(base);
+  tied = uniform(tied);
+  if (need == 0) {
     each([&](int j, unsigned key) {
-      const unsigned long long keeps = __ballot(key > prefix), equal = __ballot(key == prefix);
+      const unsigned long long keeps = __ballot(key > limit);
+      if (key > limit) cp[base + bits_below(keeps)] = j;
+      base += __popcll(keeps);
+    });
+  } else if (kept + ties > 0) {
+    each([&](int j, unsigned key) {
+      const unsigned long long keeps = __ballot(key > limit), equal = __ballot(key == limit);
       const int t = tied + bits_below(equal);                    // equal weights before this one
-      const int at = base + bits_below(keeps) + min(t, need);
-      if ((key > prefix || (key == prefix && t < need)) && at < a.C) cp[at] = j;
+      if (key > limit || (key == limit && t < need)) cp[base + bits_below(keeps) + min(t, need)] = j;
       base += __popcll(keeps);
       tied += __popcll(equal);
     });
+  }
   // the first and the recent tokens, and the empty slots
   for (int j = tid; j < lo; j += kSelThreads) cp[j] = j;
   for (int j = hi + tid; j < n; j += kSelThreads) cp[end + j - hi] = j;
