@@ -46,13 +46,15 @@ __device__ __forceinline__ int bits_below(unsigned long long b) {
 // before it.  A wave's stretch is kept in registers as ordered bits, VPT a lane (VPT = 0: sequences
 // past 32 x 1024 tokens, read again in every pass).  The one compute unit's instruction rate
 // bounds it, so tokens that are not candidates carry the key 0, below every weight's, and are told
-// apart by nothing else.  32 key heads of 32,768 tokens: 23 us (55 us with the weights read again in
-// every pass and a scan across the workgroup for every 1,024 of them).
+// apart by nothing else.  32 key heads of 32,768 tokens: 17 us (55 us with the weights read again in
+// every pass and a scan across the workgroup for every 1,024 of them).  Of it the loads take 2.8 us,
+// the digits 3.7, 1.8 and 1.8, the counts 1.4, the positions 3.1.
 template <int VPT>
 __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
   constexpr int NW = kSelThreads / 64;
-  // four copies of the histogram, a quarter of the lanes each: weights crowd into few bins, and
-  // lanes that add to one address take turns
+  // the first digit's histogram in four copies, a quarter of the lanes each: weights crowd into few
+  // bins, and lanes that add to one address take turns (one copy 1.3 us more, eight 0.6 us more to
+  // clear and add up); the later digits are of few weights
   __shared__ __align__(16) int hist[4 * 2048];
   __shared__ int red[NW];
   __shared__ int count[NW][2];
@@ -103,24 +105,28 @@ __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
     unsigned prefix = 0;
     int same = 0;
     need = m;
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
     // The digit of `BITS` bits above the lowest SHIFT of the keys that agree with prefix above it.
     // Keys 0 share no first digit with a candidate (-inf, the lowest, has the key 0x007fffff).
-    auto digit = [&](auto shift_c, auto bits_c) {
-      constexpr int SHIFT = decltype(shift_c)::value, BITS = decltype(bits_c)::value, bins = 1 << BITS;
-      typedef int i32x4 __attribute__((ext_vector_type(4)));
-      i32x4* h4 = reinterpret_cast<i32x4*>(hist);
-      h4[tid] = i32x4{0, 0, 0, 0};
-      h4[tid + 1024] = i32x4{0, 0, 0, 0};
+    auto digit = [&](auto shift_c, auto bits_c, auto copies_c) {
+      constexpr int SHIFT = decltype(shift_c)::value, BITS = decltype(bits_c)::value, bins = 1 << BITS, COPIES = decltype(copies_c)::value;
+      for (int i = tid; i < bins * COPIES / 4; i += kSelThreads) reinterpret_cast<i32x4*>(hist)[i] = i32x4{0, 0, 0, 0};
       __syncthreads();
       each([&](int, unsigned key) {
         const unsigned rest = key ^ prefix;
-        if (SHIFT + BITS == 32 ? key != 0u : rest < 1u << ((SHIFT + BITS) & 31)) atomicAdd(&hist[(rest >> SHIFT) * 4 + (lane & 3)], 1);
+        if (SHIFT + BITS == 32 ? key != 0u : rest < 1u << ((SHIFT + BITS) & 31)) atomicAdd(&hist[(rest >> SHIFT) * COPIES + lane % COPIES], 1);
       });
       __syncthreads();
-      // bins from the top: thread t has bins - 1 - 2 t and the one below
+      // bins from the top: thread t has two, the upper one first
+      int h1 = 0, h0 = 0;
       const int b1 = bins - 1 - 2 * tid;
-      auto of = [&](int b) { return b < 0 ? 0 : h4[b][0] + h4[b][1] + h4[b][2] + h4[b][3]; };
-      const int h1 = of(b1), h0 = of(b1 - 1);
+      if (b1 > 0) {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          h0 += hist[(b1 - 1) * COPIES + i];
+          h1 += hist[b1 * COPIES + i];
+        }
+      }
       int total;
       const int upto = block_scan(h1 + h0, red, total), above = upto - h1 - h0;
       if (above < need && need <= upto) {
@@ -134,9 +140,9 @@ __global__ __launch_bounds__(kSelThreads) void keep_select_kernel(FillArgs a) {
       need = uniform((int)found[1]);
       same = uniform((int)found[2]);
     };
-    digit(std::integral_constant<int, 21>{}, std::integral_constant<int, 11>{});
-    digit(std::integral_constant<int, 10>{}, std::integral_constant<int, 11>{});
-    digit(std::integral_constant<int, 0>{}, std::integral_constant<int, 10>{});
+    digit(std::integral_constant<int, 21>{}, std::integral_constant<int, 11>{}, std::integral_constant<int, 4>{});
+    digit(std::integral_constant<int, 10>{}, std::integral_constant<int, 11>{}, std::integral_constant<int, 1>{});
+    digit(std::integral_constant<int, 0>{}, std::integral_constant<int, 10>{}, std::integral_constant<int, 1>{});
     limit = prefix;
     if (need == same) {
       limit = prefix - 1;
