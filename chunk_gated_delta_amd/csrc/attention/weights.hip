@@ -201,8 +201,16 @@ __global__ __launch_bounds__(256) void weight_sum_kernel(WeightArgs a) {
   const size_t N = (size_t)a.B * a.Hkv * a.T;
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= N) return;
+  const int parts = a.n_chunk * a.n_head;
+  constexpr int U = 8;                           // loads in flight together, added in order
   float x = 0.f;
-  for (int c = 0; c < a.n_chunk * a.n_head; ++c) x += a.part[c * N + i];
+  for (int c0 = 0; c0 < parts; c0 += U) {
+    float y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) y[u] = a.part[min(c0 + u, parts - 1) * N + i];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x += c0 + u < parts ? y[u] : 0.f;
+  }
   a.out[i] = x;
 }
 
