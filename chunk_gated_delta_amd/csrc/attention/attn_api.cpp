@@ -60,6 +60,12 @@ void mask_of(const carve_swa_shape* s, int* window, int* sinks) {
   *sinks = whole ? 0 : s->sinks;
 }
 
+// Parts of a group's heads, at most `most` and none without heads.
+int head_parts(const carve_swa_shape* s, long long most) {
+  const int G = s->Hq / s->Hkv, n = (int)std::max(1ll, std::min<long long>(G, most));
+  return ceil_div(G, ceil_div(G, n));
+}
+
 // Backward: ranges of the tokens behind the window of the first key tile, so that a tile with
 // sinks is not one workgroup's walk over the whole sequence; at most about 64 (tile, range)
 // pairs a key head, of 256 tokens or more (64 in fp32): short, so that they fill the gaps of the last round.  While key tiles are
@@ -85,7 +91,7 @@ SwaPlan swa_plan(const carve_swa_shape* s) {
   const size_t one = 2 * carve::kSwaKeyTile * s->D * sizeof(float);
   p.part_bytes = up256((size_t)s->B * s->Hkv * p.n_sink_tiles * (p.n_far ? 1 + p.n_far : 0) * one);
   const long long tiles = (long long)s->B * s->Hkv * ceil_div(s->T, carve::kSwaKeyTile);
-  p.n_head_part = (int)std::max(1ll, std::min<long long>(s->Hq / s->Hkv, 256 / tiles));
+  p.n_head_part = head_parts(s, 256 / tiles);
   p.head_bytes = p.n_head_part > 1 ? (size_t)tiles * p.n_head_part * one : 0;
   return p;
 }
@@ -110,9 +116,10 @@ carve::SwaArgs swa_args(const carve_swa_shape* s, const void* q, const void* k, 
 
 // Token ranges of the weight pass: enough workgroups to fill the chip several times over (the
 // later keys are seen by few tokens, so the ranges are uneven), of at least 128 tokens.  In fp32,
-// whose products take sixteen times as long, ranges from 64 tokens and, while compute units
-// are idle, the heads of a group apart (4 rows of 11 tokens, 32 heads on 4: 28 -> 13 us, where
-// the sum's launch costs 3; in bf16 it would cost more than it gives).
+// whose products take sixteen times as long, ranges from 64 tokens and, up to four workgroups a
+// compute unit, the heads of a group apart (4 rows of 11 tokens, 32 heads on 4: 28 -> 13 us, where
+// the sum's launch costs 3; in bf16 it would cost more than it gives), into no more than 48 parts
+// with the ranges (one row of 1,999 tokens, 3 heads on 1: 26 us of 32 parts, 29 of 64).
 struct WeightPlan {
   int n_chunk, chunk, n_head;
 };
@@ -123,7 +130,7 @@ WeightPlan weight_plan(const carve_swa_shape* s) {
   WeightPlan p;
   p.chunk = ceil_div(ceil_div(s->T, want), 32) * 32;
   p.n_chunk = ceil_div(s->T, p.chunk);
-  p.n_head = f32 ? (int)std::max(1ll, std::min<long long>(s->Hq / s->Hkv, 256 / (units * p.n_chunk))) : 1;
+  p.n_head = f32 ? head_parts(s, std::min(1024 / (units * p.n_chunk), 48ll / p.n_chunk)) : 1;
   return p;
 }
 
