@@ -264,6 +264,22 @@ def test_autograd_shapes_of_gradients():
             assert torch.equal(y, g[name])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_heads_that_parts_do_not_divide(dt):
+    """Five and seven heads on one, where a group's heads are cut into parts of two and of four."""
+    case = dict(window=60, sinks=3)
+    q, k, v, dO = inputs(9, 5, 1, 500, 64, dt, seed=51)
+    lens = [500, 0, 1, 64, 65, 499, 333, 130, 500]
+    want = ref.swa(q, k, v, 60, 3, None, lens, dO)
+    o, lse = carve.swa_fwd(q, k, v, lens=ints(lens), **case)
+    g = carve.swa_bwd(q, k, v, o, lse, dO, lens=ints(lens), **case)
+    for name, x in (("o", o), ("lse", lse), ("dq", g["dq"]), ("dk", g["dk"]), ("dv", g["dv"])):
+        ref.within(x, want[name], name)
+    q, k, v, _ = inputs(1, 7, 1, 1030, 64, dt, seed=53)
+    w = carve.budget_weights(q, k, carve.swa_fwd(q, k, v, window=1030)[1])
+    ref.within(w, ref.weights(q, k, 1030, 0, None, None), "weights")
+
+
 def test_most_heads():
     """The largest accepted number of sequences and heads, a few tokens each: sampled rows."""
     B, T, D = 65535, 3, 64
