@@ -84,6 +84,8 @@ class _SwaPair(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dO):
+        if torch.is_grad_enabled():                # create_graph: the kernels' results would pass as constants
+            raise RuntimeError("swa_attention has no gradients of gradients (create_graph=True)")
         q, k, v, lens, o, lse = ctx.saved_tensors
         g = carve.swa_bwd(q, k, v, o, lse, _c(dO), lens=lens, **ctx.at)
         return g["dq"], g["dk"], g["dv"], None, None, None, None
@@ -91,7 +93,9 @@ class _SwaPair(torch.autograd.Function):
 
 def swa_attention(q, k, v, window, sinks=0, scale=None, lens=None):
     """o of sliding-window attention with sinks, differentiable in q, k and v (carve_swa_fwd /
-    carve_swa_bwd; arguments as carve.swa_fwd)."""
+    carve_swa_bwd; arguments as carve.swa_fwd).  Gradients of gradients (create_graph=True) are refused.  A backward
+    pass that is captured into a graph needs leaves of which no eager graph is alive (PyTorch's rule
+    for any function: it ends the process otherwise)."""
     return _SwaPair.apply(q, k, v, lens, window, sinks, scale)
 
 

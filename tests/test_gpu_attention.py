@@ -264,6 +264,13 @@ def test_autograd_shapes_of_gradients():
             assert torch.equal(y, g[name])
 
 
+def test_gradients_of_gradients_are_refused():
+    q, k, v, _ = inputs(1, 2, 1, 20, 64, "f32", seed=49)
+    q.requires_grad_()
+    with pytest.raises(RuntimeError, match="gradients of gradients"):
+        torch.autograd.grad(swa_attention(q, k, v, window=5).sum(), q, create_graph=True)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_heads_that_parts_do_not_divide(dt):
     """Five and seven heads on one, where a group's heads are cut into parts of two and of four."""
