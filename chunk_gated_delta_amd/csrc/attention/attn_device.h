@@ -191,16 +191,20 @@ __device__ __forceinline__ float other_half(float x) {
   return __builtin_bit_cast(float, (lane_id() & 32) ? r[0] : r[1]);
 }
 
-// Key tiles that a tile of tokens t0 .. t1 - 1 sees, in the order sinks, then window.
+// Key tiles that a tile of tokens t0 .. t1 - 1 sees, in the order sinks, then window.  Of the tiles
+// before the window only the sinks are read (rows(i): the keys that tile i is cut off at): what stands
+// beside them is not seen, and a product of its weight 0 with a value that is not finite would be.
 template <int KT>
 struct KeyTiles {
-  int lo, nsink, count;
+  int lo, nsink, count, n_sinks;
   __device__ __forceinline__ KeyTiles(int t0, int t1, int window, int sinks) {
     lo = max(0, t0 - window + 1) / KT;
-    nsink = min((min(sinks, t1) + KT - 1) / KT, lo);
+    n_sinks = min(sinks, t1);
+    nsink = min((n_sinks + KT - 1) / KT, lo);
     count = nsink + (t1 - 1) / KT - lo + 1;
   }
   __device__ __forceinline__ int operator[](int i) const { return (i < nsink ? i : lo + i - nsink) * KT; }
+  __device__ __forceinline__ int rows(int i, int n) const { return i < nsink ? n_sinks : n; }
 };
 
 // tokens of sequence b, the same for every lane of the wave

@@ -204,8 +204,8 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
     };
     auto load = [&](unsigned char* Ks, unsigned char* Vs, int i) {
       if (i < kt.count) {
-        Tile::template load<4>(Ks, kb, kt[i], n, wave);
-        Tile::template load<4>(Vs, vb, kt[i], n, wave);
+        Tile::template load<4>(Ks, kb, kt[i], kt.rows(i, n), wave);
+        Tile::template load<4>(Vs, vb, kt[i], kt.rows(i, n), wave);
       }
     };
     auto sweep = [&](auto&& step) {
@@ -427,8 +427,8 @@ __global__ __launch_bounds__(256) void swa_dq_f32_kernel(SwaArgs a) {
     const float c = a.scale * kLog2e;
     const KeyTiles<kDqK> tile(t0, min(t0 + kDqQ, n), a.window, a.sinks);
     St kst, vst;
-    kst.load(kb, tile[0], n);
-    vst.load(vb, tile[0], n);
+    kst.load(kb, tile[0], tile.rows(0, n));
+    vst.load(vb, tile[0], tile.rows(0, n));
     for (int i = 0; i < tile.count; ++i) {
       const int s0 = tile[i];
       __syncthreads();
@@ -436,8 +436,8 @@ __global__ __launch_bounds__(256) void swa_dq_f32_kernel(SwaArgs a) {
       vst.store(Vs);
       __syncthreads();
       if (i + 1 < tile.count) {
-        kst.load(kb, tile[i + 1], n);
-        vst.load(vb, tile[i + 1], n);
+        kst.load(kb, tile[i + 1], tile.rows(i + 1, n));
+        vst.load(vb, tile[i + 1], tile.rows(i + 1, n));
       }
 #pragma unroll
       for (int u = 0; u < kDqK / 32; ++u) {

@@ -76,8 +76,8 @@ __global__ __launch_bounds__(256, 3) void swa_fwd_bf16_kernel(SwaArgs a) {
     const KeyTiles<kFwdKeys> kt(t0, min(t0 + kFwdQ, n), a.window, a.sinks);
     auto load = [&](unsigned char* Ks, unsigned char* Vs, int i) {
       if (i < kt.count) {
-        Tile::template load<4>(Ks, kb, kt[i], n, wave);
-        Tile::template load<4>(Vs, vb, kt[i], n, wave);
+        Tile::template load<4>(Ks, kb, kt[i], kt.rows(i, n), wave);
+        Tile::template load<4>(Vs, vb, kt[i], kt.rows(i, n), wave);
       }
     };
     load(K0, V0, 0);
@@ -172,8 +172,8 @@ __global__ __launch_bounds__(256) void swa_fwd_f32_kernel(SwaArgs a) {
     const float c = a.scale * kLog2e;
     const KeyTiles<kFwdK> tile(t0, min(t0 + kFwdQ, n), a.window, a.sinks);
     St kst, vst;
-    kst.load(kb, tile[0], n);
-    vst.load(vb, tile[0], n);
+    kst.load(kb, tile[0], tile.rows(0, n));
+    vst.load(vb, tile[0], tile.rows(0, n));
     for (int i = 0; i < tile.count; ++i) {
       const int s0 = tile[i];
       __syncthreads();
@@ -181,8 +181,8 @@ __global__ __launch_bounds__(256) void swa_fwd_f32_kernel(SwaArgs a) {
       vst.store(Vs);
       __syncthreads();
       if (i + 1 < tile.count) {
-        kst.load(kb, tile[i + 1], n);
-        vst.load(vb, tile[i + 1], n);
+        kst.load(kb, tile[i + 1], tile.rows(i + 1, n));
+        vst.load(vb, tile[i + 1], tile.rows(i + 1, n));
       }
 #pragma unroll
       for (int u = 0; u < kFwdK / 32; ++u) {

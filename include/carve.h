@@ -440,8 +440,9 @@ typedef struct {
  * lse_t = log sum_s exp(scale q_t . k_s).  window >= T is plain causal attention.
  *   q (device) [B,Hq,T,D], k, v (device) [B,Hkv,T,D]
  *   o (device) [B,Hq,T,D] written; lse (device) [B,Hq,T] float written, or NULL
- * A key or value that is not a number or infinite within a sequence may also reach tokens of
- * the neighbouring 128 that do not see it.
+ * A key or value within a sequence that is infinite or not a number may also reach tokens that
+ * do not see it, fewer than 192 tokens from those that do: they share a tile, where their weight
+ * for it is zero, and zero times such a value is not a number.  A query reaches its own row only.
  */
 carve_status carve_swa_fwd(const carve_swa_shape* s, const void* q, const void* k, const void* v, const int* lens,
                            void* o, float* lse, void* stream);
@@ -451,6 +452,9 @@ carve_status carve_swa_fwd(const carve_swa_shape* s, const void* q, const void* 
  * ds_ts = p_ts (dO_t . v_s - delta_t),  dq_t = scale sum_s ds_ts k_s,
  * dk_s = scale sum_t ds_ts q_t,  dv_s = sum_t p_ts dO_t (dk, dv summed over the group's heads).
  *   dO (device) [B,Hq,T,D]; dq as q, dk and dv as k (all written)
+ * Keys and values that are not finite reach dq as they reach o, and through o and lse the gradients
+ * of all that those tokens see; a row of q or dO that is not finite may also reach dk and dv of keys
+ * fewer than 64 tokens from those that its token sees.
  */
 size_t carve_swa_bwd_workspace_size(const carve_swa_shape* s);
 carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* k, const void* v, const int* lens,

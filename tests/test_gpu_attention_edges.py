@@ -1,0 +1,67 @@
+"""Edges of the attention operators on the GPU: values that are not numbers, scores of any size, and
+the variants that only some sizes reach, against the definitions in float64 (tests/attention_ref.py
+states the bounds)."""
+import math
+
+import pytest
+import torch
+
+from chunk_gated_delta_amd import carve
+from tests import attention_ref as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def normal(shape, dt, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(DT[dt]).cuda()
+
+
+def ints(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def inputs(B, Hq, Hkv, T, D, dt, seed):
+    return (normal((B, Hq, T, D), dt, seed), normal((B, Hkv, T, D), dt, seed + 1), normal((B, Hkv, T, D), dt, seed + 2),
+            normal((B, Hq, T, D), dt, seed + 3))
+
+
+def same(x, y):
+    """Equal bits."""
+    kind = torch.int16 if x.dtype is torch.bfloat16 else torch.int32
+    return torch.equal(x.contiguous().view(kind), y.contiguous().view(kind))
+
+
+# ------------------------------------------------------------------ values that are not numbers
+REACH = 192          # a key or value that is not finite stays within this many tokens of those that see it
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,sinks,at", [
+    (64, 4, (10, 31, 40, 63)), (128, 1, (1, 20)), (64, 40, (45, 63, 64)), (128, 70, (75, 127))])
+def test_not_finite_keys_beside_the_sinks(D, sinks, at, dt):
+    """A key and a value beside the sinks that are not finite: past their window (and the tiles
+    that see it) every output, gradient of a query, key and value is what it is without them."""
+    B, Hq, Hkv, T, window = 1, 4, 2, 900, 100
+    q, k, v, dO = inputs(B, Hq, Hkv, T, D, dt, seed=3)
+
+    def step(k, v):
+        o, lse = carve.swa_fwd(q, k, v, window, sinks=sinks)
+        g = carve.swa_bwd(q, k, v, o, lse, dO, window, sinks=sinks)
+        return dict(o=o, lse=lse, dq=g["dq"], dk=g["dk"], dv=g["dv"])
+
+    want = step(k, v)
+    for bad in (math.nan, math.inf):
+        for which in (0, 1):
+            kv = [k.clone(), v.clone()]
+            for s in at:
+                kv[which][0, 1, s, 5] = bad
+            got = step(*kv)
+            clean = max(at) + window + REACH         # the first token that none of them reaches
+            for name, x in got.items():
+                assert same(x[:, :, clean:], want[name][:, :, clean:]), (name, bad, which)
+                heads = slice(0, 2 if name in ("o", "lse", "dq") else 1)       # of the other key head
+                assert same(x[:, heads], want[name][:, heads]), (name, bad, which)
+            # and what sees one that is not a number is not one itself
+            if bad is math.nan:
+                assert torch.isnan(got["o"][0, 2:, max(at), 5].float()).all()
