@@ -95,6 +95,13 @@ __global__ __launch_bounds__(256, 4) void weight_bf16_kernel(WeightArgs a) {
 #pragma unroll
           for (int kk = 0; kk < KK; ++kk) mma32(S, Tile::row_frag(Qs, rb, 32 * u, kk), K[kk]);
           const bool full = sw + 31 <= tt && (tt + 31 - sw < a.window || sw + 32 <= a.sinks);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 32 * u + 8 * q + 4 * half);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[4 * q + e] = S[4 * q + e] * c - ls[e];
+          }
+          // masked after the lse is taken off: one that is not a number stays with the keys that are seen
           if (!full) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -104,11 +111,7 @@ __global__ __launch_bounds__(256, 4) void weight_bf16_kernel(WeightArgs a) {
             }
           }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x4 ls = *reinterpret_cast<const f32x4*>(Ls + 32 * u + 8 * q + 4 * half);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(S[4 * q + e] * c - ls[e]);
-          }
+          for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(S[r]);
         }
       }
     };

@@ -509,6 +509,7 @@ typedef struct {
  * lse of the same window and sinks (window >= T: all tokens before).
  *   q (device) [B,Hq,T,D], k (device) [B,Hkv,T,D], lse (device) [B,Hq,T] float
  *   weights (device) [B,Hkv,T] float written (zero behind a sequence's end)
+ * A query or lse that is not a number reaches the weights of the keys that its token sees alone.
  */
 size_t carve_budget_weights_workspace_size(const carve_swa_shape* s);
 carve_status carve_budget_weights(const carve_swa_shape* s, const void* q, const void* k, const float* lse,

@@ -65,3 +65,24 @@ def test_not_finite_keys_beside_the_sinks(D, sinks, at, dt):
             # and what sees one that is not a number is not one itself
             if bad is math.nan:
                 assert torch.isnan(got["o"][0, 2:, max(at), 5].float()).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (50, 3)])
+def test_weights_of_a_query_that_is_not_a_number(window, sinks, dt):
+    """It gives the keys that its token sees weights that are not, and no other key."""
+    T, t = 300, 77
+    q, k, v, _ = inputs(1, 4, 2, T, 64, dt, seed=7)
+
+    def weights(q):
+        _, lse = carve.swa_fwd(q, k, v, window=window or T, sinks=sinks)
+        return carve.budget_weights(q, k, lse, window=window, sinks=sinks)
+
+    want = weights(q)
+    q2 = q.clone()
+    q2[0, 1, t, 9] = math.nan
+    got = weights(q2)
+    s = torch.arange(T, device="cuda")
+    sees = (s <= t) & ((t - s < (window or T)) | (s < sinks))
+    assert torch.isnan(got[0, 0, sees]).all()
+    assert same(got[0, 0, ~sees], want[0, 0, ~sees]) and same(got[0, 1], want[0, 1])
