@@ -42,6 +42,11 @@ __device__ __forceinline__ float diagonal(const f32x16& c) {
   const float other = __shfl_xor(x, 32);
   return ((lane >> 2) & 1) == half ? x : other;
 }
+// p x, and zero where p is zero whatever x is (v_mul_legacy_f32; clang has no builtin for it, so the
+// compiler's intrinsic is named): a key that a token does not see gets no part of a delta or
+// product that is not finite.  A select on ds beside that on p costs 4 % of the training step (634
+// against 608 us), this nothing.
+extern "C" __device__ float weighted(float p, float x) __asm("llvm.amdgcn.fmul.legacy");
 // no visible weight (lse = -inf): every p is exp2(. - inf) = 0
 __device__ __forceinline__ float log2_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
@@ -248,7 +253,7 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
         scores(Ks, Vs, u, see, S, dP);
         // ds rounded to bf16 for its product with k
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[r] *= dP[r] - delta;
+        for (int r = 0; r < 16; ++r) S[r] = weighted(S[r], dP[r] - delta);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           Frag<bf16> F;
@@ -352,7 +357,7 @@ __global__ __launch_bounds__(256, 2) void swa_dkdv_bf16_kernel(SwaArgs a) {
           for (int e = 0; e < 4; ++e) {
             const float p = __builtin_amdgcn_exp2f(S[4 * q + e] * c - ls[e]);
             S[4 * q + e] = see[4 * q + e] ? p : 0.f;
-            dP[4 * q + e] = S[4 * q + e] * (dP[4 * q + e] - de[e]);
+            dP[4 * q + e] = weighted(S[4 * q + e], dP[4 * q + e] - de[e]);
           }
         }
         // p and ds rounded to bf16 for their products with dO and q

@@ -86,3 +86,23 @@ def test_weights_of_a_query_that_is_not_a_number(window, sinks, dt):
     sees = (s <= t) & ((t - s < (window or T)) | (s < sinks))
     assert torch.isnan(got[0, 0, sees]).all()
     assert same(got[0, 0, ~sees], want[0, 0, ~sees]) and same(got[0, 1], want[0, 1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks,t", [(20, 2, 77), (90, 0, 200), (90, 5, 130)])
+def test_gradients_of_an_output_that_is_not_a_number(window, sinks, t, dt):
+    """One token's output row that is not a number (its delta is not): its dq, and dk of the keys
+    that it sees, are not; everything else is what it is without it."""
+    T = 300
+    q, k, v, dO = inputs(1, 4, 2, T, 64, dt, seed=13)
+    o, lse = carve.swa_fwd(q, k, v, window, sinks=sinks)
+    want = carve.swa_bwd(q, k, v, o, lse, dO, window, sinks=sinks)
+    o[0, 1, t, 9] = math.nan
+    got = carve.swa_bwd(q, k, v, o, lse, dO, window, sinks=sinks)
+    s = torch.arange(T, device="cuda")
+    sees = (s <= t) & ((t - s < window) | (s < sinks))
+    assert torch.isnan(got["dq"][0, 1, t].float()).all()
+    got["dq"][0, 1, t] = want["dq"][0, 1, t]
+    assert same(got["dq"], want["dq"]) and same(got["dv"], want["dv"])
+    assert torch.isnan(got["dk"][0, 0, sees].float()).all()
+    assert same(got["dk"][0, 0, ~sees], want["dk"][0, 0, ~sees]) and same(got["dk"][0, 1], want["dk"][0, 1])
