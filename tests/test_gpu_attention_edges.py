@@ -106,3 +106,38 @@ def test_gradients_of_an_output_that_is_not_a_number(window, sinks, t, dt):
     assert same(got["dq"], want["dq"]) and same(got["dv"], want["dv"])
     assert torch.isnan(got["dk"][0, 0, sees].float()).all()
     assert same(got["dk"][0, 0, ~sees], want["dk"][0, 0, ~sees]) and same(got["dk"][0, 1], want["dk"][0, 1])
+
+
+# ------------------------------------------------------------------ variants that only some sizes reach
+def kept(w, n, C, sinks, recent):
+    """Positions that a prompt's cache keeps, from the definition (w without NaN)."""
+    safe = set(range(min(sinks, n))) | set(range(max(0, n - recent), n))
+    rest = sorted((t for t in range(n) if t not in safe), key=lambda t: (-w[t], t))
+    return sorted(list(safe) + rest[:max(0, C - len(safe))])
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("T,C,sinks,recent,lens", [
+    (37, 20, 2, 5, [37, 12]),                      # a key a lane
+    (4096, 700, 4, 64, [4096, 1]), (4097, 700, 4, 64, [4097, 4096]),       # 4 and 12 keys a lane
+    (12288, 900, 4, 64, [12288, 700]), (12289, 900, 4, 64, [12289, 0]),    # 12 and 32
+    (20000, 3001, 4, 50, [20000, 300]),            # far more room than the sequence has tokens
+    (32768, 1500, 0, 1, [32768, 16385]), (32769, 1500, 7, 1, [32769, 900])])     # 32, and read again in every pass
+def test_keep_at_every_length(T, C, sinks, recent, lens, dt, D):
+    B, Hkv = 2, 2
+    k, v = normal((B, Hkv, T, D), dt, 21), normal((B, Hkv, T, D), dt, 22)
+    w = torch.exp(2 * torch.randn(B, Hkv, T, generator=torch.Generator().manual_seed(23)))
+    w[:, 1] = torch.floor(w[:, 1] * 2)             # many equal weights
+    w = w.cuda()
+    cache = carve.budget_cache(B, Hkv, D, C, dtype=DT[dt])
+    for x in cache[:2]:
+        x.fill_(5.0)
+    carve.budget_keep(k, v, w, C, sinks=sinks, recent=recent, lens=ints(lens), cache=cache)
+    for b, n in enumerate(lens):
+        for h in range(Hkv):
+            at = kept(w[b, h].tolist(), n, C, sinks, recent)
+            m = len(at)
+            assert cache[3][b, h].tolist() == at + [-1] * (C - m)
+            assert same(cache[2][b, h, :m], w[b, h, at]) and not cache[2][b, h, m:].any()
+            for x, y in ((cache[0], k), (cache[1], v)):
+                assert same(x[b, h, :m], y[b, h, at]) and (x[b, h, m:] == 5.0).all()
