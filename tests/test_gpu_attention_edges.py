@@ -141,3 +141,70 @@ def test_keep_at_every_length(T, C, sinks, recent, lens, dt, D):
             assert same(cache[2][b, h, :m], w[b, h, at]) and not cache[2][b, h, m:].any()
             for x, y in ((cache[0], k), (cache[1], v)):
                 assert same(x[b, h, :m], y[b, h, at]) and (x[b, h, m:] == 5.0).all()
+
+
+def one_token(B, Hq, Hkv, D, C, sinks, recent, dt, empty, skip, rows=None, seed=31):
+    """One step on a cache made for it, against the rule in float64: slots, rows and positions the
+    same, outputs and weights within their bounds (a weight is a sum of G + 1 terms).  `empty` slots of every
+    key head hold nothing; row `skip` has no token; `rows`: sequences to check."""
+    G = Hq // Hkv
+    gen = torch.Generator().manual_seed(seed)
+    cache = (normal((B, Hkv, C, D), dt, seed + 1), normal((B, Hkv, C, D), dt, seed + 2),
+             torch.exp(torch.randn(B, Hkv, C, generator=gen)).cuda(), torch.empty(B, Hkv, C, dtype=torch.int32, device="cuda"))
+    p = 3 * C
+    # the first and the recent tokens, and positions between in a mixed order
+    middle = sinks + torch.randperm(p - recent - sinks, generator=gen)[:C - sinks - recent + 1]
+    held = torch.cat([torch.arange(sinks), middle, torch.arange(p - recent + 1, p)]).to(torch.int32)
+    cache[3].copy_(held.cuda().expand(B, Hkv, C))
+    holes = (torch.arange(C) * 7 % C < empty) & (held >= sinks) & (held <= p - recent)
+    for x, y in zip(cache, (math.nan, math.nan, math.nan, -1)):           # an empty slot's rows are not read
+        x[:, :, holes.cuda()] = y
+    was = [x.clone() for x in cache]
+    q, k, v = normal((B, Hq, D), dt, seed + 3), normal((B, Hkv, D), dt, seed + 4), normal((B, Hkv, D), dt, seed + 5)
+    pos = [-1 if b == skip else p for b in range(B)]
+    o, slot = carve.budget_decode(q, k, v, cache, ints(pos), sinks=sinks, recent=recent)
+    for b in range(B) if rows is None else rows:
+        if b == skip:
+            assert not o[b].any() and (slot[b] == -1).all()
+            assert all(same(x[b], y[b]) for x, y in zip(cache, was))
+            continue
+        for h in range(Hkv):
+            w, hold = was[2][b, h].tolist(), was[3][b, h].tolist()
+            if holes.any():
+                at = hold.index(-1)
+            else:
+                at = min((j for j in range(C) if sinks <= hold[j] <= p - recent), key=lambda j: (w[j], j))
+            assert int(slot[b, h]) == at
+            kk, vv, pp, ww = was[0][b, h], was[1][b, h], was[3][b, h], was[2][b, h].double()
+            kk[at], vv[at], pp[at], ww[at] = k[b, h], v[b, h], p, 0.0
+            assert same(cache[0][b, h], kk) and same(cache[1][b, h], vv) and torch.equal(cache[3][b, h], pp)
+            live, tol = pp >= 0, torch.zeros(C, dtype=torch.float64, device="cuda")
+            for g in range(h * G, (h + 1) * G):
+                x = ref.rows(q[b, g], kk, vv, live, D ** -0.5)
+                ref.within(o[b, g], x[:2], f"row {b} head {g}")
+                ww, tol = ww + x[2], tol + x[3]
+            ref.within(cache[2][b, h][live], (ww[live], (tol + (G + 1) * ref.F32 * ww.abs())[live]), f"weights {b} {h}")
+            assert same(cache[2][b, h][~live], was[2][b, h][~live])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,C", [
+    (16, 2, 128, 512), (16, 2, 128, 516),          # eight waves: 4,096 scores and the first size past it
+    (16, 2, 64, 511), (16, 2, 64, 513), (16, 2, 64, 514),                  # slots that four do not divide
+    (32, 2, 64, 1021), (4, 4, 64, 4096), (4, 4, 64, 2000)])
+@pytest.mark.parametrize("empty", [0, 5])
+def test_eviction_by_eight_waves(Hq, Hkv, D, C, empty):
+    one_token(2, Hq, Hkv, D, C, 4, 37, "bf16", empty, skip=None)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,D,C", [
+    (8, 2, 128, 2500), (20, 1, 64, 5301), (40, 1, 64, 5302), (64, 1, 128, 2603), (5, 1, 128, 1411)])
+@pytest.mark.parametrize("empty", [0, 300])
+def test_eviction_in_joined_ranges(Hq, Hkv, D, C, empty, dt):
+    one_token(3, Hq, Hkv, D, C, 4, 100, dt, empty, skip=1)
+
+
+@pytest.mark.parametrize("Hq,C", [(4, 500), (8, 2049), (68, 70)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_eviction_in_batches_of_about_300_key_heads(Hq, C, D):
+    one_token(75, Hq, 4, D, C, 4, 20, "bf16", 3, skip=11, rows=(0, 11, 63, 64, 74))
