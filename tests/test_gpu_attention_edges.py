@@ -208,3 +208,39 @@ def test_eviction_in_joined_ranges(Hq, Hkv, D, C, empty, dt):
 @pytest.mark.parametrize("D", [64, 128])
 def test_eviction_in_batches_of_about_300_key_heads(Hq, C, D):
     one_token(75, Hq, 4, D, C, 4, 20, "bf16", 3, skip=11, rows=(0, 11, 63, 64, 74))
+
+
+def test_weight_is_conserved_from_prompt_to_tokens():
+    """A prompt's weights, the cache kept by them and tokens decoded on it: what a step adds to a
+    key head's weights is one for every query head of its group, less what left with the token that gave up
+    its slot; outputs are attention over the cache as the step leaves it; positions are distinct.  The sum
+    of a token's weights is off by their bound (attention_ref.rows), the cache's sum by one
+    rounding of each weight."""
+    B, Hq, Hkv, T, D, C, sinks, recent = 2, 8, 2, 400, 64, 96, 4, 16
+    G = Hq // Hkv
+    q, k, v, _ = inputs(B, Hq, Hkv, T, D, "bf16", seed=41)
+    lens = [400, 60]
+    _, lse = carve.swa_fwd(q, k, v, window=T, lens=ints(lens))
+    w = carve.budget_weights(q, k, lse, lens=ints(lens))
+    cache = carve.budget_keep(k, v, w, C, sinks=sinks, recent=recent, lens=ints(lens))
+    pos = ints(lens)
+    for step in range(50):                         # the second row fills its empty slots, then gives up some
+        was = [x.clone() for x in cache]
+        q1, k1, v1 = (normal((B, h, D), "bf16", 50 + 3 * step + i) for i, h in enumerate((Hq, Hkv, Hkv)))
+        o, slot = carve.budget_decode(q1, k1, v1, cache, pos, sinks=sinks, recent=recent)
+        for b in range(B):
+            for h in range(Hkv):
+                at, live = int(slot[b, h]), cache[3][b, h] >= 0
+                held = cache[3][b, h][live].tolist()
+                assert len(set(held)) == len(held) and held[int(live[:at].sum())] == int(pos[b])
+                assert int(live.sum()) == min(C, int((was[3][b, h] >= 0).sum()) + (int(was[3][b, h, at]) < 0))
+                assert set(range(sinks)) | set(range(int(pos[b]) - recent + 1, int(pos[b]) + 1)) <= set(held)
+                assert same(cache[0][b, h, at], k1[b, h]) and same(cache[1][b, h, at], v1[b, h])
+                tol = ref.F32 * cache[2][b, h].double().abs().sum()
+                for g in range(h * G, (h + 1) * G):
+                    x = ref.rows(q1[b, g], cache[0][b, h], cache[1][b, h], live, D ** -0.5)
+                    ref.within(o[b, g], x[:2], f"step {step} {b} {g}")
+                    tol += x[3].sum() + G * ref.F32
+                grown = cache[2][b, h].double().sum() - was[2][b, h].double().sum() + was[2][b, h, at].double()
+                assert abs(float(grown) - G) <= float(tol), (step, b, h)
+        pos += 1
