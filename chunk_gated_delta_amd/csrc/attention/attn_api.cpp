@@ -166,10 +166,14 @@ carve_status check_budget(const carve_budget_shape* s) {
   return CARVE_OK;
 }
 
-// whether a budget cache's scores of this step stay in LDS
+// Whether a budget cache's scores of this step stay in LDS: where its workgroup of 8 waves is its
+// compute unit's only one anyway, up to one a unit or by the LDS that its rows take at D = 128.  At D = 64
+// two fit, and the scores' 16 KB would keep the second off: 300 key heads of 1,024 slots 26.5 us with
+// them in LDS, 22.0 without, 480 of 512 slots 20.5 and 16.6 (one sequence of four heads 13.4 and 14.9).
 bool near_scores(const carve_budget_shape* s, int n_split, int waves) {
   const long long G = s->Hq / s->Hkv;
-  return s->dtype == CARVE_BF16 && n_split == 1 && waves == 8 && G <= 16 && G * carve::score_row(s->C) <= carve::kNearScores;
+  return s->dtype == CARVE_BF16 && n_split == 1 && waves == 8 && (s->D == 128 || s->B * s->Hkv <= 256) && G <= 16 &&
+         G * carve::score_row(s->C) <= carve::kNearScores;
 }
 
 }  // namespace

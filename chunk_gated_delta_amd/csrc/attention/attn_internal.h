@@ -74,7 +74,7 @@ struct CacheArgs {
   float* score;               // [B*Hkv][G][score_row(C)] scores (log2 domain), budget cache only; null: they stay in LDS
 };
 __host__ __device__ constexpr int score_row(int C) { return (C + 3) & ~3; }
-constexpr int kNearScores = 4096;      // scores of a key head that stay in LDS (bf16, one workgroup of 8 waves)
+constexpr int kNearScores = 4096;      // most scores of a key head that stay in LDS (bf16, one workgroup of 8 waves)
 
 // Rows of k and v copied into a cache.
 struct FillArgs {

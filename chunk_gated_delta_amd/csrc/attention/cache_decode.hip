@@ -319,7 +319,9 @@ struct WaveRows {
   }
 };
 
-template <int D, int NT, int NW, bool BUDGET>
+// NEAR: this step's scores of a cache kept by weight stay in LDS (the caller's rule: where that keeps no
+// second workgroup off the compute unit).
+template <int D, int NT, int NW, bool BUDGET, bool NEAR>
 __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_kernel(CacheArgs a) {
   using Rows = WaveRows<D>;
   constexpr int STEP = 32 * NW;
@@ -327,9 +329,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
   __shared__ unsigned long long red[NW];
   __shared__ float ml[NW][16][2];
   __shared__ float st[16 * NT][2];
-  // a small cache's scores stay in LDS (the workgroup is its compute unit's only one anyway)
-  constexpr bool SMALL = BUDGET && NW == 8;
-  __shared__ __align__(16) float near_score[SMALL ? kNearScores : 4];
+  __shared__ __align__(16) float near_score[NEAR ? kNearScores : 4];
   const int G = a.Hq / a.Hkv;
   const int split = uniform(blockIdx.x % a.n_split), bk = uniform(blockIdx.x / a.n_split), b = uniform(bk / a.Hkv);
   const int lane = lane_id(), wave = wave_uid(), lr = lane & 15, lg = lane >> 4;
@@ -386,7 +386,6 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
       Q[nt][kk] = load_frag(reinterpret_cast<const bf16*>(a.q) + ((size_t)bk * G + g) * D + 32 * kk + 8 * lg);
   }
   const float c = a.scale * kLog2e;
-  const bool near = SMALL && a.score == nullptr;
   f32x4 O[NT][D / 16];
   float m[NT], l[NT];
 #pragma unroll
@@ -439,7 +438,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           if (j0 + 16 * u + 4 * lg < hi) {
-            if (SMALL && near) store4(near_score + row + 16 * u, X[nt][u]);
+            if (NEAR) store4(near_score + row + 16 * u, X[nt][u]);
             else store4(a.score + (size_t)bk * G * score_row(a.C) + row + 16 * u, X[nt][u]);
           }
       }
@@ -522,7 +521,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
   }
   if (BUDGET && a.n_split == 1) {
     __syncthreads();                             // scores of all waves, and st
-    if (SMALL && near) add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], near_score);
+    if (NEAR) add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], near_score);
     else add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], a.score + (size_t)bk * G * score_row(a.C));
   }
 }
@@ -579,10 +578,13 @@ static hipError_t launch_nt(const CacheArgs& a, hipStream_t st) {
   const int units = a.B * a.Hkv, G = a.Hq / a.Hkv;
   hipError_t e;
   if constexpr (sizeof(T) == 2) {
-    if (NT == 1 && a.waves == 8)
-      e = launch_kernel<0>(cache_decode_bf16_kernel<D, 1, 8, BUDGET>, dim3(units * a.n_split), 512, a, st);
+    const dim3 grid(units * a.n_split);
+    if (NT == 1 && a.waves == 8 && BUDGET && !a.score)
+      e = launch_kernel<0>(cache_decode_bf16_kernel<D, 1, 8, BUDGET, BUDGET>, grid, 512, a, st);
+    else if (NT == 1 && a.waves == 8)
+      e = launch_kernel<0>(cache_decode_bf16_kernel<D, 1, 8, BUDGET, false>, grid, 512, a, st);
     else
-      e = launch_kernel<0>(cache_decode_bf16_kernel<D, NT, 4, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);
+      e = launch_kernel<0>(cache_decode_bf16_kernel<D, NT, 4, BUDGET, false>, grid, kDecThreads, a, st);
   } else {
     constexpr size_t lds = std::max(sizeof(T) * 4 * 32 * (D + Pad<T>::v), sizeof(float) * 4 * 16 * (D + 4));
     e = launch_kernel<lds>(cache_decode_f32_kernel<D, NT, BUDGET>, dim3(units * a.n_split), kDecThreads, a, st);

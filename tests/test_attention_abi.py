@@ -129,3 +129,12 @@ def test_binding_refuses(lib):
         carve.swa_fwd(q, k, v, window=(1 << 32) + 4)
     with pytest.raises(ValueError, match="32 bits"):
         carve.budget_keep(k, v, torch.zeros(2, 2, 8), 1 << 33)
+
+
+def test_scores_of_small_caches_stay_near_where_one_workgroup_fits(lib):
+    """A step of a cache kept by weight keeps its scores in LDS (no workspace) unless that would keep a
+    second workgroup off a compute unit: at width 64 from 257 key heads on."""
+    size = lambda **kw: lib.carve_budget_decode_workspace_size(ctypes.byref(budget(Hq=16, Hkv=4, C=512, **kw)))  # noqa: E731
+    assert size(B=64, D=64) == 0 and size(B=64, D=128) == 0
+    assert size(B=75, D=128) == 0
+    assert size(B=75, D=64) >= 75 * 16 * 512 * 4 and size(B=65, D=64) > 0
