@@ -212,9 +212,21 @@ __device__ __forceinline__ int seq_len(const int* lens, int b, int T) {
   return uniform(lens ? min(max(lens[b], 0), T) : T);
 }
 
-// Workgroups are dispatched round-robin over the 8 XCDs, each with its own L2.  Where every
-// unit of work is about as long (a window well inside the sequence), consecutive units, which share
-// keys, go to one XCD; else (units from long to short) an XCD takes every eighth group of units.
+// Workgroups are dispatched round-robin over the 8 XCDs, each with its own L2.  Consecutive units share
+// keys, so they go to one XCD, an eighth of all units each.  Where the window covers half the
+// sequence or more, the units of a key head go from long to short; with few key heads an
+// eighth is then all long or all short, and an XCD takes every eighth group of units instead.
+// Time of every eighth group over an eighth in one, D = 128, window = T, 4 heads on 1:
+//   key heads                1     2     3     4     6     8    16
+//   forward  T 4,096       1.02  1.01  1.13  1.20  1.25  1.44  1.26
+//            T 16,384      0.78  0.74  0.84  0.92  0.95  1.08
+//   backward T 4,096       0.99  0.98  1.04  1.05  1.08  1.22  1.40
+//            T 16,384      0.91  0.89  0.78  1.01  1.02  1.20
+//   weights  T 4,096       0.92  0.89  0.96  1.07  1.15  1.25  1.28
+//            T 16,384      0.61  0.70  0.84  0.93  0.99  1.08
+// (window T / 4, T = 16,384: forward 0.96, 1.02, 0.96, 0.99, 0.98, 1.05.)  So `few` is 3 in the backward;
+// 4 in the weight pass, where less is read again; in the forward 4 where more units than the chip
+// holds at once (three a compute unit) leave a short eighth idle early, else 2.
 __device__ __forceinline__ int xcd_unit(int total) {
   const int id = blockIdx.x, per = total / 8;
   return id < 8 * per ? (id % 8) * per + id / 8 : id;
@@ -223,8 +235,8 @@ __device__ __forceinline__ int xcd_unit_spread(int total, int group) {
   const int id = blockIdx.x, even = total / (8 * group) * (8 * group);
   return id < even ? ((id / 8) / group * 8 + id % 8) * group + (id / 8) % group : id;
 }
-__device__ __forceinline__ int attn_unit(int total, int group, int window, int T) {
-  return window <= T / 2 ? xcd_unit(total) : xcd_unit_spread(total, group);
+__device__ __forceinline__ int attn_unit(int total, int group, int window, int T, int key_heads, int few) {
+  return window >= T / 2 && key_heads <= few ? xcd_unit_spread(total, group) : xcd_unit(total);
 }
 
 // Launch with `lds` bytes of dynamic LDS (above 64 KB the limit has to be raised first).

@@ -24,7 +24,7 @@ struct DqUnit {
 };
 __device__ __forceinline__ DqUnit dq_unit(const SwaArgs& a, int QT) {
   const int G = a.Hq / a.Hkv, NQ = (a.T + QT - 1) / QT;
-  const int unit = attn_unit(a.B * a.Hq * NQ, G, a.window, a.T);
+  const int unit = attn_unit(a.B * a.Hq * NQ, G, a.window, a.T, a.B * a.Hkv, 3);
   DqUnit u;
   u.bk = uniform(unit / (G * NQ));
   u.t0 = uniform((NQ - 1 - (unit / G) % NQ) * QT);
@@ -64,7 +64,7 @@ struct KeyUnit {
 __device__ __forceinline__ KeyUnit key_unit(const SwaArgs& a) {
   constexpr int KT = kSwaKeyTile;
   const int NK = (a.T + KT - 1) / KT, HP = a.n_head_part, G = a.Hq / a.Hkv, per = NK * HP + a.n_sink_tiles * a.n_far;
-  const int unit = attn_unit(a.B * a.Hkv * per, 1, a.window, a.T);
+  const int unit = attn_unit(a.B * a.Hkv * per, 1, a.window, a.T, a.B * a.Hkv, 3);
   KeyUnit u;
   u.bk = uniform(unit / per);
   u.b = uniform(u.bk / a.Hkv);

@@ -18,7 +18,7 @@ struct FwdUnit {
 // tiles of a key head next to each other, late tokens (which see the most keys) first
 __device__ __forceinline__ FwdUnit fwd_unit(const SwaArgs& a, int QT) {
   const int G = a.Hq / a.Hkv, NQ = (a.T + QT - 1) / QT;
-  const int unit = attn_unit(a.B * a.Hq * NQ, G, a.window, a.T);
+  const int total = a.B * a.Hq * NQ, unit = attn_unit(total, G, a.window, a.T, a.B * a.Hkv, total > 3 * 256 ? 4 : 2);
   FwdUnit u;
   u.bk = uniform(unit / (G * NQ));
   u.t0 = uniform((NQ - 1 - (unit / G) % NQ) * QT);

@@ -18,7 +18,7 @@ struct WeightUnit {
 __device__ __forceinline__ WeightUnit weight_unit(const WeightArgs& a) {
   const int NK = (a.T + kWtK - 1) / kWtK;
   const int parts = a.n_chunk * a.n_head;
-  const int unit = attn_unit(a.B * a.Hkv * NK * parts, 1, a.window, a.T);
+  const int unit = attn_unit(a.B * a.Hkv * NK * parts, 1, a.window, a.T, a.B * a.Hkv, 4);
   WeightUnit u;
   u.s0 = uniform(unit % NK) * kWtK;
   u.part = uniform((unit / NK) % parts);
