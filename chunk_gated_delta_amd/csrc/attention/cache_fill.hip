@@ -44,7 +44,7 @@ __device__ __forceinline__ int bits_below(unsigned long long b) {
 // m-th largest weight is found by digits of its ordered bits (11, 11, 10) with a histogram each;
 // then every wave counts what stays of its stretch of tokens, and writes it behind the waves
 // before it.  A wave's stretch is kept in registers as ordered bits, VPT a lane (VPT = 0: sequences
-// past 32 x 1024 tokens, read again in every pass).  The one compute unit's instruction rate
+// past 64 x 1024 tokens, read again in every pass).  The one compute unit's instruction rate
 // bounds it, so tokens that are not candidates carry the key 0, below every weight's, and are told
 // apart by nothing else.  32 key heads of 32,768 tokens: 17 us (55 us with the weights read again in
 // every pass and a scan across the workgroup for every 1,024 of them).  Of it the loads take 2.8 us,
@@ -218,11 +218,16 @@ __global__ __launch_bounds__(256) void fill_rows_kernel(FillArgs a) {
   }
 }
 
+// Weights stay in registers as far as they go, 64 a lane (of its 128 registers 32 spill there); longer
+// prompts read them again for every digit and count.  Both launches of a cache, 32 key heads and 64
+// slots: 32,768 tokens 18 us; 65,536 tokens 30 us in registers and 70 read again.  With 4,096 slots at
+// D = 64: 27, 41 and 90 us; 131,072 tokens 161 us and 262,144 tokens 330 us, read again.
 hipError_t launch_keep_select(const FillArgs& a, hipStream_t st) {
   const dim3 grid(a.B * a.Hkv);
   if (a.T <= 4 * kSelThreads) return launch_kernel<0>(keep_select_kernel<4>, grid, kSelThreads, a, st);
   if (a.T <= 12 * kSelThreads) return launch_kernel<0>(keep_select_kernel<12>, grid, kSelThreads, a, st);
   if (a.T <= 32 * kSelThreads) return launch_kernel<0>(keep_select_kernel<32>, grid, kSelThreads, a, st);
+  if (a.T <= 64 * kSelThreads) return launch_kernel<0>(keep_select_kernel<64>, grid, kSelThreads, a, st);
   return launch_kernel<0>(keep_select_kernel<0>, grid, kSelThreads, a, st);
 }
 

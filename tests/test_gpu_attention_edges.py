@@ -122,7 +122,7 @@ def kept(w, n, C, sinks, recent):
     (4096, 700, 4, 64, [4096, 1]), (4097, 700, 4, 64, [4097, 4096]),       # 4 and 12 keys a lane
     (12288, 900, 4, 64, [12288, 700]), (12289, 900, 4, 64, [12289, 0]),    # 12 and 32
     (20000, 3001, 4, 50, [20000, 300]),            # far more room than the sequence has tokens
-    (32768, 1500, 0, 1, [32768, 16385]), (32769, 1500, 7, 1, [32769, 900])])     # 32, and read again in every pass
+    (32768, 1500, 0, 1, [32768, 16385]), (32769, 1500, 7, 1, [32769, 900])])     # 32 and 64
 def test_keep_at_every_length(T, C, sinks, recent, lens, dt, D):
     B, Hkv = 2, 2
     k, v = normal((B, Hkv, T, D), dt, 21), normal((B, Hkv, T, D), dt, 22)
@@ -244,3 +244,17 @@ def test_weight_is_conserved_from_prompt_to_tokens():
                 grown = cache[2][b, h].double().sum() - was[2][b, h].double().sum() + was[2][b, h, at].double()
                 assert abs(float(grown) - G) <= float(tol), (step, b, h)
         pos += 1
+
+
+@pytest.mark.parametrize("T,C,lens", [(65536, 2000, [65536, 40000]), (65537, 2000, [65537, 65536])])
+def test_keep_of_the_longest_prompts_in_registers(T, C, lens):
+    """The largest register variant and the first length that reads its weights again."""
+    k = normal((2, 1, T, 64), "bf16", 61)
+    w = torch.exp(2 * torch.randn(2, 1, T, generator=torch.Generator().manual_seed(62)))
+    w[1] = torch.floor(w[1] * 2)
+    w = w.cuda()
+    cache = carve.budget_keep(k, k, w, C, sinks=5, recent=100, lens=ints(lens))
+    for b, n in enumerate(lens):
+        at = kept(w[b, 0].tolist(), n, C, 5, 100)
+        assert cache[3][b, 0].tolist() == at
+        assert same(cache[2][b, 0], w[b, 0, at]) and same(cache[0][b, 0], k[b, 0, at]) and same(cache[1][b, 0], k[b, 0, at])
