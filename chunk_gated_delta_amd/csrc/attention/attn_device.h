@@ -8,7 +8,7 @@
 // the same lane values).  Registers 8 x .. 8 x + 7 of C are, rounded, a B operand whose
 // contraction index runs over the rows 16 x + 8 (j / 4) + 4 (l / 32) + j % 4 of C, so
 // weights go from the score tile into the next product without leaving their lane; the
-// other operand of that product is read with its rows in the same order (frag_cols32).
+// other operand of that product is read with its rows in the same order (frag_cols32, col_frag).
 #pragma once
 #include "../carve_device.h"
 #include "attn_internal.h"
@@ -46,18 +46,7 @@ __device__ __forceinline__ Frag<T> frag_rows32(const T* m, int ld, int r0, int k
   return load_frag(m + (r0 + (lane & 31)) * ld + k0 + 8 * (lane >> 5));
 }
 // Columns c0 .. c0 + 31 of a row-major LDS matrix as the 32 rows of an A operand, its 16-deep
-// contraction over rows k0 + 8 (j / 4) + 4 (l / 32) + j % 4.  bf16: two transpose reads
-// (lane s of a 16-lane group points at row s / 4, columns 4 (s % 4) of a 4 x 16 block and
-// receives column s; checked with the layout of lds_frag_tr).
-__device__ __forceinline__ Frag<bf16> frag_cols32(const bf16* m, int ld, int c0, int k0) {
-  const int lane = lane_id(), s = lane & 15, g = lane >> 4;
-  bf16* p = const_cast<bf16*>(m) + (k0 + 4 * (g >> 1) + (s >> 2)) * ld + c0 + 16 * (g & 1) + 4 * (s & 3);
-  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * ld));
-  Frag<bf16> f;
-  f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  return f;
-}
+// contraction over rows k0 + 8 (j / 4) + 4 (l / 32) + j % 4 (fp32; bf16 tiles: SwzTile::col_frag).
 __device__ __forceinline__ Frag<float> frag_cols32(const float* m, int ld, int c0, int k0) {
   const int lane = lane_id();
   const float* p = m + (k0 + 4 * (lane >> 5)) * ld + c0 + (lane & 31);
