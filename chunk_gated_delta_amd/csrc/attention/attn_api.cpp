@@ -68,8 +68,9 @@ int head_parts(const carve_swa_shape* s, long long most) {
 
 // Backward: ranges of the tokens behind the window of the first key tile, so that a tile with
 // sinks is not one workgroup's walk over the whole sequence; at most about 64 (tile, range)
-// pairs a key head, of 256 tokens or more (64 in fp32): short, so that they fill the gaps of the last round.  While key tiles are
-// fewer than the 256 compute units, the heads that share a key head are also taken apart.
+// pairs a key head, of 256 tokens or more (64 in fp32): short, so that they fill the gaps of the
+// last round.  While key tiles are fewer than the 256 compute units, the heads that share a key
+// head are also taken apart.
 struct SwaPlan {
   int window, sinks, n_sink_tiles, n_far, far_len, n_head_part;
   size_t delta_bytes, part_bytes, head_bytes;
@@ -210,7 +211,8 @@ carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* 
       !all_aligned({lens, lse}, 4))
     return CARVE_ERR_INVALID_ARG;
   const SwaPlan p = swa_plan(s);
-  if ((long long)s->B * s->Hq * ((long long)ceil_div(s->T, carve::kSwaKeyTile) * p.n_head_part + (long long)p.n_sink_tiles * p.n_far) > kMaxUnits)
+  const long long per = (long long)ceil_div(s->T, carve::kSwaKeyTile) * p.n_head_part + (long long)p.n_sink_tiles * p.n_far;
+  if ((long long)s->B * s->Hq * per > kMaxUnits)
     return CARVE_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes()) return CARVE_ERR_WORKSPACE;
   carve::SwaArgs a = swa_args(s, q, k, v, lens);

@@ -105,10 +105,11 @@ __device__ __forceinline__ int wave_uid() { return uniform(threadIdx.x >> 6); }
 // ROWS bf16 token rows of width D in LDS, brought there by buffer loads that write LDS directly
 // (16 bytes a lane, 1 KB a wave and instruction, no registers on the way; rows past a sequence's
 // end lie past the buffer's end and read as zero).  Such loads fill LDS in lane order, so rows
-// cannot be padded.  The tile is D / 32 blocks of [ROWS][64 bytes], and the 16-byte piece c of
-// a row's 64 stands at piece c ^ (r / 4) % 4: both read patterns are free of bank conflicts (16
-// rows at one piece for the row operand, 4 rows at 4 neighbouring pieces for the transpose
-// read), and blocks and rows are reached by constant offsets from two addresses a pattern.
+// cannot be padded.  The tile is D / 64 blocks of [ROWS][128 bytes], whole cache lines of a row, and
+// the 16-byte piece c of a row's eight stands at piece c ^ swz(row), swz = bits 1, 3, 2 of the row
+// from the top: neither read pattern has bank conflicts (32 rows at one piece for the row
+// operand, 4 rows at 4 neighbouring pieces a 16 lanes for the transpose read), and blocks and rows
+// are reached by constant offsets from two addresses a pattern.
 // The compiler does not always wait for such loads before the LDS they fill is read: every reader
 // waits itself (wait_loads<N>: all but the N youngest vector memory operations of the wave are
 // done, loads among themselves in order), then, where other waves read, the barrier.

@@ -70,8 +70,9 @@ struct CacheArgs {
   int* slot;                  // [B,Hkv]
   int n_split, split_len;     // slots of a workgroup
   int waves;                  // of a workgroup, 4 or 8 (bf16, at most 16 heads a group)
-  float* part;                // [B*Hkv][n_split][G][2 + D]: max, sum, sum of p v
-  float* score;               // [B*Hkv][G][score_row(C)] scores (log2 domain), budget cache only; null: they stay in LDS
+  float* part;                // [B*Hkv][n_split][G][4 + D]: max, sum, two unused, sum of p v
+  float* score;               // [B*Hkv][G][score_row(C)] scores (log2 domain), budget cache only;
+                              // null: they stay in LDS
 };
 __host__ __device__ constexpr int score_row(int C) { return (C + 3) & ~3; }
 constexpr int kNearScores = 4096;      // most scores of a key head that stay in LDS (bf16, one workgroup of 8 waves)

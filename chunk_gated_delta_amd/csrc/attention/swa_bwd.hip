@@ -9,8 +9,9 @@
 // That is seven products of a visible pair where one pass with shared sums has five.
 // Bound by the products and the vector work beside them, and in the second pass by waits that its
 // 256 registers a wave leave uncovered (matrix cores busy 0.48, vector units 0.37 and 0.30).
-// B4, 16 heads on 4, T = 4,096, window 1,024, 4 sinks, D = 128: dq 214 us, dk/dv 268 us, sinks 5 us
-// (0.61 ms with the forward pass, 0.69 PFLOP/s of 14 D flops a visible pair).
+// B4, 16 heads on 4, T = 4,096, window 1,024, 4 sinks, D = 128: dq 224 us, dk/dv 285 us, sinks 5 us
+// (0.60 to 0.65 ms from card to card with the forward pass, 0.65 to 0.70 PFLOP/s of 14 D flops a visible
+// pair).
 #include <algorithm>
 
 #include "attn_device.h"
@@ -50,10 +51,11 @@ extern "C" __device__ float weighted(float p, float x) __asm("llvm.amdgcn.fmul.l
 // no visible weight (lse = -inf): every p is exp2(. - inf) = 0
 __device__ __forceinline__ float log2_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-// A workgroup of the dk / dv pass: kSwaKeyTile keys of one key head (a lane owns one key), over the tokens t_lo .. t_hi - 1 that see them inside the window and all heads of the
-// group.  The tokens behind the window of a tile that holds sinks see only the sinks: they are cut
-// into n_far ranges with workgroups of their own, whose sums, like the tile's, go to `part`
-// and are added by swa_sink_kernel.
+// A workgroup of the dk / dv pass: kSwaKeyTile keys of one key head (a lane owns one key), over the
+// tokens t_lo .. t_hi - 1 that see them inside the window and all heads of the group.  The tokens
+// behind the window of a tile that holds sinks see only the sinks: they are cut into n_far ranges
+// with workgroups of their own, whose sums, like the tile's, go to `part` and are added by
+// swa_sink_kernel.
 // Where tiles are few (a.n_head_part > 1), the heads of a group are cut into parts as well; then every
 // tile's sums go to `head_part`, and the same kernel adds them.
 struct KeyUnit {
@@ -276,7 +278,9 @@ __global__ __launch_bounds__(256, 2) void swa_dq_bf16_kernel(SwaArgs a) {
 // ------------------------------------------------------------------ bf16: dk, dv
 // Workgroup = 64 keys: waves 0, 1 take 32 keys each with the first 32 tokens of every tile, waves 2,
 // 3 the same keys with the last 32 (their sums are added at the end), so that a unit of work is
-// half as long as with 128 keys (695 -> 374 us at the size above: two rounds of units, not a short third).  Tiles of 64 tokens (q, dO, lse, delta) in two sets of LDS buffers.  Rows at and past t_hi read as
+// half as long as with 128 keys: two rounds of units at the size above, not two and a short third (when
+// they were halved, before the masks were decided ahead of the products, 695 -> 374 us; 285 now).
+// Tiles of 64 tokens (q, dO, lse, delta) in two sets of LDS buffers.  Rows at and past t_hi read as
 // zero throughout: p = 1 there, but dO = 0 and ds = 1 (0 - 0), so they add nothing.
 constexpr int kDkRows = 64;
 

@@ -46,14 +46,14 @@ __device__ __forceinline__ void fwd_store(const SwaArgs& a, const FwdUnit& u, in
 // buffers: the next tile's loads go straight to LDS while this one is worked on, one barrier a
 // tile.  The accumulators are rescaled only when a token's maximum grows by more than 2^8 (weights
 // up to 2^8 keep their relative precision in bf16 and fp32).
-// Bound by the products and the vector work, which together fill the SIMDs' time (counters: matrix
-// cores busy 0.51, vector units 0.49; per 32 x 32 scores at D = 128: 16 products of 32 cycles, 16
+// Its time is that of the products and the vector work one after the other (counters: matrix cores
+// busy 0.54, vector units 0.52; per 32 x 32 scores at D = 128: 16 products of 32 cycles, 16
 // exponentials of 16, some 60 other vector instructions of 4).  32 tokens a wave
 // and 32 keys a tile keep it at 162 registers, three waves a SIMD: tiles of 64 keys (two waves)
-// took 580 us where this takes 531, 64 tokens a wave spilled (1,261 us), and the next tile's
+// took 580 us where this took 531, 64 tokens a wave spilled (1,261 us), and the next tile's
 // scores formed among this one's exponentials in one wave gained nothing over a second wave.
-// B1, 16 heads on 4, T = 32,768, window 2,048, 4 sinks, D = 128: 531 us, 1.00 PFLOP/s of visible
-// pairs (a library product of 8,192^3 reaches 1.20 on the same card).
+// B1, 16 heads on 4, T = 32,768, window 2,048, 4 sinks, D = 128: 530 to 565 us from card to card, 0.94
+// to 1.01 PFLOP/s of visible pairs (a library product of 8,192^3 reaches 1.20).
 constexpr int kFwdQ = 128, kFwdKeys = 32;
 
 template <int D>

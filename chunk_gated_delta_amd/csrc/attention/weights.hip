@@ -44,10 +44,12 @@ __device__ __forceinline__ void weight_store(const WeightArgs& a, const WeightUn
 
 // ------------------------------------------------------------------ bf16
 // Tiles of 64 tokens in two swizzled LDS buffers filled by direct loads; their lse goes through a
-// register one tile ahead.  Little state a wave (k and one sum): four waves a SIMD.  Bound by the
-// vector work and the products, which together fill the time (vector units 0.53, matrix cores 0.43;
-// per 32 x 32 scores at D = 128: 16 exponentials of 16 cycles, 32 vector instructions of 4, 8 products
-// of 32).  B1, 16 heads on 4, T = 8,192: 180 us, 0.77 PFLOP/s of visible pairs.
+// register one tile ahead.  Little state a wave (k and one sum): four waves a SIMD.  Its time is that of
+// the vector work and the products one after the other (vector units 0.58, matrix cores 0.47; per 32 x
+// 32 scores at D = 128: 16 exponentials of 16 cycles, 32 vector instructions of 4, 8 products of
+// 32).  B1, 16 heads on 4, T = 8,192: 174 us, 0.79 PFLOP/s of visible pairs.  With a window, the
+// tiles of sinks walk every token of their range for the sinks alone: T = 32,768, window 2,048, 340 us
+// without sinks and 955 with four.
 constexpr int kWtRows = 64;
 
 template <int D>

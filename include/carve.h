@@ -419,7 +419,9 @@ carve_status carve_decode_step(const carve_shape* s,
  * Query head h reads key head h / (Hq / Hkv).  q, k, v, o and the caches are of one dtype;
  * scores, softmax statistics and sums are float32; the softmax weights (and, backward, the
  * score gradients) are rounded to the dtype as operands of the products with v, k, q and dO.
- * Every result is computed in a fixed order: the same call gives the same bits.
+ * Every result is computed in a fixed order: the same call gives the same bits.  A weight is off
+ * by up to 2^-23 (D + 4) times the largest scale sum_i |q_i k_i| of its row, relative: float32 scores of
+ * 2^20 and more in size say little about the weights, and past 2^30 they may overflow.
  *
  * lens (device) [B] int32 or NULL (= T): tokens of each sequence in a padded batch, taken
  * in [0, T].  Rows at and behind a sequence's end are not read into any result, whatever
