@@ -28,12 +28,17 @@ CFLAGS = [
 ]
 
 
-def source_digest():
-    """Digest of the delta rule's kernel sources (csrc/*, without csrc/attention); counter measurements record it so that a
-    later change to the kernels marks them stale."""
+def source_digest(attention=False):
+    """Digest of the delta rule's kernel sources (csrc/*, without csrc/attention), or of the attention
+    operators' (csrc/attention/* and the device header that they share); measurements
+    record it so that a later change to the kernels marks them stale."""
     import hashlib
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
+    if attention:
+        files = ["carve_device.h"] + [os.path.join("attention", f) for f in sorted(os.listdir(os.path.join(CSRC, "attention")))]
+    else:
+        files = sorted(os.listdir(CSRC))
+    for name in files:
         if name.endswith((".hip", ".h", ".cpp")):
             h.update(name.encode())
             with open(os.path.join(CSRC, name), "rb") as f:

@@ -1,7 +1,7 @@
 """Turn rocprofv3 CSV output into the short text summaries kept with the project.
 
     python -m chunk_gated_delta_amd.prof_summary stats KERNEL_STATS_CSV --title T --command C [--bench-json J]
-                                                   [--trace KERNEL_TRACE_CSV] --out F
+                                                   [--trace KERNEL_TRACE_CSV] [--attention] --out F
     python -m chunk_gated_delta_amd.prof_summary traffic FETCH_CSV WRITE_CSV --copy-mib N --title T
                                                    --command-fetch C1 --command-write C2 --out F
 
@@ -29,6 +29,7 @@ import sys
 
 TRAFFIC_TAG = "<!-- hbm-traffic: "
 MFMA_TAG = "<!-- mfma: "
+DIGEST_LINE = "Kernel sources digest at measurement: "
 
 
 def short_name(mangled):
@@ -78,6 +79,9 @@ def stats(args):
             out.append(f"* {k_}: {1e3 * v_:.1f} us")
         out.append(f"* step: {1e3 * b['ms_per_step']:.1f} us; roofline kernel {b['roofline']['kernel']}, "
                    f"launch {1e3 * b['roofline']['launch_ms']:.1f} us")
+    if args.attention:
+        from chunk_gated_delta_amd.build import source_digest
+        out += ["", DIGEST_LINE + "`" + source_digest(attention=True) + "`"]
     open(args.out, "w").write("\n".join(out) + "\n")
 
 
@@ -118,7 +122,7 @@ def traffic(args):
         out.append(f"| {short_name(name)} `{name[:70]}` | {len(fetch[name])} | {fk:.0f} | {wk:.0f} | "
                    f"{rd / 1e6:.1f} | {wr / 1e6:.1f} | {(rd + wr) / 1e6:.1f} |")
         record["bytes_per_launch"][short_name(name)] = {"read": round(rd), "write": round(wr)}
-    out += ["", "Kernel sources digest at measurement: `" + record["source_digest"] + "`", "",
+    out += ["", DIGEST_LINE + "`" + record["source_digest"] + "`", "",
             TRAFFIC_TAG + json.dumps(record) + " -->"]
     open(args.out, "w").write("\n".join(out) + "\n")
 
@@ -166,7 +170,7 @@ def mfma(args):
         record["kernels"][short_name(name)] = {
             "busy_frac": None if busy is None else round(busy, 4), "bf16_flops": fb, "f32_flops": ff,
             "tflops": None if tf is None else round(tf, 2), "avg_us": None if not ns else round(ns / 1e3, 1)}
-    out += ["", "Kernel sources digest at measurement: `" + record["source_digest"] + "`", "",
+    out += ["", DIGEST_LINE + "`" + record["source_digest"] + "`", "",
             MFMA_TAG + json.dumps(record) + " -->"]
     open(args.out, "w").write("\n".join(out) + "\n")
 
@@ -189,7 +193,7 @@ def lds(args):
         con = mean.get("SQ_LDS_BANK_CONFLICT", 0.0)
         out.append(f"| {short_name(name)} `{name[:70]}` | {len(c.get('SQ_LDS_IDX_ACTIVE', []))} | "
                    f"{mean.get('SQ_INSTS_LDS', 0.0):.0f} | {act:.0f} | {con:.0f} | {con / act if act else 0.0:.2f} |")
-    out += ["", "Kernel sources digest at measurement: `" + source_digest() + "`"]
+    out += ["", DIGEST_LINE + "`" + source_digest() + "`"]
     open(args.out, "w").write("\n".join(out) + "\n")
 
 
@@ -198,6 +202,17 @@ def _read_tagged(path, tag):
         for line in open(path):
             if line.startswith(tag):
                 return json.loads(line[len(tag):].rsplit(" -->", 1)[0])
+    except OSError:
+        return None
+    return None
+
+
+def read_digest(path):
+    """The digest of the kernel sources that a summary was measured on, or None."""
+    try:
+        for line in open(path):
+            if line.startswith(DIGEST_LINE):
+                return line[len(DIGEST_LINE):].strip(" `\n")
     except OSError:
         return None
     return None
@@ -222,6 +237,7 @@ def main(argv=None):
     s.add_argument("--command", required=True)
     s.add_argument("--bench-json")
     s.add_argument("--trace", help="kernel trace CSV of the same run: adds per-launch-shape statistics")
+    s.add_argument("--attention", action="store_true", help="a run of the attention operators: adds their sources' digest")
     s.add_argument("--out", required=True)
     t = sub.add_parser("traffic")
     t.add_argument("fetch_csv")

@@ -33,3 +33,25 @@ def test_stale_digest_gives_no_traffic(tmp_path, monkeypatch):
 def test_source_digest_is_stable():
     assert source_digest() == source_digest()
     assert len(source_digest()) == 16
+
+
+def test_attention_sources_have_a_digest_of_their_own(tmp_path, monkeypatch):
+    """A change to the attention kernels marks their summary stale and leaves the delta rule's."""
+    import shutil
+
+    from chunk_gated_delta_amd import build, prof_summary
+    committed = os.path.join(os.path.dirname(bench.TRAFFIC_SUMMARY), "attention_kernel_stats.md")
+    assert len(prof_summary.read_digest(committed)) == 16
+    assert prof_summary.read_digest(str(tmp_path / "none.md")) is None
+    shutil.copytree(build.CSRC, tmp_path / "csrc")
+    monkeypatch.setattr(build, "CSRC", str(tmp_path / "csrc"))
+    rule, attention = source_digest(), source_digest(attention=True)
+    stats = tmp_path / "stats.csv"
+    stats.write_text("Name,Calls,TotalDurationNs,AverageNs,MinNs,MaxNs\nk,1,10,10,10,10\n")
+    out = tmp_path / "s.md"
+    prof_summary.main(["stats", str(stats), "--title", "t", "--command", "c", "--attention", "--out", str(out)])
+    assert prof_summary.read_digest(str(out)) == attention
+    with open(tmp_path / "csrc" / "attention" / "weights.hip", "a") as f:
+        f.write("// another line\n")
+    assert source_digest() == rule
+    assert source_digest(attention=True) != prof_summary.read_digest(str(out))
