@@ -16,7 +16,8 @@ LIB = os.path.join(HERE, "libcarve.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["carve_api.cpp", "fwd_kernels.hip", "bwd_kernels.hip", "decode_kernels.hip", "content_bwd_kernels.hip",
            "stream_kernels.hip", "width_kernels.hip", "attention/attn_api.cpp", "attention/swa_fwd.hip",
-           "attention/swa_bwd.hip", "attention/weights.hip", "attention/cache_decode.hip", "attention/cache_fill.hip"]
+           "attention/swa_bwd.hip", "attention/weights.hip", "attention/cache_decode.hip", "attention/cache_fill.hip",
+           "attention/mx_rows.hip", "attention/mx_decode.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

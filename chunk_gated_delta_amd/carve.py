@@ -75,6 +75,11 @@ class carve_budget_shape(ctypes.Structure):
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
 
 
+class carve_mx_rows(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("bits", ctypes.c_int)]
+
+
 class carve_profile(ctypes.Structure):
     _fields_ = [("events", ctypes.c_void_p * 9), ("n_events", ctypes.c_int)]
 
@@ -150,8 +155,9 @@ def load_library():
     lib.carve_decode_step.restype = i
     wp = ctypes.POINTER(carve_swa_shape)
     bp = ctypes.POINTER(carve_budget_shape)
+    rp = ctypes.POINTER(carve_mx_rows)
     for name, args in (("carve_swa_bwd", [wp]), ("carve_swa_decode", [wp]), ("carve_budget_weights", [wp]),
-                       ("carve_budget_decode", [bp])):
+                       ("carve_budget_decode", [bp]), ("carve_swa_decode_mx", [wp, i]), ("carve_budget_decode_mx", [bp, i])):
         size = getattr(lib, name + "_workspace_size")
         size.argtypes = args
         size.restype = sz
@@ -161,7 +167,13 @@ def load_library():
                        ("carve_swa_decode", [wp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
                        ("carve_budget_weights", [wp, vp, vp, vp, vp, vp, vp, sz, vp]),
                        ("carve_budget_keep", [bp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
-                       ("carve_budget_decode", [bp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp])):
+                       ("carve_budget_decode", [bp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+                       ("carve_mx_quant", [sz, i, i, vp, vp, vp, vp]),
+                       ("carve_mx_dequant", [sz, i, i, vp, vp, vp, vp]),
+                       ("carve_swa_fill_mx", [wp, vp, vp, vp, rp, vp]),
+                       ("carve_swa_decode_mx", [wp, vp, vp, vp, rp, vp, vp, vp, sz, vp]),
+                       ("carve_budget_keep_mx", [bp, vp, vp, vp, vp, rp, vp, vp, vp]),
+                       ("carve_budget_decode_mx", [bp, vp, vp, vp, rp, vp, vp, vp, vp, vp, vp, sz, vp])):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = i
@@ -702,9 +714,9 @@ def _swa_shape(q, k, ndim, window, sinks, scale):
     return B, Hq, Hkv, T, D, dev, dt, s, ctypes.byref(s)
 
 
-def _workspace(what, s, dev, workspace):
+def _workspace(what, s, dev, workspace, *more):
     """(workspace kept alive, its address, its bytes) for a call that needs one."""
-    need = getattr(load_library(), what)(s)
+    need = getattr(load_library(), what)(s, *more)
     if workspace is not None:
         if workspace.device != dev:
             raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
@@ -854,6 +866,145 @@ def budget_decode(q, k, v, cache, pos, sinks=0, recent=1, scale=None, o=None, sl
         slot = torch.empty(slots, dtype=torch.int32, device=dev)
     workspace, ws, nbytes = _workspace("carve_budget_decode_workspace_size", sp, dev, workspace)
     _call("carve_budget_decode", dev, sp, *ptrs, _fit(o, "o", q.shape, dt, dev),
+          _fit(slot, "slot", slots, torch.int32, dev), ws, nbytes)
+    return o, slot
+
+
+def _bits(bits):
+    if bits not in (4, 8):
+        raise ValueError(f"bits: 4 or 8, got {bits}")
+    return bits
+
+
+def _row_bits(codes, scales):
+    """The bits of a code, from the widths of codes [..., D*bits/8] and scales [..., D/32]."""
+    bits, rest = divmod(codes.shape[-1], 4 * scales.shape[-1]) if scales.dim() and codes.dim() and scales.shape[-1] else (0, 1)
+    if rest or bits not in (4, 8) or codes.shape[:-1] != scales.shape[:-1]:
+        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not rows of 4 or 8 bits")
+    return bits
+
+
+def mx_quant(x, bits=4, codes=None, scales=None):
+    """Rows in codes of 4 or 8 bits: (codes [..., D*bits/8], scales [..., D/32]), uint8.
+
+    x [..., D] (float32 or bfloat16, contiguous, D a multiple of 32).  Every 32 neighbouring values
+    share a power of two, its exponent plus 127 in scales; no value is off by more than half a step of
+    its grid (0 .5 1 1.5 2 3 4 6, or three bits behind the leading one).  32 values with one that is
+    not finite are read back as not a number.  Outputs may be passed preallocated."""
+    if not x.is_cuda:
+        raise ValueError(f"x: expected a GPU tensor, got {x.device}")
+    if x.dim() < 1 or x.shape[-1] % 32:
+        raise ValueError(f"x: the last dimension must be a multiple of 32, got {tuple(x.shape)}")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    rows, D, dev, code = x.shape[:-1], x.shape[-1], x.device, _dtype_code(x)
+    cs, ss = rows + (D * _bits(bits) // 8,), rows + (D // 32,)
+    if codes is None:
+        codes = torch.empty(cs, dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(ss, dtype=torch.uint8, device=dev)
+    _call("carve_mx_quant", dev, x.numel(), code, bits, x.data_ptr(), _fit(codes, "codes", cs, torch.uint8, dev),
+          _fit(scales, "scales", ss, torch.uint8, dev))
+    return codes, scales
+
+
+def mx_dequant(codes, scales, dtype=torch.bfloat16, out=None):
+    """What codes [..., D*bits/8] and scales [..., D/32] stand for: [..., D] in `dtype` (bfloat16 or
+    float32; rows that mx_quant wrote are held exactly by either)."""
+    bits = _row_bits(codes, scales)
+    if not codes.is_cuda:
+        raise ValueError(f"codes: expected a GPU tensor, got {codes.device}")
+    shape, dev = codes.shape[:-1] + (scales.shape[-1] * 32,), codes.device
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    _call("carve_mx_dequant", dev, out.numel(), _dtype_code(out), bits, _fit(codes, "codes", codes.shape, torch.uint8, dev),
+          _fit(scales, "scales", scales.shape, torch.uint8, dev), _fit(out, "out", shape, dtype, dev))
+    return out
+
+
+def _mx_cache(B, Hkv, D, C, bits, device):
+    codes, scales = (B, Hkv, C, D * _bits(bits) // 8), (B, Hkv, C, D // 32)
+    return tuple(torch.zeros(shape, dtype=torch.uint8, device=device) for shape in (codes, scales, codes, scales))
+
+
+def _mx_rows(cache, B, Hkv, C, D, dev):
+    """A carve_mx_rows of (k_codes, k_scales, v_codes, v_scales) that fit."""
+    k_codes, k_scales, v_codes, v_scales = cache
+    bits = _row_bits(k_codes, k_scales)
+    codes, scales, u8 = (B, Hkv, C, D * bits // 8), (B, Hkv, C, D // 32), torch.uint8
+    return carve_mx_rows(_fit(k_codes, "k_codes", codes, u8, dev), _fit(k_scales, "k_scales", scales, u8, dev),
+                         _fit(v_codes, "v_codes", codes, u8, dev), _fit(v_scales, "v_scales", scales, u8, dev), bits)
+
+
+def swa_cache_mx(B, Hkv, D, window, sinks=0, bits=4, device="cuda"):
+    """An empty ring cache of a windowed layer in codes of 4 or 8 bits (mx_quant's): (k_codes, k_scales,
+    v_codes, v_scales), codes [B,Hkv,sinks+window,D*bits/8] and scales [B,Hkv,sinks+window,D/32]."""
+    return _mx_cache(B, Hkv, D, sinks + window, bits, device)
+
+
+def swa_fill_mx(k, v, cache, window, sinks=0, lens=None):
+    """swa_fill into a ring cache as swa_cache_mx makes it: k, v are written in codes and scales."""
+    B, _, Hkv, T, D, dev, dt, s, sp = _swa_shape(k, k, 4, window, sinks, 1.0)
+    rows = _mx_rows(cache, B, Hkv, window + sinks, D, dev)
+    _call("carve_swa_fill_mx", dev, sp, k.data_ptr(), _fit(v, "v", k.shape, dt, dev),
+          _fit_opt(lens, "lens", (B,), torch.int32, dev), ctypes.byref(rows))
+
+
+def swa_decode_mx(q, k, v, cache, pos, window, sinks=0, scale=None, o=None, workspace=None):
+    """swa_decode on a ring cache as swa_cache_mx makes it: the new token's k, v are written in codes and
+    scales first, and attended to as written; o [B,Hq,D] of q's type."""
+    B, Hq, Hkv, _, D, dev, dt, s, sp = _swa_shape(q, k, 3, window, sinks, scale)
+    kv, rows = (B, Hkv, D), _mx_rows(cache, B, Hkv, window + sinks, D, dev)
+    ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev), ctypes.byref(rows),
+            _fit(pos, "pos", (B,), torch.int32, dev))
+    if o is None:
+        o = torch.empty_like(q)
+    workspace, ws, nbytes = _workspace("carve_swa_decode_mx_workspace_size", sp, dev, workspace, rows.bits)
+    _call("carve_swa_decode_mx", dev, sp, *ptrs, _fit(o, "o", q.shape, dt, dev), ws, nbytes)
+    return o
+
+
+def budget_cache_mx(B, Hkv, D, C, bits=4, device="cuda"):
+    """An empty cache of C slots kept by accumulated attention weight, its rows in codes of 4 or 8 bits:
+    (k_codes, k_scales, v_codes, v_scales, cache_w, cache_pos); the last two as budget_cache's."""
+    return _mx_cache(B, Hkv, D, C, bits, device) + (torch.zeros((B, Hkv, C), dtype=torch.float32, device=device),
+                                                    torch.full((B, Hkv, C), -1, dtype=torch.int32, device=device))
+
+
+def budget_keep_mx(k, v, weights, C, sinks=0, recent=1, lens=None, cache=None, bits=4):
+    """budget_keep into a cache as budget_cache_mx makes it: `cache`, overwritten, or a new one."""
+    _whole(C=C, sinks=sinks, recent=recent)
+    B, _, Hkv, T, D, dev, dt = _heads(k, k, 4)
+    s = carve_budget_shape(B, Hkv, Hkv, T, D, C, sinks, recent, 1.0, _dtype_code(k))
+    if cache is None:
+        cache = budget_cache_mx(B, Hkv, D, C, bits, dev)
+    rows, slots = _mx_rows(cache[:4], B, Hkv, C, D, dev), (B, Hkv, C)
+    cache_w, cache_pos = cache[4:]
+    _call("carve_budget_keep_mx", dev, ctypes.byref(s), k.data_ptr(), _fit(v, "v", k.shape, dt, dev),
+          _fit(weights, "weights", (B, Hkv, T), torch.float32, dev), _fit_opt(lens, "lens", (B,), torch.int32, dev),
+          ctypes.byref(rows), _fit(cache_w, "cache_w", slots, torch.float32, dev),
+          _fit(cache_pos, "cache_pos", slots, torch.int32, dev))
+    return tuple(cache)
+
+
+def budget_decode_mx(q, k, v, cache, pos, sinks=0, recent=1, scale=None, o=None, slot=None, workspace=None):
+    """budget_decode on a cache as budget_cache_mx makes it: (o [B,Hq,D], slot [B,Hkv] int32).  The new
+    token's k, v are written in codes and scales first, and attended to as written."""
+    _whole(sinks=sinks, recent=recent)
+    B, Hq, Hkv, _, D, dev, dt = _heads(q, k, 3)
+    C = cache[0].shape[2]
+    s = carve_budget_shape(B, Hq, Hkv, 1, D, C, sinks, recent, D ** -0.5 if scale is None else scale, _dtype_code(q))
+    sp, kv, slots, rows = ctypes.byref(s), (B, Hkv, D), (B, Hkv), _mx_rows(cache[:4], B, Hkv, C, D, dev)
+    cache_w, cache_pos = cache[4:]
+    ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev), ctypes.byref(rows),
+            _fit(cache_w, "cache_w", (B, Hkv, C), torch.float32, dev),
+            _fit(cache_pos, "cache_pos", (B, Hkv, C), torch.int32, dev), _fit(pos, "pos", (B,), torch.int32, dev))
+    if o is None:
+        o = torch.empty_like(q)
+    if slot is None:
+        slot = torch.empty(slots, dtype=torch.int32, device=dev)
+    workspace, ws, nbytes = _workspace("carve_budget_decode_mx_workspace_size", sp, dev, workspace, rows.bits)
+    _call("carve_budget_decode_mx", dev, sp, *ptrs, _fit(o, "o", q.shape, dt, dev),
           _fit(slot, "slot", slots, torch.int32, dev), ws, nbytes)
     return o, slot
 

@@ -156,6 +156,16 @@ size_t part_bytes(int units, int G, int D, int n_split) {
   return n_split > 1 ? up256((size_t)units * n_split * G * (D + 4) * sizeof(float)) : 0;
 }
 
+int mx_row_bytes(int D, int bits) { return D * bits / 8 + D / 32; }
+carve_status check_rows(const carve_mx_rows* r) {
+  if (!r) return CARVE_ERR_INVALID_ARG;
+  if (r->bits != 4 && r->bits != 8) return CARVE_ERR_UNSUPPORTED;
+  if (!all_given({r->k_codes, r->k_scales, r->v_codes, r->v_scales}) || !all_aligned({r->k_codes, r->v_codes}, 16) ||
+      !all_aligned({r->k_scales, r->v_scales}, 4))
+    return CARVE_ERR_INVALID_ARG;
+  return CARVE_OK;
+}
+
 carve_status check_budget(const carve_budget_shape* s) {
   if (!s) return CARVE_ERR_INVALID_ARG;
   if (s->sinks < 0 || s->recent < 1 || s->C < 1) return CARVE_ERR_INVALID_ARG;
@@ -175,6 +185,152 @@ bool near_scores(const carve_budget_shape* s, int n_split, int waves) {
   const long long G = s->Hq / s->Hkv;
   return s->dtype == CARVE_BF16 && n_split == 1 && waves == 8 && (s->D == 128 || s->B * s->Hkv <= 256) && G <= 16 &&
          G * carve::score_row(s->C) <= carve::kNearScores;
+}
+
+// A cache as the calls give it: rows of the call's dtype, or codes and scales.
+struct CacheRows {
+  int bits;                                 // 0: rows of dtype
+  void *k, *v;
+  unsigned char *k_scales, *v_scales;
+};
+CacheRows plain_rows(void* k, void* v) { return {0, k, v, nullptr, nullptr}; }
+CacheRows mx_rows(const carve_mx_rows* r) {
+  return {r->bits, r->k_codes, r->v_codes, (unsigned char*)r->k_scales, (unsigned char*)r->v_scales};
+}
+template <typename Args>
+void set_rows(Args& a, const CacheRows& r) {
+  a.cache_k = r.k;
+  a.cache_v = r.v;
+  a.bits = r.bits;
+  a.k_scales = r.k_scales;
+  a.v_scales = r.v_scales;
+}
+int cache_row_bytes(int D, carve_dtype dtype, int bits) { return bits ? mx_row_bytes(D, bits) : row_bytes(D, dtype); }
+hipError_t fill(const carve::FillArgs& a, hipStream_t st) {
+  return a.bits ? carve::launch_mx_fill(a, st) : carve::launch_fill_rows(a, st);
+}
+hipError_t decode(const carve::CacheArgs& a, hipStream_t st) {
+  return a.bits ? carve::launch_mx_decode(a, st) : carve::launch_cache_decode(a, st);
+}
+
+carve_status swa_fill(const carve_swa_shape* s, const void* k, const void* v, const int* lens, const CacheRows& rows,
+                      void* stream) {
+  carve::FillArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = s->B;
+  a.Hkv = s->Hkv;
+  a.T = s->T;
+  a.D = s->D;
+  a.C = s->window + s->sinks;
+  a.window = s->window;
+  a.sinks = s->sinks;
+  a.dtype = s->dtype == CARVE_BF16;
+  a.k = k;
+  a.v = v;
+  a.lens = lens;
+  set_rows(a, rows);
+  return hip_status(fill(a, (hipStream_t)stream));
+}
+
+size_t swa_decode_bytes(const carve_swa_shape* s, int bits) {
+  if (check_swa(s) != CARVE_OK || s->T != 1 || empty(s) || s->Hq / s->Hkv > kMaxGroup) return 0;
+  int n, len, waves;
+  split_plan(s->B * s->Hkv, s->window + s->sinks, cache_row_bytes(s->D, s->dtype, bits), &n, &len, &waves);
+  const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n);
+  return bytes ? bytes + 256 : 0;
+}
+
+carve_status swa_decode(const carve_swa_shape* s, const void* q, const void* k, const void* v, const CacheRows& rows,
+                        const int* pos, void* o, void* workspace, size_t workspace_bytes, void* stream) {
+  carve::CacheArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = s->B;
+  a.Hq = s->Hq;
+  a.Hkv = s->Hkv;
+  a.D = s->D;
+  a.C = s->window + s->sinks;
+  a.window = s->window;
+  a.sinks = s->sinks;
+  a.dtype = s->dtype == CARVE_BF16;
+  a.scale = s->scale;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  set_rows(a, rows);
+  a.pos = pos;
+  a.o = o;
+  split_plan(a.B * a.Hkv, a.C, cache_row_bytes(s->D, s->dtype, rows.bits), &a.n_split, &a.split_len, &a.waves);
+  const size_t need = swa_decode_bytes(s, rows.bits);
+  if (need && (!workspace || workspace_bytes < need)) return CARVE_ERR_WORKSPACE;
+  a.part = reinterpret_cast<float*>(up256(reinterpret_cast<uintptr_t>(workspace)));
+  return hip_status(decode(a, (hipStream_t)stream));
+}
+
+carve_status budget_keep(const carve_budget_shape* s, const void* k, const void* v, const float* weights, const int* lens,
+                         const CacheRows& rows, float* cache_w, int* cache_pos, void* stream) {
+  carve::FillArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = s->B;
+  a.Hkv = s->Hkv;
+  a.T = s->T;
+  a.D = s->D;
+  a.C = s->C;
+  a.sinks = s->sinks;
+  a.recent = s->recent;
+  a.dtype = s->dtype == CARVE_BF16;
+  a.k = k;
+  a.v = v;
+  a.weights = weights;
+  a.lens = lens;
+  set_rows(a, rows);
+  a.cache_w = cache_w;
+  a.cache_pos = cache_pos;
+  const hipError_t e = carve::launch_keep_select(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_status(e);
+  return hip_status(fill(a, (hipStream_t)stream));
+}
+
+size_t budget_decode_bytes(const carve_budget_shape* s, int bits) {
+  if (check_budget(s) != CARVE_OK || s->T != 1 || s->B == 0 || s->Hq == 0 || s->Hq / s->Hkv > kMaxGroup) return 0;
+  int n, len, waves;
+  split_plan(s->B * s->Hkv, s->C, cache_row_bytes(s->D, s->dtype, bits), &n, &len, &waves);
+  const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n) +
+                       (near_scores(s, n, waves) ? 0 : (size_t)s->B * s->Hq * carve::score_row(s->C) * sizeof(float));
+  return bytes ? bytes + 256 : 0;
+}
+
+carve_status budget_decode(const carve_budget_shape* s, const void* q, const void* k, const void* v,
+                           const CacheRows& rows, float* cache_w, int* cache_pos, const int* pos, void* o, int* slot,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  carve::CacheArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = s->B;
+  a.Hq = s->Hq;
+  a.Hkv = s->Hkv;
+  a.D = s->D;
+  a.C = s->C;
+  a.sinks = s->sinks;
+  a.recent = s->recent;
+  a.dtype = s->dtype == CARVE_BF16;
+  a.scale = s->scale;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  set_rows(a, rows);
+  a.cache_w = cache_w;
+  a.cache_pos = cache_pos;
+  a.pos = pos;
+  a.o = o;
+  a.slot = slot;
+  split_plan(a.B * a.Hkv, a.C, cache_row_bytes(s->D, s->dtype, rows.bits), &a.n_split, &a.split_len, &a.waves);
+  const size_t need = budget_decode_bytes(s, rows.bits);
+  if (need && (!workspace || workspace_bytes < need)) return CARVE_ERR_WORKSPACE;
+  char* ws = reinterpret_cast<char*>(up256(reinterpret_cast<uintptr_t>(workspace)));
+  a.part = reinterpret_cast<float*>(ws);
+  a.score = near_scores(s, a.n_split, a.waves)
+                ? nullptr
+                : reinterpret_cast<float*>(ws + part_bytes(a.B * a.Hkv, a.Hq / a.Hkv, a.D, a.n_split));
+  return hip_status(decode(a, (hipStream_t)stream));
 }
 
 }  // namespace
@@ -234,73 +390,64 @@ carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* 
   return hip_status(carve::launch_swa_bwd(a, (hipStream_t)stream));
 }
 
-carve_status carve_swa_fill(const carve_swa_shape* s, const void* k, const void* v, const int* lens, void* cache_k,
-                            void* cache_v, void* stream) {
+// (a cache in codes: the same checks, of its rows last)
+static carve_status fill_call(const carve_swa_shape* s, const void* k, const void* v, const int* lens) {
   const carve_status st = check_swa(s);
-  if (st != CARVE_OK) return st;
-  if (empty(s)) return CARVE_OK;
-  if (!all_given({k, v, cache_k, cache_v}) || !all_aligned({k, v, cache_k, cache_v}, 16) || !aligned(lens, 4))
-    return CARVE_ERR_INVALID_ARG;
-  carve::FillArgs a;
-  memset(&a, 0, sizeof(a));
-  a.B = s->B;
-  a.Hkv = s->Hkv;
-  a.T = s->T;
-  a.D = s->D;
-  a.C = s->window + s->sinks;
-  a.window = s->window;
-  a.sinks = s->sinks;
-  a.dtype = s->dtype == CARVE_BF16;
-  a.k = k;
-  a.v = v;
-  a.lens = lens;
-  a.cache_k = cache_k;
-  a.cache_v = cache_v;
-  return hip_status(carve::launch_fill_rows(a, (hipStream_t)stream));
+  if (st != CARVE_OK || empty(s)) return st;
+  if (!all_given({k, v}) || !all_aligned({k, v}, 16) || !aligned(lens, 4)) return CARVE_ERR_INVALID_ARG;
+  return CARVE_OK;
 }
-
-size_t carve_swa_decode_workspace_size(const carve_swa_shape* s) {
-  if (check_swa(s) != CARVE_OK || s->T != 1 || empty(s) || s->Hq / s->Hkv > kMaxGroup) return 0;
-  int n, len, waves;
-  split_plan(s->B * s->Hkv, s->window + s->sinks, row_bytes(s->D, s->dtype), &n, &len, &waves);
-  const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n);
-  return bytes ? bytes + 256 : 0;
-}
-
-carve_status carve_swa_decode(const carve_swa_shape* s, const void* q, const void* k, const void* v, void* cache_k,
-                              void* cache_v, const int* pos, void* o, void* workspace, size_t workspace_bytes,
-                              void* stream) {
+static carve_status decode_call(const carve_swa_shape* s, const void* q, const void* k, const void* v, const int* pos,
+                                const void* o) {
   const carve_status st = check_swa(s);
   if (st != CARVE_OK) return st;
   if (s->T != 1) return CARVE_ERR_INVALID_ARG;
   if (empty(s)) return CARVE_OK;
   if (s->Hq / s->Hkv > kMaxGroup) return CARVE_ERR_UNSUPPORTED;
-  if (!all_given({q, k, v, cache_k, cache_v, pos, o}) || !all_aligned({q, k, v, cache_k, cache_v, o}, 16) ||
-      !aligned(pos, 4))
-    return CARVE_ERR_INVALID_ARG;
-  carve::CacheArgs a;
-  memset(&a, 0, sizeof(a));
-  a.B = s->B;
-  a.Hq = s->Hq;
-  a.Hkv = s->Hkv;
-  a.D = s->D;
-  a.C = s->window + s->sinks;
-  a.window = s->window;
-  a.sinks = s->sinks;
-  a.dtype = s->dtype == CARVE_BF16;
-  a.scale = s->scale;
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.cache_k = cache_k;
-  a.cache_v = cache_v;
-  a.pos = pos;
-  a.o = o;
-  split_plan(a.B * a.Hkv, a.C, row_bytes(s->D, s->dtype), &a.n_split, &a.split_len, &a.waves);
-  const size_t need = part_bytes(a.B * a.Hkv, a.Hq / a.Hkv, a.D, a.n_split);
-  if (need && (!workspace || workspace_bytes < need + 256)) return CARVE_ERR_WORKSPACE;
-  a.part = reinterpret_cast<float*>(up256(reinterpret_cast<uintptr_t>(workspace)));
-  return hip_status(carve::launch_cache_decode(a, (hipStream_t)stream));
+  if (!all_given({q, k, v, pos, o}) || !all_aligned({q, k, v, o}, 16) || !aligned(pos, 4)) return CARVE_ERR_INVALID_ARG;
+  return CARVE_OK;
+}
+
+carve_status carve_swa_fill(const carve_swa_shape* s, const void* k, const void* v, const int* lens, void* cache_k,
+                            void* cache_v, void* stream) {
+  const carve_status st = fill_call(s, k, v, lens);
+  if (st != CARVE_OK || empty(s)) return st;
+  if (!all_given({cache_k, cache_v}) || !all_aligned({cache_k, cache_v}, 16)) return CARVE_ERR_INVALID_ARG;
+  return swa_fill(s, k, v, lens, plain_rows(cache_k, cache_v), stream);
+}
+
+carve_status carve_swa_fill_mx(const carve_swa_shape* s, const void* k, const void* v, const int* lens,
+                               const carve_mx_rows* cache, void* stream) {
+  carve_status st = fill_call(s, k, v, lens);
+  if (st != CARVE_OK || empty(s)) return st;
+  st = check_rows(cache);
+  if (st != CARVE_OK) return st;
+  return swa_fill(s, k, v, lens, mx_rows(cache), stream);
+}
+
+size_t carve_swa_decode_workspace_size(const carve_swa_shape* s) { return swa_decode_bytes(s, 0); }
+
+carve_status carve_swa_decode(const carve_swa_shape* s, const void* q, const void* k, const void* v, void* cache_k,
+                              void* cache_v, const int* pos, void* o, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  const carve_status st = decode_call(s, q, k, v, pos, o);
+  if (st != CARVE_OK || empty(s)) return st;
+  if (!all_given({cache_k, cache_v}) || !all_aligned({cache_k, cache_v}, 16)) return CARVE_ERR_INVALID_ARG;
+  return swa_decode(s, q, k, v, plain_rows(cache_k, cache_v), pos, o, workspace, workspace_bytes, stream);
+}
+
+size_t carve_swa_decode_mx_workspace_size(const carve_swa_shape* s, int bits) {
+  return bits == 4 || bits == 8 ? swa_decode_bytes(s, bits) : 0;
+}
+
+carve_status carve_swa_decode_mx(const carve_swa_shape* s, const void* q, const void* k, const void* v,
+                                 const carve_mx_rows* cache, const int* pos, void* o, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  carve_status st = decode_call(s, q, k, v, pos, o);
+  if (st != CARVE_OK || empty(s)) return st;
+  st = check_rows(cache);
+  if (st != CARVE_OK) return st;
+  return swa_decode(s, q, k, v, mx_rows(cache), pos, o, workspace, workspace_bytes, stream);
 }
 
 size_t carve_budget_weights_workspace_size(const carve_swa_shape* s) {
@@ -344,88 +491,96 @@ carve_status carve_budget_weights(const carve_swa_shape* s, const void* q, const
   return hip_status(carve::launch_weights(a, (hipStream_t)stream));
 }
 
-carve_status carve_budget_keep(const carve_budget_shape* s, const void* k, const void* v, const float* weights,
-                               const int* lens, void* cache_k, void* cache_v, float* cache_w, int* cache_pos,
-                               void* stream) {
+static carve_status keep_call(const carve_budget_shape* s, const void* k, const void* v, const float* weights,
+                              const int* lens, const float* cache_w, const int* cache_pos) {
   const carve_status st = check_budget(s);
-  if (st != CARVE_OK) return st;
-  if (s->B == 0 || s->Hkv == 0) return CARVE_OK;
-  if (!all_given({cache_k, cache_v, cache_w, cache_pos}) || (s->T > 0 && !all_given({k, v, weights})) ||
-      !all_aligned({k, v, cache_k, cache_v}, 16) || !all_aligned({weights, lens, cache_w, cache_pos}, 4))
+  if (st != CARVE_OK || s->B == 0 || s->Hkv == 0) return st;
+  if (!all_given({cache_w, cache_pos}) || (s->T > 0 && !all_given({k, v, weights})) || !all_aligned({k, v}, 16) ||
+      !all_aligned({weights, lens, cache_w, cache_pos}, 4))
     return CARVE_ERR_INVALID_ARG;
-  carve::FillArgs a;
-  memset(&a, 0, sizeof(a));
-  a.B = s->B;
-  a.Hkv = s->Hkv;
-  a.T = s->T;
-  a.D = s->D;
-  a.C = s->C;
-  a.sinks = s->sinks;
-  a.recent = s->recent;
-  a.dtype = s->dtype == CARVE_BF16;
-  a.k = k;
-  a.v = v;
-  a.weights = weights;
-  a.lens = lens;
-  a.cache_k = cache_k;
-  a.cache_v = cache_v;
-  a.cache_w = cache_w;
-  a.cache_pos = cache_pos;
-  const hipError_t e = carve::launch_keep_select(a, (hipStream_t)stream);
-  if (e != hipSuccess) return hip_status(e);
-  return hip_status(carve::launch_fill_rows(a, (hipStream_t)stream));
+  return CARVE_OK;
 }
-
-size_t carve_budget_decode_workspace_size(const carve_budget_shape* s) {
-  if (check_budget(s) != CARVE_OK || s->T != 1 || s->B == 0 || s->Hq == 0 || s->Hq / s->Hkv > kMaxGroup) return 0;
-  int n, len, waves;
-  split_plan(s->B * s->Hkv, s->C, row_bytes(s->D, s->dtype), &n, &len, &waves);
-  const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n) +
-                       (near_scores(s, n, waves) ? 0 : (size_t)s->B * s->Hq * carve::score_row(s->C) * sizeof(float));
-  return bytes ? bytes + 256 : 0;
-}
-
-carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, const void* k, const void* v,
-                                 void* cache_k, void* cache_v, float* cache_w, int* cache_pos, const int* pos, void* o,
-                                 int* slot, void* workspace, size_t workspace_bytes, void* stream) {
+static carve_status evict_call(const carve_budget_shape* s, const void* q, const void* k, const void* v,
+                               const float* cache_w, const int* cache_pos, const int* pos, const void* o, const int* slot) {
   const carve_status st = check_budget(s);
   if (st != CARVE_OK) return st;
   if (s->T != 1) return CARVE_ERR_INVALID_ARG;
   if (s->B == 0 || s->Hq == 0) return CARVE_OK;
   if (s->Hq / s->Hkv > kMaxGroup) return CARVE_ERR_UNSUPPORTED;
-  if (!all_given({q, k, v, cache_k, cache_v, cache_w, cache_pos, pos, o, slot}) ||
-      !all_aligned({q, k, v, cache_k, cache_v, o}, 16) || !all_aligned({cache_w, cache_pos, pos, slot}, 4))
+  if (!all_given({q, k, v, cache_w, cache_pos, pos, o, slot}) || !all_aligned({q, k, v, o}, 16) ||
+      !all_aligned({cache_w, cache_pos, pos, slot}, 4))
     return CARVE_ERR_INVALID_ARG;
-  carve::CacheArgs a;
-  memset(&a, 0, sizeof(a));
-  a.B = s->B;
-  a.Hq = s->Hq;
-  a.Hkv = s->Hkv;
-  a.D = s->D;
-  a.C = s->C;
-  a.sinks = s->sinks;
-  a.recent = s->recent;
-  a.dtype = s->dtype == CARVE_BF16;
-  a.scale = s->scale;
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.cache_k = cache_k;
-  a.cache_v = cache_v;
-  a.cache_w = cache_w;
-  a.cache_pos = cache_pos;
-  a.pos = pos;
-  a.o = o;
-  a.slot = slot;
-  split_plan(a.B * a.Hkv, a.C, row_bytes(s->D, s->dtype), &a.n_split, &a.split_len, &a.waves);
-  const size_t need = carve_budget_decode_workspace_size(s);
-  if (need && (!workspace || workspace_bytes < need)) return CARVE_ERR_WORKSPACE;
-  char* ws = reinterpret_cast<char*>(up256(reinterpret_cast<uintptr_t>(workspace)));
-  a.part = reinterpret_cast<float*>(ws);
-  a.score = near_scores(s, a.n_split, a.waves)
-                ? nullptr
-                : reinterpret_cast<float*>(ws + part_bytes(a.B * a.Hkv, a.Hq / a.Hkv, a.D, a.n_split));
-  return hip_status(carve::launch_cache_decode(a, (hipStream_t)stream));
+  return CARVE_OK;
+}
+
+carve_status carve_budget_keep(const carve_budget_shape* s, const void* k, const void* v, const float* weights,
+                               const int* lens, void* cache_k, void* cache_v, float* cache_w, int* cache_pos,
+                               void* stream) {
+  const carve_status st = keep_call(s, k, v, weights, lens, cache_w, cache_pos);
+  if (st != CARVE_OK || s->B == 0 || s->Hkv == 0) return st;
+  if (!all_given({cache_k, cache_v}) || !all_aligned({cache_k, cache_v}, 16)) return CARVE_ERR_INVALID_ARG;
+  return budget_keep(s, k, v, weights, lens, plain_rows(cache_k, cache_v), cache_w, cache_pos, stream);
+}
+
+carve_status carve_budget_keep_mx(const carve_budget_shape* s, const void* k, const void* v, const float* weights,
+                                  const int* lens, const carve_mx_rows* cache, float* cache_w, int* cache_pos,
+                                  void* stream) {
+  carve_status st = keep_call(s, k, v, weights, lens, cache_w, cache_pos);
+  if (st != CARVE_OK || s->B == 0 || s->Hkv == 0) return st;
+  st = check_rows(cache);
+  if (st != CARVE_OK) return st;
+  return budget_keep(s, k, v, weights, lens, mx_rows(cache), cache_w, cache_pos, stream);
+}
+
+size_t carve_budget_decode_workspace_size(const carve_budget_shape* s) { return budget_decode_bytes(s, 0); }
+
+carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, const void* k, const void* v,
+                                 void* cache_k, void* cache_v, float* cache_w, int* cache_pos, const int* pos, void* o,
+                                 int* slot, void* workspace, size_t workspace_bytes, void* stream) {
+  const carve_status st = evict_call(s, q, k, v, cache_w, cache_pos, pos, o, slot);
+  if (st != CARVE_OK || s->B == 0 || s->Hq == 0) return st;
+  if (!all_given({cache_k, cache_v}) || !all_aligned({cache_k, cache_v}, 16)) return CARVE_ERR_INVALID_ARG;
+  return budget_decode(s, q, k, v, plain_rows(cache_k, cache_v), cache_w, cache_pos, pos, o, slot, workspace,
+                       workspace_bytes, stream);
+}
+
+size_t carve_budget_decode_mx_workspace_size(const carve_budget_shape* s, int bits) {
+  return bits == 4 || bits == 8 ? budget_decode_bytes(s, bits) : 0;
+}
+
+carve_status carve_budget_decode_mx(const carve_budget_shape* s, const void* q, const void* k, const void* v,
+                                    const carve_mx_rows* cache, float* cache_w, int* cache_pos, const int* pos, void* o,
+                                    int* slot, void* workspace, size_t workspace_bytes, void* stream) {
+  carve_status st = evict_call(s, q, k, v, cache_w, cache_pos, pos, o, slot);
+  if (st != CARVE_OK || s->B == 0 || s->Hq == 0) return st;
+  st = check_rows(cache);
+  if (st != CARVE_OK) return st;
+  return budget_decode(s, q, k, v, mx_rows(cache), cache_w, cache_pos, pos, o, slot, workspace, workspace_bytes, stream);
+}
+
+// Values in pieces of eight; both directions check alike.
+static carve_status row_call(size_t n, carve_dtype dtype, int bits, const void* x, const void* codes, const void* scales) {
+  if (dtype != CARVE_F32 && dtype != CARVE_BF16) return CARVE_ERR_INVALID_ARG;
+  if (n % 32 != 0) return CARVE_ERR_INVALID_ARG;
+  if (bits != 4 && bits != 8) return CARVE_ERR_UNSUPPORTED;
+  if (n == 0) return CARVE_OK;
+  if (!all_given({x, codes, scales}) || !all_aligned({x, codes}, 16)) return CARVE_ERR_INVALID_ARG;
+  return CARVE_OK;
+}
+
+carve_status carve_mx_quant(size_t n, carve_dtype dtype, int bits, const void* x, void* codes, void* scales, void* stream) {
+  const carve_status st = row_call(n, dtype, bits, x, codes, scales);
+  if (st != CARVE_OK || n == 0) return st;
+  const carve::MxRowArgs a = {n / 8, dtype == CARVE_BF16, bits, const_cast<void*>(x), codes, scales};
+  return hip_status(carve::launch_mx_quant(a, (hipStream_t)stream));
+}
+
+carve_status carve_mx_dequant(size_t n, carve_dtype dtype, int bits, const void* codes, const void* scales, void* x,
+                              void* stream) {
+  const carve_status st = row_call(n, dtype, bits, x, codes, scales);
+  if (st != CARVE_OK || n == 0) return st;
+  const carve::MxRowArgs a = {n / 8, dtype == CARVE_BF16, bits, x, const_cast<void*>(codes), const_cast<void*>(scales)};
+  return hip_status(carve::launch_mx_dequant(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -202,6 +202,15 @@ __device__ __forceinline__ int seq_len(const int* lens, int b, int T) {
   return uniform(lens ? min(max(lens[b], 0), T) : T);
 }
 
+// The token of a prompt whose last is `last` that slot j of a ring cache holds (the last of its residue
+// behind the sinks), -1 if none.
+__device__ __forceinline__ int ring_token(const FillArgs& a, int j, int last) {
+  if (j < a.sinks) return j <= last ? j : -1;
+  const int back = last >= a.sinks ? ((last - a.sinks) % a.window - (j - a.sinks) + a.window) % a.window : last + 1;
+  const int p = last - back;
+  return p < a.sinks ? -1 : p;
+}
+
 // Workgroups are dispatched round-robin over the 8 XCDs, each with its own L2.  Consecutive units share
 // keys, so they go to one XCD, an eighth of all units each.  Where the window covers half the
 // sequence or more, the units of a key head go from long to short; with few key heads an

@@ -63,6 +63,9 @@ struct CacheArgs {
   const void* v;              // [B,Hkv,D]
   void* cache_k;              // [B,Hkv,C,D]
   void* cache_v;
+  int bits;                   // of a code; 0: the cache holds rows of dtype
+  unsigned char* k_scales;    // [B,Hkv,C,D/32], rows of codes only (cache_k, cache_v: [B,Hkv,C,D*bits/8])
+  unsigned char* v_scales;
   float* cache_w;             // [B,Hkv,C]  accumulated weights (null: ring cache)
   int* cache_pos;             // [B,Hkv,C]  position of every slot, < 0 = empty
   const int* pos;             // [B] tokens before this one, < 0 = no token for this sequence
@@ -88,8 +91,20 @@ struct FillArgs {
   const int* lens;
   void* cache_k;
   void* cache_v;
+  int bits;                   // as in CacheArgs
+  unsigned char* k_scales;
+  unsigned char* v_scales;
   float* cache_w;             // null: ring cache
   int* cache_pos;
+};
+
+// Rows written in codes and scales, and read back.
+struct MxRowArgs {
+  size_t pieces;              // of eight values
+  int dtype, bits;
+  void* x;                    // written by the read back
+  void* codes;
+  void* scales;
 };
 
 hipError_t launch_swa_fwd(const SwaArgs& a, hipStream_t st);
@@ -98,5 +113,9 @@ hipError_t launch_weights(const WeightArgs& a, hipStream_t st);
 hipError_t launch_cache_decode(const CacheArgs& a, hipStream_t st);
 hipError_t launch_keep_select(const FillArgs& a, hipStream_t st);
 hipError_t launch_fill_rows(const FillArgs& a, hipStream_t st);
+hipError_t launch_mx_quant(const MxRowArgs& a, hipStream_t st);
+hipError_t launch_mx_dequant(const MxRowArgs& a, hipStream_t st);
+hipError_t launch_mx_fill(const FillArgs& a, hipStream_t st);
+hipError_t launch_mx_decode(const CacheArgs& a, hipStream_t st);
 
 }  // namespace carve

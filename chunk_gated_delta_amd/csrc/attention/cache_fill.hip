@@ -205,13 +205,7 @@ __global__ __launch_bounds__(256) void fill_rows_kernel(FillArgs a) {
       if (i % ROW16 == 0) a.cache_w[row] = p < 0 ? 0.f : a.weights[bk * a.T + p];
     } else {
       const int last = (a.lens ? min(max(a.lens[bk / a.Hkv], 0), a.T) : a.T) - 1;   // (lanes of several rows)
-      if (j < a.sinks) {
-        p = j <= last ? j : -1;
-      } else {
-        const int back = last >= a.sinks ? ((last - a.sinks) % a.window - (j - a.sinks) + a.window) % a.window : last + 1;
-        p = last - back;
-        if (p < a.sinks) p = -1;
-      }
+      p = ring_token(a, j, last);
     }
     if (p < 0) continue;
     const size_t src = (bk * a.T + p) * ROW16 + i % ROW16;

@@ -1,0 +1,154 @@
+// Rows written in codes and scales and read back, and the caches of a prompt written that way.
+//
+// A lane holds eight values, a quarter of a block, so a block's largest value needs two exchanges
+// between neighbouring lanes; loads are 16 bytes a lane (bf16), stores of codes 4 or 8, and lanes of one
+// instruction touch neighbouring bytes.  Bound by the bytes moved.
+#include <algorithm>
+
+#include "mx_device.h"
+
+namespace carve {
+
+constexpr int kRowThreads = 256, kRowUnroll = 4;
+
+// Pieces of eight values; a thread takes kRowUnroll of them, a workgroup's width apart, all loads first.
+template <typename T, int BITS>
+__global__ __launch_bounds__(kRowThreads) void mx_quant_kernel(MxRowArgs a) {
+  const T* x = reinterpret_cast<const T*>(a.x);
+  for (size_t p0 = (size_t)blockIdx.x * kRowUnroll * kRowThreads + threadIdx.x; p0 < a.pieces;
+       p0 += (size_t)gridDim.x * kRowUnroll * kRowThreads) {
+    Frag<T> f[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const size_t p = p0 + u * kRowThreads;
+      f[u] = p < a.pieces ? load_frag(x + 8 * p) : zero_frag(T());
+    }
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const size_t p = p0 + u * kRowThreads;
+      u32 scale;
+      const Eight<BITS> c = write_block<BITS>(f[u], scale);
+      if (p < a.pieces) {
+        reinterpret_cast<Eight<BITS>*>(a.codes)[p] = c;
+        if ((p & 3) == 0) reinterpret_cast<unsigned char*>(a.scales)[p >> 2] = (unsigned char)scale;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void store_eight(bf16* x, const Eight<4>& c, float s) {
+  *reinterpret_cast<Frag<bf16>*>(x) = read_eight<4>(c, s);
+}
+__device__ __forceinline__ void store_eight(bf16* x, const Eight<8>& c, float s) {
+  *reinterpret_cast<Frag<bf16>*>(x) = read_eight<8>(c, s);
+}
+__device__ __forceinline__ void store_eight(float* x, const Eight<4>& c, float s) {
+  const f32x2 p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.w, s, 0), q = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.w, s, 1);
+  const f32x2 r = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.w, s, 2), t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.w, s, 3);
+  *reinterpret_cast<f32x4*>(x) = f32x4{p[0], p[1], q[0], q[1]};
+  *reinterpret_cast<f32x4*>(x + 4) = f32x4{r[0], r[1], t[0], t[1]};
+}
+__device__ __forceinline__ void store_eight(float* x, const Eight<8>& c, float s) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x2 p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.w[h], s, false), q = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.w[h], s, true);
+    *reinterpret_cast<f32x4*>(x + 4 * h) = f32x4{p[0], p[1], q[0], q[1]};
+  }
+}
+template <typename T, int BITS>
+__global__ __launch_bounds__(kRowThreads) void mx_dequant_kernel(MxRowArgs a) {
+  T* x = reinterpret_cast<T*>(a.x);
+  for (size_t p0 = (size_t)blockIdx.x * kRowUnroll * kRowThreads + threadIdx.x; p0 < a.pieces;
+       p0 += (size_t)gridDim.x * kRowUnroll * kRowThreads) {
+    Eight<BITS> c[kRowUnroll];
+    u32 s[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const size_t p = std::min(p0 + u * kRowThreads, a.pieces - 1);
+      c[u] = reinterpret_cast<const Eight<BITS>*>(a.codes)[p];
+      s[u] = reinterpret_cast<const unsigned char*>(a.scales)[p >> 2];
+    }
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const size_t p = p0 + u * kRowThreads;
+      if (p < a.pieces) store_eight(x + 8 * p, c[u], scale_value(s[u]));
+    }
+  }
+}
+
+// The cache of a prompt: blockIdx.y is the key head, a thread takes a piece of eight values of k and of v
+// in kFillUnroll slots.  Which token a slot holds as in fill_rows_kernel; rows of slots that
+// hold none stay as they were.
+constexpr int kFillUnroll = 2;
+template <typename T, int BITS, int D, bool BUDGET>
+__global__ __launch_bounds__(kRowThreads) void mx_fill_kernel(FillArgs a) {
+  constexpr int PR = D / 8, ROWS = kRowThreads / PR;       // pieces of a row, rows of a pass
+  const size_t bk = blockIdx.y;
+  const int piece = threadIdx.x % PR, first = blockIdx.x * ROWS * kFillUnroll + threadIdx.x / PR;
+  const int last = seq_len(a.lens, (int)(bk / a.Hkv), a.T) - 1;
+  int p[kFillUnroll];
+  Frag<T> k[kFillUnroll], v[kFillUnroll];
+#pragma unroll
+  for (int u = 0; u < kFillUnroll; ++u) {
+    const int j = first + u * ROWS;
+    p[u] = -1;
+    if (j < a.C) p[u] = BUDGET ? a.cache_pos[bk * a.C + j] : ring_token(a, j, last);
+    k[u] = v[u] = zero_frag(T());
+    if (p[u] >= 0) {
+      const size_t src = (bk * a.T + p[u]) * D + 8 * piece;
+      k[u] = load_frag(reinterpret_cast<const T*>(a.k) + src);
+      v[u] = load_frag(reinterpret_cast<const T*>(a.v) + src);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kFillUnroll; ++u) {
+    const int j = first + u * ROWS;
+    const size_t row = bk * a.C + j, at = row * PR + piece;
+    u32 ks, vs;
+    const Eight<BITS> kc = write_block<BITS>(k[u], ks), vc = write_block<BITS>(v[u], vs);
+    if (j < a.C && BUDGET && piece == 0) a.cache_w[row] = p[u] < 0 ? 0.f : a.weights[bk * a.T + p[u]];
+    if (p[u] >= 0) {
+      reinterpret_cast<Eight<BITS>*>(a.cache_k)[at] = kc;
+      reinterpret_cast<Eight<BITS>*>(a.cache_v)[at] = vc;
+      if ((piece & 3) == 0) {
+        reinterpret_cast<unsigned char*>(a.k_scales)[at >> 2] = (unsigned char)ks;
+        reinterpret_cast<unsigned char*>(a.v_scales)[at >> 2] = (unsigned char)vs;
+      }
+    }
+  }
+}
+
+template <bool QUANT, int BITS>
+static hipError_t launch_rows(const MxRowArgs& a, hipStream_t st) {
+  const size_t per = kRowUnroll * kRowThreads;
+  const dim3 grid((unsigned)std::min<size_t>((a.pieces + per - 1) / per, 1u << 16));
+  if (QUANT)
+    return a.dtype ? launch_kernel<0>(mx_quant_kernel<bf16, BITS>, grid, kRowThreads, a, st)
+                   : launch_kernel<0>(mx_quant_kernel<float, BITS>, grid, kRowThreads, a, st);
+  return a.dtype ? launch_kernel<0>(mx_dequant_kernel<bf16, BITS>, grid, kRowThreads, a, st)
+                 : launch_kernel<0>(mx_dequant_kernel<float, BITS>, grid, kRowThreads, a, st);
+}
+hipError_t launch_mx_quant(const MxRowArgs& a, hipStream_t st) {
+  return a.bits == 4 ? launch_rows<true, 4>(a, st) : launch_rows<true, 8>(a, st);
+}
+hipError_t launch_mx_dequant(const MxRowArgs& a, hipStream_t st) {
+  return a.bits == 4 ? launch_rows<false, 4>(a, st) : launch_rows<false, 8>(a, st);
+}
+
+template <typename T, int BITS, int D>
+static hipError_t launch_fill(const FillArgs& a, hipStream_t st) {
+  constexpr int rows = kRowThreads / (D / 8) * kFillUnroll;
+  const dim3 grid((a.C + rows - 1) / rows, a.B * a.Hkv);
+  return a.cache_w ? launch_kernel<0>(mx_fill_kernel<T, BITS, D, true>, grid, kRowThreads, a, st)
+                   : launch_kernel<0>(mx_fill_kernel<T, BITS, D, false>, grid, kRowThreads, a, st);
+}
+template <typename T, int BITS>
+static hipError_t launch_fill_d(const FillArgs& a, hipStream_t st) {
+  return a.D == 128 ? launch_fill<T, BITS, 128>(a, st) : launch_fill<T, BITS, 64>(a, st);
+}
+hipError_t launch_mx_fill(const FillArgs& a, hipStream_t st) {
+  if (a.bits == 4) return a.dtype ? launch_fill_d<bf16, 4>(a, st) : launch_fill_d<float, 4>(a, st);
+  return a.dtype ? launch_fill_d<bf16, 8>(a, st) : launch_fill_d<float, 8>(a, st);
+}
+
+}  // namespace carve

@@ -546,6 +546,57 @@ carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, con
                                  int* slot, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Rows in codes: the same caches in 4 or 8 bits a value.  Each block of 32 neighbouring values has a
+ * scale byte s, for 2^(s - 127), and each value a code: of 4 bits, a sign and one of 0 .5 1 1.5 2 3 4 6
+ * (codes 0 .. 7, 8 more with the sign), the value of even index in the low half of its byte; of 8
+ * bits, sign, four exponent and three mantissa bits, 2^-9 to 448 (bias 7, code 127: not a number).
+ *
+ * A block is written with the least scale, of 2^-115 and more, at which its largest size is at most 7
+ * (464) scales: then no value is off by more than half a step, the last code standing for what is past
+ * it.  Values go to the nearest code, of two equally near ones to the even one, and keep their
+ * sign at zero.  (Scales stop at 2^125 and 2^119: sizes beyond 7 (464) of those are held as the last code.)
+ * A block with a value that is infinite or not a number gets scale byte 255 and codes 0 and is
+ * read as not a number.  Any scale byte is read; what those two write is a bf16 exactly, and writing
+ * it again gives the same values.
+ *
+ * carve_mx_quant writes, and carve_mx_dequant reads back, n values (n a multiple of 32; 0: nothing):
+ *   x (device) [n] dtype; codes (device) [n bits / 8] bytes, 16-byte aligned; scales (device) [n / 32]
+ */
+carve_status carve_mx_quant(size_t n, carve_dtype dtype, int bits, const void* x, void* codes, void* scales, void* stream);
+carve_status carve_mx_dequant(size_t n, carve_dtype dtype, int bits, const void* codes, const void* scales, void* x,
+                              void* stream);
+
+/* A cache of such rows (bits 4 or 8): codes [B,Hkv,C,D bits/8], scales [B,Hkv,C,D/32], 4-byte aligned. */
+typedef struct {
+  void* k_codes;       /* (device) */
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  int bits;
+} carve_mx_rows;
+
+/*
+ * carve_swa_fill, carve_swa_decode, carve_budget_keep and carve_budget_decode on such caches; all other
+ * arguments as there (q, k, v and o of shape->dtype).  k and v of the tokens are rounded as above
+ * when they are written, the new token's too: it sees itself as the next ones will.  What a cache holds
+ * enters the products exactly; q and, with float32, the weights are not rounded either (with bf16
+ * the weights are, as in carve_swa_decode).
+ */
+carve_status carve_swa_fill_mx(const carve_swa_shape* s, const void* k, const void* v, const int* lens,
+                               const carve_mx_rows* cache, void* stream);
+size_t carve_swa_decode_mx_workspace_size(const carve_swa_shape* s, int bits);
+carve_status carve_swa_decode_mx(const carve_swa_shape* s, const void* q, const void* k, const void* v,
+                                 const carve_mx_rows* cache, const int* pos, void* o, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+carve_status carve_budget_keep_mx(const carve_budget_shape* s, const void* k, const void* v, const float* weights,
+                                  const int* lens, const carve_mx_rows* cache, float* cache_w, int* cache_pos,
+                                  void* stream);
+size_t carve_budget_decode_mx_workspace_size(const carve_budget_shape* s, int bits);
+carve_status carve_budget_decode_mx(const carve_budget_shape* s, const void* q, const void* k, const void* v,
+                                    const carve_mx_rows* cache, float* cache_w, int* cache_pos, const int* pos, void* o,
+                                    int* slot, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Measurement helper, not part of the CARVE operation: copies `bytes` from src to dst
  * (both device pointers, 16-byte aligned, non-overlapping; bytes a multiple of 16) with a
  * plain streaming kernel (each byte read once and written once by 16-byte vector accesses,
