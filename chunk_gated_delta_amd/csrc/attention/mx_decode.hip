@@ -42,7 +42,7 @@ __device__ __forceinline__ void bf16_parts(const float (&x)[8], Frag<bf16> (&f)[
 // 32 slots of a wave as they come from memory.  Lane (lr, lg): elements lg D / 4 .. of the keys of slots lr
 // and 16 + lr; elements lr D / 16 .. of the values of slots 16 u + 4 lg + i, i < 4; scales of all
 // blocks of these slots.
-template <int BITS, int D, bool BUDGET>
+template <int BITS, int D>
 struct MxStep {
   static constexpr int RB = D * BITS / 8, SB = D / 32;         // bytes of a row, of its scales
   static constexpr int KW = RB / 16, VB = RB / 16, VW = VB < 4 ? 1 : VB / 4;   // words a lane and key; bytes, words a slot
@@ -52,58 +52,53 @@ struct MxStep {
   static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const void* base, size_t j0, int n, int row_bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((char*)base + j0 * row_bytes, 0, n * row_bytes, 0x00020000);
   }
+  // (constant parts of an offset are the scalar operand: one address register for all slots)
   template <int N>
-  static __device__ __forceinline__ void words(__amdgpu_buffer_rsrc_t r, int off, u32* w) {
+  static __device__ __forceinline__ void words(__amdgpu_buffer_rsrc_t r, int off, int more, u32* w) {
     if constexpr (N == 1) {
-      w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, more, 0);
     } else if constexpr (N == 2) {
-      const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+      const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, off, more, 0);
       w[0] = x[0];
       w[1] = x[1];
     } else {
 #pragma unroll
       for (int h = 0; h < N / 4; ++h) {
-        const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(r, off + 16 * h, 0, 0);
+        const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(r, off, more + 16 * h, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[4 * h + i] = x[i];
       }
     }
   }
-  // offset of a slot's bytes, or past the end where the slot is not live
-  static __device__ __forceinline__ int at(unsigned live, int slot, int off) {
-    return BUDGET && !((live >> slot) & 1) ? 0x40000000 : off;
-  }
-  __device__ __forceinline__ void load_k(const void* codes, const void* scales, size_t j0, int n, unsigned live) {
+  __device__ __forceinline__ void load_k(const void* codes, const void* scales, size_t j0, int n) {
     const int lane = lane_id(), lr = lane & 15, lg = lane >> 4;
     const auto c = rows(codes, j0, n, RB), s = rows(scales, j0, n, SB);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int slot = 16 * u + lr;
-      words<KW>(c, at(live, slot, slot * RB + lg * KW * 4), k[u]);
-      ks[u] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(s, at(live, slot, slot * SB + lg * SB / 4), 0, 0);
+      words<KW>(c, lr * RB + lg * KW * 4, 16 * u * RB, k[u]);
+      ks[u] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(s, lr * SB + lg * SB / 4, 16 * u * SB, 0);
     }
   }
-  // (the scales of a slot without a token are read, and not used)
-  __device__ __forceinline__ void load_v(const void* codes, const void* scales, size_t j0, int n, unsigned live) {
+  __device__ __forceinline__ void load_v(const void* codes, const void* scales, size_t j0, int n) {
     const int lane = lane_id(), lr = lane & 15, lg = lane >> 4;
     const auto c = rows(codes, j0, n, RB), s = rows(scales, j0, n, SB);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int slot = 16 * (j >> 2) + 4 * lg + (j & 3), off = at(live, slot, slot * RB + lr * VB);
-      if constexpr (VB == 2) v[j][0] = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(c, off, 0, 0);
-      else words<VW>(c, off, v[j]);
+      const int more = 16 * (j >> 2) + (j & 3), off = 4 * lg * RB + lr * VB;
+      if constexpr (VB == 2) v[j][0] = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(c, off, more * RB, 0);
+      else words<VW>(c, off, more * RB, v[j]);
     }
     if (n == 32) {                               // four slots at a time, where all four are there
 #pragma unroll
-      for (int u = 0; u < 2; ++u) words<SB>(s, (16 * u + 4 * lg) * SB, vs[u]);
+      for (int u = 0; u < 2; ++u) words<SB>(s, 4 * lg * SB, 16 * u * SB, vs[u]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int u = j >> 2, i = j & 3, off = (16 * u + 4 * lg + i) * SB;
+        const int u = j >> 2, i = j & 3, more = (16 * u + i) * SB;
         if constexpr (SB == 4) {
-          vs[u][i] = __builtin_amdgcn_raw_buffer_load_b32(s, off, 0, 0);
+          vs[u][i] = __builtin_amdgcn_raw_buffer_load_b32(s, 4 * lg * SB, more, 0);
         } else {
-          const u32 x = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(s, off, 0, 0);
+          const u32 x = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(s, 4 * lg * SB, more, 0);
           vs[u][i >> 1] = (i & 1) ? vs[u][i >> 1] | x << 16 : x;
         }
       }
@@ -118,9 +113,19 @@ struct MxStep {
   }
 };
 
+// the largest x of the four lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ __forceinline__ float group_max(float x) {
+  const u32 u = __builtin_bit_cast(u32, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const float y = fmaxf(__builtin_bit_cast(float, (u32)r[0]), __builtin_bit_cast(float, (u32)r[1]));
+  const u32 w = __builtin_bit_cast(u32, y);
+  const auto s = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return fmaxf(__builtin_bit_cast(float, (u32)s[0]), __builtin_bit_cast(float, (u32)s[1]));
+}
+
 template <typename T, int BITS, int D, int NT, int NW, bool BUDGET, bool NEAR>
 __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(CacheArgs a) {
-  using Step = MxStep<BITS, D, BUDGET>;
+  using Step = MxStep<BITS, D>;
   constexpr int STEP = 32 * NW, N = sizeof(T) == 2 ? 1 : 3, KK = D / 32, DT = D / 16;
   constexpr int RB = Step::RB, SB = Step::SB;
   __shared__ __align__(16) float mg[NW * 16 * D];
@@ -156,13 +161,31 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
     const int j = j0 + (lane & 31);
     return (unsigned)__ballot(j < hi && (!BUDGET || pos >= 0));
   };
-  auto rows_from = [&](int j0) { return max(0, min(hi - j0, 32)); };
+  // (q before the rows: loads arrive in order, so what waits for rows has q)
+  Frag<bf16> Q[NT][KK][N];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int g = min(16 * nt + lr, G - 1);
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      const Frag<T> f = load_frag(reinterpret_cast<const T*>(a.q) + ((size_t)bk * G + g) * D + lg * (D / 4) + 8 * kk);
+      if constexpr (N == 1) {
+        Q[nt][kk][0] = f;
+      } else {
+        float y[8];
+        to_floats(f, y);
+        bf16_parts<N>(y, Q[nt][kk]);
+      }
+    }
+  }
+  // rows of the 32 to read: up to the last that holds a token
+  auto rows_of = [&](unsigned live) { return uniform(32 - __clz((int)live)); };
   Step x;
   unsigned live = 0;
   if (first < hi) {
     live = live_of(first, position(first));
-    x.load_k(ck, sk, first, rows_from(first), live);
-    x.load_v(cv, sv, first, rows_from(first), live);
+    x.load_k(ck, sk, first, rows_of(live));
+    x.load_v(cv, sv, first, rows_of(live));
   }
   const int at = uniform(BUDGET ? pick_slot<NW>(a, bk, p, red) : ring_slot(a, p));
   if (BUDGET && split == 0 && threadIdx.x == 0) a.slot[bk] = at;
@@ -182,22 +205,6 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // written and read by this wave alone
     __builtin_amdgcn_wave_barrier();
-  }
-  Frag<bf16> Q[NT][KK][N];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int g = min(16 * nt + lr, G - 1);
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      const Frag<T> f = load_frag(reinterpret_cast<const T*>(a.q) + ((size_t)bk * G + g) * D + lg * (D / 4) + 8 * kk);
-      if constexpr (N == 1) {
-        Q[nt][kk][0] = f;
-      } else {
-        float y[8];
-        to_floats(f, y);
-        bf16_parts<N>(y, Q[nt][kk]);
-      }
-    }
   }
   const float c = a.scale * kLog2e;
   f32x4 O[NT][DT];
@@ -246,20 +253,20 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    x.load_k(ck, sk, (size_t)j0 + STEP, rows_from(j0 + STEP), next);   // (behind the last slots: no rows)
+    x.load_k(ck, sk, (size_t)j0 + STEP, rows_of(next));   // (behind the last slots: no rows)
     Frag<bf16> P[NT][N];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mx = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) X[nt][u] *= c;
+      if (live != ~0u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 16 * u + 4 * lg + i;
-          const float y = ((live >> r) & 1) ? X[nt][u][i] * c : -INFINITY;
-          X[nt][u][i] = y;
-          mx = fmaxf(mx, y);
-        }
+        for (int j = 0; j < 8; ++j)
+          if (!((live >> (16 * (j >> 2) + 4 * lg + (j & 3))) & 1)) X[nt][j >> 2][j & 3] = -INFINITY;
+      }
+      float mx = X[nt][0][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) mx = fmaxf(mx, X[nt][j >> 2][j & 3]);
       // four slots of a head at a time (past the last slot into the row's padding)
       if (BUDGET && 16 * nt + lr < G) {
         const size_t row = (size_t)(16 * nt + lr) * score_row(a.C) + j0 + 4 * lg;
@@ -270,8 +277,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
             else store4(a.score + (size_t)bk * G * score_row(a.C) + row + 16 * u, X[nt][u]);
           }
       }
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      mx = group_max(mx);
       if (__any(mx > m[nt] + 8.f)) {             // rescale only when a maximum grows by 2^8
         const float mn = fmaxf(m[nt], mx), alpha = __builtin_amdgcn_exp2f(m[nt] - mn);
         m[nt] = mn;
@@ -307,9 +313,15 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
     // V^T operands, two rows d of it at a time: two values of each of the eight slots, paired up by slot
     float vscale[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const u32 s = x.v_scale(j);
-      vscale[j] = BUDGET && !((live >> (16 * (j >> 2) + 4 * lg + (j & 3))) & 1) ? 0.f : scale_value(s);
+    for (int j = 0; j < 8; ++j) vscale[j] = scale_value(x.v_scale(j));
+    if (BUDGET && live != ~0u) {                 // what stands in empty slots reaches nothing
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!((live >> (16 * (j >> 2) + 4 * lg + (j & 3))) & 1)) {
+          vscale[j] = 0.f;
+#pragma unroll
+          for (int w = 0; w < Step::VW; ++w) x.v[j][w] = 0;
+        }
     }
     auto pair_of_rows = [&](auto xx) {
       constexpr int X2 = decltype(xx)::value, W = BITS == 4 ? X2 / 4 : X2 / 2, S = BITS == 4 ? X2 % 4 : X2 % 2;
@@ -338,7 +350,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
       pair_of_rows(std::integral_constant<int, 3>());
     }
     __builtin_amdgcn_sched_barrier(0);
-    x.load_v(cv, sv, (size_t)j0 + STEP, rows_from(j0 + STEP), next);
+    x.load_v(cv, sv, (size_t)j0 + STEP, rows_of(next));
     live = next;
   }
   // join the waves, 16 heads at a time (4-float pieces of a row swizzled by the head); row 4 lg + i of tile
