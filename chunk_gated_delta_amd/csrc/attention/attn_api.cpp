@@ -152,11 +152,28 @@ void split_plan(int units, int C, int row_bytes, int* n_split, int* split_len, i
   *split_len = ceil_div(ceil_div(C, n), 128) * 128;
   *n_split = ceil_div(C, *split_len);
 }
+// The same for rows of codes, which are read sooner than a step of 128 slots is computed.  Up to 256 key heads one
+// workgroup of 8 waves each, above of 4 (400 of 512 slots with weights: 13.8 against 18.6 us, without 9.8
+// against 10.2; 256: 11.1 against 10.4, 7.6 against 7.4).  Few key heads are cut into ranges where that saves more than the
+// launch that joins them: 4 key heads of 1,028 / 2,052 / 4,100 slots 8.6 / 12.2 / 19.7 us in one, 7.7 / 8.2 / 8.9
+// in ranges, with weights 12.2 / 17.0 / 26.9 and 10.9 / 11.7 / 13.1; 32 of 2,052 slots 12.5 and 10.1;
+// 128 of 2,052 / 4,100 / 8,196 slots 13.8 / 22 / 39 and 14.7 / 19.5 / 34, with weights 20 / 32 / 55
+// and 23 / 34 / 55; 256 not at any length.  (A caller that launches each step anew pays the second launch's 4 us too.)
+void mx_split_plan(int units, int C, bool weights, int* n_split, int* split_len, int* waves) {
+  const int most = units <= 64 ? 1536 : weights ? 8192 : 3072;      // slots of one workgroup
+  int n = 1;
+  *waves = units <= 256 ? 8 : 4;
+  if (units < 256 && C > most) {
+    n = std::min({ceil_div(512, units), ceil_div(C, 128), 64});
+    *waves = 4;
+  }
+  *split_len = ceil_div(ceil_div(C, n), 128) * 128;
+  *n_split = ceil_div(C, *split_len);
+}
 size_t part_bytes(int units, int G, int D, int n_split) {
   return n_split > 1 ? up256((size_t)units * n_split * G * (D + 4) * sizeof(float)) : 0;
 }
 
-int mx_row_bytes(int D, int bits) { return D * bits / 8 + D / 32; }
 carve_status check_rows(const carve_mx_rows* r) {
   if (!r) return CARVE_ERR_INVALID_ARG;
   if (r->bits != 4 && r->bits != 8) return CARVE_ERR_UNSUPPORTED;
@@ -181,9 +198,10 @@ carve_status check_budget(const carve_budget_shape* s) {
 // compute unit's only one anyway, up to one a unit or by the LDS that its rows take at D = 128.  At D = 64
 // two fit, and the scores' 16 KB would keep the second off: 300 key heads of 1,024 slots 26.5 us with
 // them in LDS, 22.0 without, 480 of 512 slots 20.5 and 16.6 (one sequence of four heads 13.4 and 14.9).
-bool near_scores(const carve_budget_shape* s, int n_split, int waves) {
+// (Rows of codes have 8 waves up to 256 key heads only, in either type.)
+bool near_scores(const carve_budget_shape* s, int bits, int n_split, int waves) {
   const long long G = s->Hq / s->Hkv;
-  return s->dtype == CARVE_BF16 && n_split == 1 && waves == 8 && (s->D == 128 || s->B * s->Hkv <= 256) && G <= 16 &&
+  return (bits || s->dtype == CARVE_BF16) && n_split == 1 && waves == 8 && (s->D == 128 || s->B * s->Hkv <= 256) && G <= 16 &&
          G * carve::score_row(s->C) <= carve::kNearScores;
 }
 
@@ -205,7 +223,10 @@ void set_rows(Args& a, const CacheRows& r) {
   a.k_scales = r.k_scales;
   a.v_scales = r.v_scales;
 }
-int cache_row_bytes(int D, carve_dtype dtype, int bits) { return bits ? mx_row_bytes(D, bits) : row_bytes(D, dtype); }
+void plan(int units, int C, int D, carve_dtype dtype, int bits, bool weights, int* n_split, int* split_len, int* waves) {
+  if (bits) mx_split_plan(units, C, weights, n_split, split_len, waves);
+  else split_plan(units, C, row_bytes(D, dtype), n_split, split_len, waves);
+}
 hipError_t fill(const carve::FillArgs& a, hipStream_t st) {
   return a.bits ? carve::launch_mx_fill(a, st) : carve::launch_fill_rows(a, st);
 }
@@ -235,7 +256,7 @@ carve_status swa_fill(const carve_swa_shape* s, const void* k, const void* v, co
 size_t swa_decode_bytes(const carve_swa_shape* s, int bits) {
   if (check_swa(s) != CARVE_OK || s->T != 1 || empty(s) || s->Hq / s->Hkv > kMaxGroup) return 0;
   int n, len, waves;
-  split_plan(s->B * s->Hkv, s->window + s->sinks, cache_row_bytes(s->D, s->dtype, bits), &n, &len, &waves);
+  plan(s->B * s->Hkv, s->window + s->sinks, s->D, s->dtype, bits, false, &n, &len, &waves);
   const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n);
   return bytes ? bytes + 256 : 0;
 }
@@ -259,7 +280,7 @@ carve_status swa_decode(const carve_swa_shape* s, const void* q, const void* k, 
   set_rows(a, rows);
   a.pos = pos;
   a.o = o;
-  split_plan(a.B * a.Hkv, a.C, cache_row_bytes(s->D, s->dtype, rows.bits), &a.n_split, &a.split_len, &a.waves);
+  plan(a.B * a.Hkv, a.C, a.D, s->dtype, rows.bits, false, &a.n_split, &a.split_len, &a.waves);
   const size_t need = swa_decode_bytes(s, rows.bits);
   if (need && (!workspace || workspace_bytes < need)) return CARVE_ERR_WORKSPACE;
   a.part = reinterpret_cast<float*>(up256(reinterpret_cast<uintptr_t>(workspace)));
@@ -293,9 +314,9 @@ carve_status budget_keep(const carve_budget_shape* s, const void* k, const void*
 size_t budget_decode_bytes(const carve_budget_shape* s, int bits) {
   if (check_budget(s) != CARVE_OK || s->T != 1 || s->B == 0 || s->Hq == 0 || s->Hq / s->Hkv > kMaxGroup) return 0;
   int n, len, waves;
-  split_plan(s->B * s->Hkv, s->C, cache_row_bytes(s->D, s->dtype, bits), &n, &len, &waves);
+  plan(s->B * s->Hkv, s->C, s->D, s->dtype, bits, true, &n, &len, &waves);
   const size_t bytes = part_bytes(s->B * s->Hkv, s->Hq / s->Hkv, s->D, n) +
-                       (near_scores(s, n, waves) ? 0 : (size_t)s->B * s->Hq * carve::score_row(s->C) * sizeof(float));
+                       (near_scores(s, bits, n, waves) ? 0 : (size_t)s->B * s->Hq * carve::score_row(s->C) * sizeof(float));
   return bytes ? bytes + 256 : 0;
 }
 
@@ -322,12 +343,12 @@ carve_status budget_decode(const carve_budget_shape* s, const void* q, const voi
   a.pos = pos;
   a.o = o;
   a.slot = slot;
-  split_plan(a.B * a.Hkv, a.C, cache_row_bytes(s->D, s->dtype, rows.bits), &a.n_split, &a.split_len, &a.waves);
+  plan(a.B * a.Hkv, a.C, a.D, s->dtype, rows.bits, true, &a.n_split, &a.split_len, &a.waves);
   const size_t need = budget_decode_bytes(s, rows.bits);
   if (need && (!workspace || workspace_bytes < need)) return CARVE_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(up256(reinterpret_cast<uintptr_t>(workspace)));
   a.part = reinterpret_cast<float*>(ws);
-  a.score = near_scores(s, a.n_split, a.waves)
+  a.score = near_scores(s, rows.bits, a.n_split, a.waves)
                 ? nullptr
                 : reinterpret_cast<float*>(ws + part_bytes(a.B * a.Hkv, a.Hq / a.Hkv, a.D, a.n_split));
   return hip_status(decode(a, (hipStream_t)stream));

@@ -19,12 +19,24 @@ __device__ __forceinline__ int pick_slot(const CacheArgs& a, int bk, int p, unsi
   const float* w = a.cache_w + (size_t)bk * a.C;
   const int* held = a.cache_pos + (size_t)bk * a.C;
   unsigned long long best = ~0ull;
-  for (int j = threadIdx.x; j < a.C; j += 64 * NW) {
-    const int h = held[j];
-    const int cls = h == p ? 0 : h < 0 ? 1 : (h >= a.sinks && h <= p - a.recent) ? 2 : 3;
-    const unsigned o = cls < 2 ? 0u : weight_order(w[j]);
-    const unsigned long long key = ((unsigned long long)cls << 62) | ((unsigned long long)o << 30) | (unsigned)j;
-    best = key < best ? key : best;
+  constexpr int U = 4;                           // slots a thread takes at a time, their loads in flight together
+  for (int j0 = threadIdx.x; j0 < a.C; j0 += U * 64 * NW) {
+    int h[U];
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = min(j0 + u * 64 * NW, a.C - 1);        // (the last slot again, behind it)
+      h[u] = held[j];
+      x[u] = w[j];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = min(j0 + u * 64 * NW, a.C - 1);
+      const int cls = h[u] == p ? 0 : h[u] < 0 ? 1 : (h[u] >= a.sinks && h[u] <= p - a.recent) ? 2 : 3;
+      const unsigned o = cls < 2 ? 0u : weight_order(x[u]);
+      const unsigned long long key = ((unsigned long long)cls << 62) | ((unsigned long long)o << 30) | (unsigned)j;
+      best = key < best ? key : best;
+    }
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {

@@ -39,77 +39,178 @@ __device__ __forceinline__ void bf16_parts(const float (&x)[8], Frag<bf16> (&f)[
   }
 }
 
-// 32 slots of a wave as they come from memory.  Lane (lr, lg): elements lg D / 4 .. of the keys of slots lr
-// and 16 + lr; elements lr D / 16 .. of the values of slots 16 u + 4 lg + i, i < 4; scales of all
-// blocks of these slots.
+// 32 slots of a wave in LDS, where buffer loads that write it directly put them (the scales come through a
+// register each).  Such loads fill LDS in lane order, 16 bytes a lane; which row they come from is free:
+// keys: lane (lr, lg) reads back what it brought, elements lg D / 4 .. of slots lr and 16 + lr (4 bits and
+// D = 64, 8 bytes a key: rows in order); values: rows 4 lg + i stand at i-major places of their 16, so that the
+// lanes' elements lr D / 16 .. of slots 4 lg + i, one i a read, are neighbours.  No bank conflicts either way.
 template <int BITS, int D>
-struct MxStep {
-  static constexpr int RB = D * BITS / 8, SB = D / 32;         // bytes of a row, of its scales
+struct MxTile {
+  static constexpr int RB = D * BITS / 8, SB = D / 32;                  // bytes of a row, of its scales
   static constexpr int KW = RB / 16, VB = RB / 16, VW = VB < 4 ? 1 : VB / 4;   // words a lane and key; bytes, words a slot
-  u32 k[2][KW], v[8][VW], ks[2], vs[2][SB];
+  static constexpr int kRows = 32 * RB, kBytes = 2 * kRows, kLoads = kRows / 1024;   // a side; both; instructions a side
+  static constexpr int kScales = 64 * SB;
 
-  // n rows from slot j0 on (a read behind them gives zero)
+  // n rows of a cache from slot j0 on (a read behind them gives zero)
   static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const void* base, size_t j0, int n, int row_bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((char*)base + j0 * row_bytes, 0, n * row_bytes, 0x00020000);
   }
-  // (constant parts of an offset are the scalar operand: one address register for all slots)
-  template <int N>
-  static __device__ __forceinline__ void words(__amdgpu_buffer_rsrc_t r, int off, int more, u32* w) {
-    if constexpr (N == 1) {
-      w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, more, 0);
-    } else if constexpr (N == 2) {
-      const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, off, more, 0);
-      w[0] = x[0];
-      w[1] = x[1];
+  // place of a key row's piece of 16 bytes within the row: ^ this
+  static __device__ __forceinline__ int swz(int row) { return RB == 32 ? 0 : RB == 64 ? (row >> 2) & 3 : (row >> 1) & 7; }
+  // 16 bytes a lane to LDS, marked as not used again (2): codes are read once a step, and a load that takes no place in
+  // the caches need not move out what others wrote there.  256 / 64 sequences, 16 heads on 4, window 4,096, 4 bits: 108 /
+  // 29 us again and again, 137 / 44 after other work has filled the caches; without the mark 122 / 26.5 and 180 / 69.
+  // (The scales, 128 bytes of a line at a time, are left their places: 107 against 111 us.)
+  static __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, unsigned char* dst, int off, int more) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, off, more, 0, 2);
+  }
+  static __device__ __forceinline__ void load_k(unsigned char* dst, const void* codes, size_t j0, int n) {
+    const auto r = rows(codes, j0, n, RB);
+    const int lane = lane_id(), row = lane * 16 / RB;
+    const int off = 16 * (lane ^ swz(row));
+#pragma unroll
+    for (int h = 0; h < kLoads; ++h)             // (8 bits, D = 128: eight rows a load; the swizzle of rows 8 .. 15 is ^ 4)
+      load(r, dst + 1024 * h, RB == 128 && (h & 1) ? off ^ 64 : off, 1024 * h);
+  }
+  static __device__ __forceinline__ void load_v(unsigned char* dst, const void* codes, size_t j0, int n) {
+    const int lane = lane_id(), place = lane * 16 / RB;
+    const auto r = rows(codes, j0, n, RB);
+    const int off = (16 * (place >> 4) + 4 * (place & 3) + ((place & 15) >> 2)) * RB + lane * 16 % RB;
+#pragma unroll
+    for (int h = 0; h < kLoads; ++h)
+      load(r, dst + kRows + 1024 * h, off, (RB == 128 ? (h >> 1) * 16 + (h & 1) * 2 : h * 16) * RB);
+  }
+  // the scales of slot lane % 32, of its key and its value
+  static __device__ __forceinline__ u32x2 load_scales(const void* sk, const void* sv, size_t j0, int n) {
+    const int slot = lane_id() & 31;
+    const auto rk = rows(sk, j0, n, SB), rv = rows(sv, j0, n, SB);
+    u32 x, y;
+    if constexpr (SB == 4) {
+      x = __builtin_amdgcn_raw_buffer_load_b32(rk, slot * SB, 0, 0);
+      y = __builtin_amdgcn_raw_buffer_load_b32(rv, slot * SB, 0, 0);
     } else {
+      x = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rk, slot * SB, 0, 0);
+      y = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rv, slot * SB, 0, 0);
+    }
+    return u32x2{x, y};
+  }
+  // to LDS: all keys', then all values'
+  static __device__ __forceinline__ void put_scales(unsigned char* s, u32x2 f) {
+    const u32 x = lane_id() < 32 ? f[0] : f[1];
+    if constexpr (SB == 4) reinterpret_cast<u32*>(s)[lane_id()] = x;
+    else reinterpret_cast<unsigned short*>(s)[lane_id()] = (unsigned short)x;
+  }
+  // Reads of what direct loads brought are written out, each with its own wait: before a read that the
+  // compiler makes it waits for every direct load, those of the next steps too.
+  static __device__ __forceinline__ u32 address(const unsigned char* p) {
+    return (u32)(uintptr_t)(__attribute__((address_space(3))) const unsigned char*)p;
+  }
+  // the lane's key elements of slots lr and 16 + lr, and their scales
+  static __device__ __forceinline__ void read_k(const unsigned char* src, const unsigned char* s, u32 (&w)[2][KW], float (&f)[2]) {
+    const int lane = lane_id(), lr = lane & 15, lg = lane >> 4;
+    const u32 at = address(src) + (KW == 2 ? 32 * lr + 8 * lg : KW == 4 ? 64 * lr + 16 * (lg ^ swz(lr)) : 128 * lr + 16 * ((2 * lg) ^ swz(lr))), st = address(s) + lr * SB + lg * SB / 4;
+    u32 sc[2];
+    if constexpr (KW == 2) {
+      u32x2 x, y;
+      asm volatile("ds_read_b64 %0, %4\n\tds_read_b64 %1, %4 offset:512\n\tds_read_u8 %2, %5\n\tds_read_u8 %3, %5 offset:%6\n\t"
+                   "s_waitcnt lgkmcnt(0)" : "=&v"(x), "=&v"(y), "=&v"(sc[0]), "=&v"(sc[1]) : "v"(at), "v"(st), "n"(16 * SB) : "memory");
 #pragma unroll
-      for (int h = 0; h < N / 4; ++h) {
-        const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(r, off, more + 16 * h, 0);
+      for (int i = 0; i < 2; ++i) {
+        w[0][i] = x[i];
+        w[1][i] = y[i];
+      }
+    } else if constexpr (KW == 4) {
+      u32x4 x, y;
+      asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:1024\n\tds_read_u8 %2, %5\n\tds_read_u8 %3, %5 offset:%6\n\t"
+                   "s_waitcnt lgkmcnt(0)" : "=&v"(x), "=&v"(y), "=&v"(sc[0]), "=&v"(sc[1]) : "v"(at), "v"(st), "n"(16 * SB) : "memory");
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[4 * h + i] = x[i];
+      for (int i = 0; i < 4; ++i) {
+        w[0][i] = x[i];
+        w[1][i] = y[i];
+      }
+    } else {
+      u32x4 x[4];
+      asm volatile("ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\tds_read_b128 %2, %6 offset:2048\n\t"
+                   "ds_read_b128 %3, %7 offset:2048\n\tds_read_u8 %4, %8\n\tds_read_u8 %5, %8 offset:%9\n\ts_waitcnt lgkmcnt(0)"
+                   : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(sc[0]), "=&v"(sc[1])
+                   : "v"(at), "v"(at ^ 16), "v"(st), "n"(16 * SB) : "memory");
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[0][i] = x[i >> 2][i & 3];
+        w[1][i] = x[2 + (i >> 2)][i & 3];
       }
     }
+    f[0] = scale_value(sc[0]);
+    f[1] = scale_value(sc[1]);
   }
-  __device__ __forceinline__ void load_k(const void* codes, const void* scales, size_t j0, int n) {
-    const int lane = lane_id(), lr = lane & 15, lg = lane >> 4;
-    const auto c = rows(codes, j0, n, RB), s = rows(scales, j0, n, SB);
+  // the lane's value elements of slots 16 u + 4 lg + i, j = 4 u + i, and their scales: the byte of the block
+  // turned to where a float has its exponent (the conversions look at nothing else of it)
+  static __device__ __forceinline__ void read_v(const unsigned char* src, const unsigned char* s, u32 (&w)[8][VW], float (&f)[8]) {
+    const int lane = lane_id(), blk = (lane & 15) * SB / 16;
+    const u32 at = address(src + kRows) + lane * VB, st = address(s) + (32 + 4 * (lane >> 4)) * SB;
+    u32 sc[2][SB];
+    if constexpr (VB == 2) {
+      u32x2 p, q;
+      asm volatile("ds_read_u16 %0, %10\n\tds_read_u16 %1, %10 offset:128\n\tds_read_u16 %2, %10 offset:256\n\t"
+                   "ds_read_u16 %3, %10 offset:384\n\tds_read_u16 %4, %10 offset:512\n\tds_read_u16 %5, %10 offset:640\n\t"
+                   "ds_read_u16 %6, %10 offset:768\n\tds_read_u16 %7, %10 offset:896\n\t"
+                   "ds_read_b64 %8, %11\n\tds_read_b64 %9, %11 offset:32\n\ts_waitcnt lgkmcnt(0)"
+                   : "=&v"(w[0][0]), "=&v"(w[1][0]), "=&v"(w[2][0]), "=&v"(w[3][0]), "=&v"(w[4][0]), "=&v"(w[5][0]),
+                     "=&v"(w[6][0]), "=&v"(w[7][0]), "=&v"(p), "=&v"(q) : "v"(at), "v"(st) : "memory");
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      words<KW>(c, lr * RB + lg * KW * 4, 16 * u * RB, k[u]);
-      ks[u] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(s, lr * SB + lg * SB / 4, 16 * u * SB, 0);
-    }
-  }
-  __device__ __forceinline__ void load_v(const void* codes, const void* scales, size_t j0, int n) {
-    const int lane = lane_id(), lr = lane & 15, lg = lane >> 4;
-    const auto c = rows(codes, j0, n, RB), s = rows(scales, j0, n, SB);
+      for (int i = 0; i < 2; ++i) {
+        sc[0][i] = p[i];
+        sc[1][i] = q[i];
+      }
+    } else if constexpr (VB == 4) {
+      u32x2 x[4];
+      if constexpr (SB == 4) {
+        u32x4 p, q;
+        asm volatile("ds_read2st64_b32 %0, %6 offset1:1\n\tds_read2st64_b32 %1, %6 offset0:2 offset1:3\n\t"
+                     "ds_read2st64_b32 %2, %6 offset0:4 offset1:5\n\tds_read2st64_b32 %3, %6 offset0:6 offset1:7\n\t"
+                     "ds_read_b128 %4, %7\n\tds_read_b128 %5, %7 offset:64\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(p), "=&v"(q) : "v"(at), "v"(st) : "memory");
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int more = 16 * (j >> 2) + (j & 3), off = 4 * lg * RB + lr * VB;
-      if constexpr (VB == 2) v[j][0] = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(c, off, more * RB, 0);
-      else words<VW>(c, off, more * RB, v[j]);
-    }
-    if (n == 32) {                               // four slots at a time, where all four are there
+        for (int i = 0; i < 4; ++i) {
+          sc[0][i] = p[i];
+          sc[1][i] = q[i];
+        }
+      } else {
+        u32x2 p, q;
+        asm volatile("ds_read2st64_b32 %0, %6 offset1:1\n\tds_read2st64_b32 %1, %6 offset0:2 offset1:3\n\t"
+                     "ds_read2st64_b32 %2, %6 offset0:4 offset1:5\n\tds_read2st64_b32 %3, %6 offset0:6 offset1:7\n\t"
+                     "ds_read_b64 %4, %7\n\tds_read_b64 %5, %7 offset:32\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(p), "=&v"(q) : "v"(at), "v"(st) : "memory");
 #pragma unroll
-      for (int u = 0; u < 2; ++u) words<SB>(s, 4 * lg * SB, 16 * u * SB, vs[u]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int u = j >> 2, i = j & 3, more = (16 * u + i) * SB;
-        if constexpr (SB == 4) {
-          vs[u][i] = __builtin_amdgcn_raw_buffer_load_b32(s, 4 * lg * SB, more, 0);
-        } else {
-          const u32 x = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(s, 4 * lg * SB, more, 0);
-          vs[u][i >> 1] = (i & 1) ? vs[u][i >> 1] | x << 16 : x;
+        for (int i = 0; i < 2; ++i) {
+          sc[0][i] = p[i];
+          sc[1][i] = q[i];
         }
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j][0] = x[j >> 1][j & 1];
+    } else {
+      u32x4 x[4], p, q;
+      asm volatile("ds_read2st64_b64 %0, %6 offset1:1\n\tds_read2st64_b64 %1, %6 offset0:2 offset1:3\n\t"
+                   "ds_read2st64_b64 %2, %6 offset0:4 offset1:5\n\tds_read2st64_b64 %3, %6 offset0:6 offset1:7\n\t"
+                   "ds_read_b128 %4, %7\n\tds_read_b128 %5, %7 offset:64\n\ts_waitcnt lgkmcnt(0)"
+                   : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(p), "=&v"(q) : "v"(at), "v"(st) : "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[j][i] = x[j >> 1][2 * (j & 1) + i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sc[0][i] = p[i];
+        sc[1][i] = q[i];
+      }
     }
-  }
-  // scale of this lane's values of its slot j
-  __device__ __forceinline__ u32 v_scale(int j) const {
-    const int lr = lane_id() & 15, blk = lr * SB / 16;
-    const int i = j & 3;
-    if constexpr (SB == 4) return (vs[j >> 2][i] >> (8 * blk)) & 255u;
-    else return (vs[j >> 2][i >> 1] >> (8 * (blk + 2 * (i & 1)))) & 255u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = j & 3;
+      const u32 y = sc[j >> 2][i * SB / 4];
+      f[j] = __builtin_bit_cast(float, __builtin_amdgcn_alignbit(y, y, (8 * (blk + (SB == 4 ? 0 : 2 * (i & 1))) + 9) & 31));
+    }
   }
 };
 
@@ -124,11 +225,14 @@ __device__ __forceinline__ float group_max(float x) {
 }
 
 template <typename T, int BITS, int D, int NT, int NW, bool BUDGET, bool NEAR>
-__global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(CacheArgs a) {
-  using Step = MxStep<BITS, D>;
+__global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) void mx_decode_kernel(CacheArgs a) {
+  using Tile = MxTile<BITS, D>;
   constexpr int STEP = 32 * NW, N = sizeof(T) == 2 ? 1 : 3, KK = D / 32, DT = D / 16;
-  constexpr int RB = Step::RB, SB = Step::SB;
-  __shared__ __align__(16) float mg[NW * 16 * D];
+  constexpr int RB = Tile::RB, SB = Tile::SB;
+  constexpr int AHEAD = 2;                                       // steps whose rows are on their way or in use
+  constexpr int BUFFERS = NW * AHEAD * Tile::kBytes, MERGE = NW * 16 * D * 4;
+  __shared__ __align__(16) unsigned char smem[BUFFERS > MERGE ? BUFFERS : MERGE];
+  __shared__ __align__(16) unsigned char scales[NW][Tile::kScales];
   __shared__ unsigned long long red[NW];
   __shared__ float ml[NW][16][2];
   __shared__ float st[16 * NT][2];
@@ -138,64 +242,72 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
   const int G = a.Hq / a.Hkv;
   const int split = uniform(blockIdx.x % a.n_split), bk = uniform(blockIdx.x / a.n_split), b = uniform(bk / a.Hkv);
   const int lane = lane_id(), wave = wave_uid(), lr = lane & 15, lg = lane >> 4;
-  const int p = uniform(a.pos[b]);
+  const int lo = split * a.split_len, end = min(lo + a.split_len, a.C), first = lo + 32 * wave;
+  char* ck = reinterpret_cast<char*>(a.cache_k) + (size_t)bk * a.C * RB;
+  char* cv = reinterpret_cast<char*>(a.cache_v) + (size_t)bk * a.C * RB;
+  unsigned char* sk = a.k_scales + (size_t)bk * a.C * SB;
+  unsigned char* sv = a.v_scales + (size_t)bk * a.C * SB;
+  const int* held = BUDGET ? a.cache_pos + (size_t)bk * a.C : nullptr;
+  auto position = [&](int j0) { return BUDGET ? held[min(j0 + (lane & 31), a.C - 1)] : 0; };
+  // What does not depend on the position is asked for before it is known: q, a piece a lane of the token's k and v, the
+  // first steps' rows.  In this order, since loads arrive in order.
+  const int pos_b = a.pos[b];
+  const int piece = lane % (D / 8), is_v = lane / (D / 8) & 1;
+  const Frag<T> token = load_frag(reinterpret_cast<const T*>(is_v ? a.v : a.k) + (size_t)bk * D + 8 * piece);
+  Frag<T> q[NT][KK];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+      q[nt][kk] = load_frag(reinterpret_cast<const T*>(a.q) + ((size_t)bk * G + min(16 * nt + lr, G - 1)) * D + lg * (D / 4) + 8 * kk);
+  int pos[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) pos[i] = position(first + i * STEP);
+  unsigned char* buf = smem + wave * AHEAD * Tile::kBytes;
+  unsigned char* sc = scales[wave];
+  u32x2 scale_ahead[AHEAD];
+  auto fetch_k = [&](int stage, int j0, int n) {
+    Tile::load_k(buf + stage * Tile::kBytes, ck, j0, n);
+    scale_ahead[stage] = Tile::load_scales(sk, sv, j0, n);
+  };
+  auto fetch_v = [&](int stage, int j0, int n) { Tile::load_v(buf + stage * Tile::kBytes, cv, j0, n); };
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    const int j0 = first + i * STEP, n = uniform(max(0, min(end - j0, 32)));
+    fetch_k(i, j0, n);
+    __builtin_amdgcn_sched_barrier(0);           // the waits below count on this order
+    fetch_v(i, j0, n);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  const int p = uniform(pos_b);
   T* ob = reinterpret_cast<T*>(a.o) + (size_t)bk * G * D;
   if (p < 0) {                                   // no token: the cache stays as it is
     if (split == 0) {
       for (int i = threadIdx.x; i < G * D; i += 64 * NW) ob[i] = to<T>(0.f);
       if (BUDGET && threadIdx.x == 0) a.slot[bk] = -1;
     }
+    wait_loads<0>();                             // (they write LDS that the next workgroup may have)
     return;
   }
   const int count = BUDGET ? a.C : min(p, a.C - 1) + 1;          // a ring holds its tokens from slot 0 up
-  const int lo = split * a.split_len, hi = min(min(lo + a.split_len, a.C), count);
-  char* ck = reinterpret_cast<char*>(a.cache_k) + (size_t)bk * a.C * RB;
-  char* cv = reinterpret_cast<char*>(a.cache_v) + (size_t)bk * a.C * RB;
-  unsigned char* sk = a.k_scales + (size_t)bk * a.C * SB;
-  unsigned char* sv = a.v_scales + (size_t)bk * a.C * SB;
-  const int* held = BUDGET ? a.cache_pos + (size_t)bk * a.C : nullptr;
-  const int first = lo + 32 * wave;
-  // slots of the 32 from j0 that hold a token, one bit each
-  auto position = [&](int j0) { return BUDGET ? held[min(j0 + (lane & 31), a.C - 1)] : 0; };
-  auto live_of = [&](int j0, int pos) {
+  const int hi = min(end, count);
+  // slots of the 32 from j0 that hold a token, one bit each; rows to read: up to the last of them
+  auto live_of = [&](int j0, int held_pos) {
     const int j = j0 + (lane & 31);
-    return (unsigned)__ballot(j < hi && (!BUDGET || pos >= 0));
+    return (unsigned)__ballot(j < hi && (!BUDGET || held_pos >= 0));
   };
-  // (q before the rows: loads arrive in order, so what waits for rows has q)
-  Frag<bf16> Q[NT][KK][N];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int g = min(16 * nt + lr, G - 1);
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      const Frag<T> f = load_frag(reinterpret_cast<const T*>(a.q) + ((size_t)bk * G + g) * D + lg * (D / 4) + 8 * kk);
-      if constexpr (N == 1) {
-        Q[nt][kk][0] = f;
-      } else {
-        float y[8];
-        to_floats(f, y);
-        bf16_parts<N>(y, Q[nt][kk]);
-      }
-    }
-  }
-  // rows of the 32 to read: up to the last that holds a token
   auto rows_of = [&](unsigned live) { return uniform(32 - __clz((int)live)); };
-  Step x;
-  unsigned live = 0;
-  if (first < hi) {
-    live = live_of(first, position(first));
-    x.load_k(ck, sk, first, rows_of(live));
-    x.load_v(cv, sv, first, rows_of(live));
-  }
+  unsigned live[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) live[i] = live_of(first + i * STEP, pos[i]);
   const int at = uniform(BUDGET ? pick_slot<NW>(a, bk, p, red) : ring_slot(a, p));
   if (BUDGET && split == 0 && threadIdx.x == 0) a.slot[bk] = at;
   // the wave that holds the slot writes the token's rows
   if (at >= lo && at < hi && (at - lo) / 32 % NW == wave) {
     if (lane < D / 4) {
-      const int piece = lane % (D / 8), is_v = lane / (D / 8);
       u32 scale;
-      const Eight<BITS> c =
-          write_block<BITS>(load_frag(reinterpret_cast<const T*>(is_v ? a.v : a.k) + (size_t)bk * D + 8 * piece), scale);
+      const Eight<BITS> c = write_block<BITS>(token, scale);
       reinterpret_cast<Eight<BITS>*>(fresh[is_v])[piece] = c;
       reinterpret_cast<Eight<BITS>*>((is_v ? cv : ck) + (size_t)at * RB)[piece] = c;
       if ((piece & 3) == 0) {
@@ -206,6 +318,33 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // written and read by this wave alone
     __builtin_amdgcn_wave_barrier();
   }
+  auto put_token = [&](unsigned char* rows, unsigned char* s, int own) {
+    const int u = own >> 4, r = own & 15;
+    const u32* k = fresh[0];
+    const u32* v = fresh[1];
+    if (lane < RB / 4) {                         // a word of k and of v
+      const int place = own * (RB / 4) + (lane ^ 4 * Tile::swz(r));
+      reinterpret_cast<u32*>(rows)[place] = k[lane];
+      reinterpret_cast<u32*>(rows + Tile::kRows)[(16 * u + 4 * (r & 3) + (r >> 2)) * (RB / 4) + lane] = v[lane];
+    }
+    if (lane < SB) {
+      s[own * SB + lane] = fresh_scale[0][lane];
+      s[(32 + own) * SB + lane] = fresh_scale[1][lane];
+    }
+  };
+  Frag<bf16> Q[NT][KK][N];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      if constexpr (N == 1) {
+        Q[nt][kk][0] = q[nt][kk];
+      } else {
+        float y[8];
+        to_floats(q[nt][kk], y);
+        bf16_parts<N>(y, Q[nt][kk]);
+      }
+    }
   const float c = a.scale * kLog2e;
   f32x4 O[NT][DT];
   float m[NT], l[NT];
@@ -216,32 +355,38 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) O[nt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  int ahead = position(first + STEP);            // positions are asked for a step before the rows
-  for (int j0 = first; j0 < hi; j0 += STEP) {
-    const unsigned next = live_of(j0 + STEP, ahead);
-    ahead = position(j0 + 2 * STEP);
+  // instructions of a step's loads in the order they are issued: k, scales (two), v, and one for positions; waiting
+  // for k (v) leaves those that were issued after it on their way
+  constexpr int kStep = 2 * Tile::kLoads + 2 + BUDGET;
+  constexpr int kAfterK = Tile::kLoads + (AHEAD - 1) * kStep, kAfterV = (AHEAD - 1) * kStep + Tile::kLoads + 2;
+  int ahead = position(first + AHEAD * STEP);    // asked for a step before the rows
+  auto step = [&](auto stage_, int j0) {
+    constexpr int stage = decltype(stage_)::value;
+    unsigned char* rows = buf + stage * Tile::kBytes;
+    const unsigned next = live_of(j0 + AHEAD * STEP, ahead);
+    ahead = position(j0 + (AHEAD + 1) * STEP);
     const int own = at - j0;                     // the token's slot, if of these
-    if (own >= 0 && own < 32) {
-      live |= 1u << own;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (own == 16 * u + lr) {
-#pragma unroll
-          for (int i = 0; i < Step::KW; ++i) x.k[u][i] = fresh[0][lg * Step::KW + i];
-          x.ks[u] = fresh_scale[0][lg * SB / 4];
-        }
+    wait_loads<kAfterK>();
+    Tile::put_scales(sc, scale_ahead[stage]);
+    if (own >= 0 && own < 32) {                  // its rows as codes, over what was there
+      live[stage] |= 1u << own;
+      wait_loads<0>();
+      put_token(rows, sc, own);
     }
+    const unsigned on = live[stage];
+    u32 kw[2][Tile::KW];
+    float kscale[2];
+    Tile::read_k(rows, sc, kw, kscale);
     f32x4 X[NT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       Frag<bf16> K[KK];
-      const float s = scale_value(x.ks[u]);
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
         Eight<BITS> e;
-        if constexpr (BITS == 4) e.w = x.k[u][kk];
-        else e.w = u32x2{x.k[u][2 * kk], x.k[u][2 * kk + 1]};
-        K[kk] = read_eight<BITS>(e, s);
+        if constexpr (BITS == 4) e.w = kw[u][kk];
+        else e.w = u32x2{kw[u][2 * kk], kw[u][2 * kk + 1]};
+        K[kk] = read_eight<BITS>(e, kscale[u]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -252,17 +397,18 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
           for (int kk = 0; kk < KK; ++kk) mma(X[nt][u], K[kk], Q[nt][kk][n]);
       }
     }
+    live[stage] = next;
     __builtin_amdgcn_sched_barrier(0);
-    x.load_k(ck, sk, (size_t)j0 + STEP, rows_of(next));   // (behind the last slots: no rows)
+    fetch_k(stage, j0 + AHEAD * STEP, rows_of(next));            // (behind the last slots: no rows)
     Frag<bf16> P[NT][N];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) X[nt][u] *= c;
-      if (live != ~0u) {
+      if (on != ~0u) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (!((live >> (16 * (j >> 2) + 4 * lg + (j & 3))) & 1)) X[nt][j >> 2][j & 3] = -INFINITY;
+          if (!((on >> (16 * (j >> 2) + 4 * lg + (j & 3))) & 1)) X[nt][j >> 2][j & 3] = -INFINITY;
       }
       float mx = X[nt][0][0];
 #pragma unroll
@@ -293,34 +439,18 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
       }
       bf16_parts<N>(y, P[nt]);                   // (bf16: rounded for the product with v, the sum l is not)
     }
-    if (own >= 0 && own < 32) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = j & 3, u = j >> 2;
-        if (own == 16 * u + 4 * lg + i) {
-          if constexpr (Step::VB == 2) x.v[j][0] = reinterpret_cast<const unsigned short*>(fresh[1])[lr];
-          else
-#pragma unroll
-            for (int w = 0; w < Step::VW; ++w) x.v[j][w] = fresh[1][lr * Step::VW + w];
-          if constexpr (SB == 4) x.vs[u][i] = *reinterpret_cast<const u32*>(fresh_scale[1]);
-          else {
-            const u32 s = *reinterpret_cast<const unsigned short*>(fresh_scale[1]);
-            x.vs[u][i >> 1] = (i & 1) ? (x.vs[u][i >> 1] & 0xffffu) | s << 16 : (x.vs[u][i >> 1] & 0xffff0000u) | s;
-          }
-        }
-      }
-    }
     // V^T operands, two rows d of it at a time: two values of each of the eight slots, paired up by slot
+    u32 v[8][Tile::VW];
     float vscale[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) vscale[j] = scale_value(x.v_scale(j));
-    if (BUDGET && live != ~0u) {                 // what stands in empty slots reaches nothing
+    wait_loads<kAfterV>();
+    Tile::read_v(rows, sc, v, vscale);
+    if (on != ~0u) {                             // what stands in empty slots reaches nothing
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (!((live >> (16 * (j >> 2) + 4 * lg + (j & 3))) & 1)) {
+        if (!((on >> (16 * (j >> 2) + 4 * lg + (j & 3))) & 1)) {
           vscale[j] = 0.f;
 #pragma unroll
-          for (int w = 0; w < Step::VW; ++w) x.v[j][w] = 0;
+          for (int w = 0; w < Tile::VW; ++w) v[j][w] = 0;
         }
     }
     auto pair_of_rows = [&](auto xx) {
@@ -328,7 +458,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
       u32x4 even, odd;
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        const u32 y = read_pair<BITS, S>(x.v[j][W], vscale[j]), z = read_pair<BITS, S>(x.v[j + 1][W], vscale[j + 1]);
+        const u32 y = read_pair<BITS, S>(v[j][W], vscale[j]), z = read_pair<BITS, S>(v[j + 1][W], vscale[j + 1]);
         even[j / 2] = __builtin_amdgcn_perm(z, y, 0x05040100u);
         odd[j / 2] = __builtin_amdgcn_perm(z, y, 0x07060302u);
       }
@@ -350,9 +480,20 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void mx_decode_kernel(Cac
       pair_of_rows(std::integral_constant<int, 3>());
     }
     __builtin_amdgcn_sched_barrier(0);
-    x.load_v(cv, sv, (size_t)j0 + STEP, rows_of(next));
-    live = next;
+    fetch_v(stage, j0 + AHEAD * STEP, rows_of(next));
+  };
+  if (first < hi) {
+    for (int j0 = first;;) {
+      step(std::integral_constant<int, 0>(), j0);
+      j0 += STEP;
+      if (j0 >= hi) break;
+      step(std::integral_constant<int, 1>(), j0);
+      j0 += STEP;
+      if (j0 >= hi) break;
+    }
   }
+  wait_loads<0>();                               // nothing writes LDS any more
+  float* mg = reinterpret_cast<float*>(smem);
   // join the waves, 16 heads at a time (4-float pieces of a row swizzled by the head); row 4 lg + i of tile
   // dt of an accumulator is element (4 lg + i) D / 16 + dt
 #pragma unroll
