@@ -877,11 +877,22 @@ def _bits(bits):
 
 
 def _row_bits(codes, scales):
-    """The bits of a code, from the widths of codes [..., D*bits/8] and scales [..., D/32]."""
-    bits, rest = divmod(codes.shape[-1], 4 * scales.shape[-1]) if scales.dim() and codes.dim() and scales.shape[-1] else (0, 1)
-    if rest or bits not in (4, 8) or codes.shape[:-1] != scales.shape[:-1]:
-        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not rows of 4 or 8 bits")
-    return bits
+    """The bits of a code, from the shapes of codes [..., D*bits/8] and scales [..., D/32]."""
+    cs, ss = codes.shape, scales.shape
+    if cs and ss and cs[:-1] == ss[:-1]:
+        if cs[-1] == 16 * ss[-1] and ss[-1]:
+            return 4
+        if cs[-1] == 32 * ss[-1] and ss[-1]:
+            return 8
+    raise ValueError(f"codes {tuple(cs)} and scales {tuple(ss)} are not rows of 4 or 8 bits")
+
+
+def _given(t, name, shape, dtype, dev):
+    """An output that the caller passed, or a new one: (tensor, its address)."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _fit(t, name, shape, dtype, dev)
 
 
 def mx_quant(x, bits=4, codes=None, scales=None):
@@ -893,18 +904,15 @@ def mx_quant(x, bits=4, codes=None, scales=None):
     not finite are read back as not a number.  Outputs may be passed preallocated."""
     if not x.is_cuda:
         raise ValueError(f"x: expected a GPU tensor, got {x.device}")
-    if x.dim() < 1 or x.shape[-1] % 32:
-        raise ValueError(f"x: the last dimension must be a multiple of 32, got {tuple(x.shape)}")
+    shape = x.shape
+    if not shape or shape[-1] % 32:
+        raise ValueError(f"x: the last dimension must be a multiple of 32, got {tuple(shape)}")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    rows, D, dev, code = x.shape[:-1], x.shape[-1], x.device, _dtype_code(x)
-    cs, ss = rows + (D * _bits(bits) // 8,), rows + (D // 32,)
-    if codes is None:
-        codes = torch.empty(cs, dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty(ss, dtype=torch.uint8, device=dev)
-    _call("carve_mx_quant", dev, x.numel(), code, bits, x.data_ptr(), _fit(codes, "codes", cs, torch.uint8, dev),
-          _fit(scales, "scales", ss, torch.uint8, dev))
+    rows, D, dev, code = shape[:-1], shape[-1], x.device, _dtype_code(x)
+    codes, to_codes = _given(codes, "codes", rows + (D * _bits(bits) // 8,), torch.uint8, dev)
+    scales, to_scales = _given(scales, "scales", rows + (D // 32,), torch.uint8, dev)
+    _call("carve_mx_quant", dev, x.numel(), code, bits, x.data_ptr(), to_codes, to_scales)
     return codes, scales
 
 
@@ -914,11 +922,10 @@ def mx_dequant(codes, scales, dtype=torch.bfloat16, out=None):
     bits = _row_bits(codes, scales)
     if not codes.is_cuda:
         raise ValueError(f"codes: expected a GPU tensor, got {codes.device}")
-    shape, dev = codes.shape[:-1] + (scales.shape[-1] * 32,), codes.device
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    _call("carve_mx_dequant", dev, out.numel(), _dtype_code(out), bits, _fit(codes, "codes", codes.shape, torch.uint8, dev),
-          _fit(scales, "scales", scales.shape, torch.uint8, dev), _fit(out, "out", shape, dtype, dev))
+    dev, ss = codes.device, scales.shape
+    ptrs = _fit(codes, "codes", codes.shape, torch.uint8, dev), _fit(scales, "scales", ss, torch.uint8, dev)
+    out, to_out = _given(out, "out", ss[:-1] + (ss[-1] * 32,), dtype, dev)
+    _call("carve_mx_dequant", dev, out.numel(), _dtype_code(out), bits, *ptrs, to_out)
     return out
 
 
@@ -957,8 +964,7 @@ def swa_decode_mx(q, k, v, cache, pos, window, sinks=0, scale=None, o=None, work
     kv, rows = (B, Hkv, D), _mx_rows(cache, B, Hkv, window + sinks, D, dev)
     ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev), ctypes.byref(rows),
             _fit(pos, "pos", (B,), torch.int32, dev))
-    if o is None:
-        o = torch.empty_like(q)
+    o = torch.empty_like(q) if o is None else o
     workspace, ws, nbytes = _workspace("carve_swa_decode_mx_workspace_size", sp, dev, workspace, rows.bits)
     _call("carve_swa_decode_mx", dev, sp, *ptrs, _fit(o, "o", q.shape, dt, dev), ws, nbytes)
     return o
@@ -999,13 +1005,10 @@ def budget_decode_mx(q, k, v, cache, pos, sinks=0, recent=1, scale=None, o=None,
     ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev), ctypes.byref(rows),
             _fit(cache_w, "cache_w", (B, Hkv, C), torch.float32, dev),
             _fit(cache_pos, "cache_pos", (B, Hkv, C), torch.int32, dev), _fit(pos, "pos", (B,), torch.int32, dev))
-    if o is None:
-        o = torch.empty_like(q)
-    if slot is None:
-        slot = torch.empty(slots, dtype=torch.int32, device=dev)
+    o = torch.empty_like(q) if o is None else o
+    slot, to_slot = _given(slot, "slot", slots, torch.int32, dev)
     workspace, ws, nbytes = _workspace("carve_budget_decode_mx_workspace_size", sp, dev, workspace, rows.bits)
-    _call("carve_budget_decode_mx", dev, sp, *ptrs, _fit(o, "o", q.shape, dt, dev),
-          _fit(slot, "slot", slots, torch.int32, dev), ws, nbytes)
+    _call("carve_budget_decode_mx", dev, sp, *ptrs, _fit(o, "o", q.shape, dt, dev), to_slot, ws, nbytes)
     return o, slot
 
 

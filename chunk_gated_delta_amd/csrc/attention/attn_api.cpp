@@ -202,7 +202,7 @@ carve_status check_budget(const carve_budget_shape* s) {
 bool near_scores(const carve_budget_shape* s, int bits, int n_split, int waves) {
   const long long G = s->Hq / s->Hkv;
   return (bits || s->dtype == CARVE_BF16) && n_split == 1 && waves == 8 && (s->D == 128 || s->B * s->Hkv <= 256) && G <= 16 &&
-         G * carve::score_row(s->C) <= carve::kNearScores;
+         G * carve::score_row(s->C) <= (bits ? carve::mx_near_scores(bits, s->D) : carve::kNearScores);
 }
 
 // A cache as the calls give it: rows of the call's dtype, or codes and scales.

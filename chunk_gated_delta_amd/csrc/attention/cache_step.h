@@ -56,22 +56,31 @@ __device__ __forceinline__ int ring_slot(const CacheArgs& a, int p) {
 
 // Adds the token's weights to the cache's: slots lo .. hi - 1, with max and sum of every head
 // (log2 domain) in st[head] = {m, 1 / l}, scores [G][score_row(C)] of the key head in `score`.
+// Slots a thread takes at a time, their positions and weights in flight together; a kernel may ask for the
+// first of them (from `lo` on) early.
 template <int NW>
-__device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st,
-                                            const float* score) {
-  const int G = a.Hq / a.Hkv;
-  const size_t row = (size_t)bk * a.C;
-  constexpr int STEP = 64 * NW, U = 4;           // slots a thread takes at a time, their loads in flight together
-  for (int j0 = lo + threadIdx.x; j0 < hi; j0 += U * STEP) {
-    float x[U], w[U];
-    int held[U];
+struct WeightBatch {
+  static constexpr int STEP = 64 * NW, U = 4;
+  int held[U];
+  float w[U];
+  __device__ __forceinline__ void load(const CacheArgs& a, int bk, int j0, int hi) {
+    const size_t row = (size_t)bk * a.C;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = min(j0 + u * STEP, hi - 1);
       held[u] = a.cache_pos[row + j];
       w[u] = a.cache_w[row + j];
-      x[u] = 0.f;
     }
+  }
+};
+template <int NW>
+__device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st,
+                                            const float* score, WeightBatch<NW> b) {
+  const int G = a.Hq / a.Hkv;
+  const size_t row = (size_t)bk * a.C;
+  constexpr int STEP = WeightBatch<NW>::STEP, U = WeightBatch<NW>::U;
+  for (int j0 = lo + threadIdx.x; j0 < hi; j0 += U * STEP) {
+    float x[U] = {};
     for (int g = 0; g < G; ++g) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -81,10 +90,18 @@ __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, i
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * STEP;
-      if (j < hi && (j == at || held[u] >= 0)) a.cache_w[row + j] = j == at ? x[u] : w[u] + x[u];
+      if (j < hi && (j == at || b.held[u] >= 0)) a.cache_w[row + j] = j == at ? x[u] : b.w[u] + x[u];
       if (j < hi && j == at) a.cache_pos[row + j] = p;
     }
+    if (j0 + U * STEP < hi) b.load(a, bk, j0 + U * STEP, hi);
   }
+}
+template <int NW>
+__device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st,
+                                            const float* score) {
+  WeightBatch<NW> b;
+  b.load(a, bk, lo + threadIdx.x, hi);
+  add_weights<NW>(a, bk, p, at, lo, hi, st, score, b);
 }
 
 // Joins the ranges of one key head: the output (a workgroup per head of the group, its ranges'

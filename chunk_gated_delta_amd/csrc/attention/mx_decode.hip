@@ -238,7 +238,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
   __shared__ float st[16 * NT][2];
   __shared__ __align__(16) u32 fresh[2][RB / 4];                 // the token's k and v
   __shared__ unsigned char fresh_scale[2][SB];
-  __shared__ __align__(16) float near_score[NEAR ? kNearScores : 4];
+  __shared__ __align__(16) float near_score[NEAR ? mx_near_scores(BITS, D) : 4];
   const int G = a.Hq / a.Hkv;
   const int split = uniform(blockIdx.x % a.n_split), bk = uniform(blockIdx.x / a.n_split), b = uniform(bk / a.Hkv);
   const int lane = lane_id(), wave = wave_uid(), lr = lane & 15, lg = lane >> 4;
@@ -494,6 +494,8 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
   }
   wait_loads<0>();                               // nothing writes LDS any more
   float* mg = reinterpret_cast<float*>(smem);
+  WeightBatch<NW> before;                        // on their way while the waves are joined
+  if (BUDGET && a.n_split == 1) before.load(a, bk, threadIdx.x, a.C);
   // join the waves, 16 heads at a time (4-float pieces of a row swizzled by the head); row 4 lg + i of tile
   // dt of an accumulator is element (4 lg + i) D / 16 + dt
 #pragma unroll
@@ -545,8 +547,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
   }
   if (BUDGET && a.n_split == 1) {
     __syncthreads();                             // scores of all waves, and st
-    if (NEAR) add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], near_score);
-    else add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], a.score + (size_t)bk * G * score_row(a.C));
+    add_weights<NW>(a, bk, p, at, 0, a.C, &st[0][0], NEAR ? near_score : a.score + (size_t)bk * G * score_row(a.C), before);
   }
 }
 
