@@ -556,10 +556,11 @@ static hipError_t launch_nt(const CacheArgs& a, hipStream_t st) {
   const int units = a.B * a.Hkv, G = a.Hq / a.Hkv;
   const dim3 grid(units * a.n_split);
   hipError_t e;
-  if (NT == 1 && a.waves == 8 && BUDGET && !a.score)
-    e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, 1, 8, BUDGET, BUDGET>, grid, 512, a, st);
-  else if (NT == 1 && a.waves == 8)
-    e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, 1, 8, BUDGET, false>, grid, 512, a, st);
+  constexpr int N8 = NT == 4 ? 2 : NT;           // (more than 32 heads: 4 waves only, registers)
+  if (NT < 4 && a.waves == 8 && BUDGET && !a.score)
+    e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, N8, 8, BUDGET, BUDGET>, grid, 512, a, st);
+  else if (NT < 4 && a.waves == 8)
+    e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, N8, 8, BUDGET, false>, grid, 512, a, st);
   else
     e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, NT, 4, BUDGET, false>, grid, kDecThreads, a, st);
   if (e != hipSuccess || a.n_split == 1) return e;
