@@ -978,7 +978,7 @@ def budget_cache_mx(B, Hkv, D, C, bits=4, device="cuda"):
 
 
 def budget_keep_mx(k, v, weights, C, sinks=0, recent=1, lens=None, cache=None, bits=4):
-    """budget_keep into a cache as budget_cache_mx makes it: `cache`, overwritten, or a new one."""
+    """budget_keep into a cache as budget_cache_mx makes it: `cache`, overwritten, or a new one of `bits`."""
     _whole(C=C, sinks=sinks, recent=recent)
     B, _, Hkv, T, D, dev, dt = _heads(k, k, 4)
     s = carve_budget_shape(B, Hkv, Hkv, T, D, C, sinks, recent, 1.0, _dtype_code(k))

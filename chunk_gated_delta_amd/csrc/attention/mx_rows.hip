@@ -104,21 +104,21 @@ template <typename T, int BITS, int D, bool BUDGET>
 __global__ __launch_bounds__(kRowThreads) void mx_fill_kernel(FillArgs a) {
   constexpr int PR = D / 8, ROWS = kRowThreads / PR;       // pieces of a row, rows of a workgroup
   const size_t bk = blockIdx.y;
-  const int piece = threadIdx.x % PR, j = blockIdx.x * ROWS + threadIdx.x / PR;
-  const int last = seq_len(a.lens, (int)(bk / a.Hkv), a.T) - 1;
-  if (j >= a.C) return;                          // (whole rows, whole blocks)
-  const size_t row = bk * a.C + j, at = row * PR + piece;
-  const int p = BUDGET ? a.cache_pos[row] : ring_token(a, j, last);
-  if (BUDGET && piece == 0) a.cache_w[row] = p < 0 ? 0.f : a.weights[bk * a.T + p];
-  if (p < 0) return;
-  const size_t src = (bk * a.T + p) * D + 8 * piece;
-  const Frag<T> k = load_once(reinterpret_cast<const T*>(a.k) + src), v = load_once(reinterpret_cast<const T*>(a.v) + src);
-  u32 ks, vs;
-  reinterpret_cast<Eight<BITS>*>(a.cache_k)[at] = write_block<BITS>(k, ks);
-  reinterpret_cast<Eight<BITS>*>(a.cache_v)[at] = write_block<BITS>(v, vs);
-  if ((piece & 3) == 0) {
-    reinterpret_cast<unsigned char*>(a.k_scales)[at >> 2] = (unsigned char)ks;
-    reinterpret_cast<unsigned char*>(a.v_scales)[at >> 2] = (unsigned char)vs;
+  const int piece = threadIdx.x % PR, last = seq_len(a.lens, (int)(bk / a.Hkv), a.T) - 1;
+  for (long long j = (long long)blockIdx.x * ROWS + threadIdx.x / PR; j < a.C; j += (long long)gridDim.x * ROWS) {
+    const size_t row = bk * a.C + j, at = row * PR + piece;      // (whole rows of lanes, whole blocks)
+    const int p = BUDGET ? a.cache_pos[row] : ring_token(a, (int)j, last);
+    if (BUDGET && piece == 0) a.cache_w[row] = p < 0 ? 0.f : a.weights[bk * a.T + p];
+    if (p < 0) continue;
+    const size_t src = (bk * a.T + p) * D + 8 * piece;
+    const Frag<T> k = load_once(reinterpret_cast<const T*>(a.k) + src), v = load_once(reinterpret_cast<const T*>(a.v) + src);
+    u32 ks, vs;
+    reinterpret_cast<Eight<BITS>*>(a.cache_k)[at] = write_block<BITS>(k, ks);
+    reinterpret_cast<Eight<BITS>*>(a.cache_v)[at] = write_block<BITS>(v, vs);
+    if ((piece & 3) == 0) {
+      reinterpret_cast<unsigned char*>(a.k_scales)[at >> 2] = (unsigned char)ks;
+      reinterpret_cast<unsigned char*>(a.v_scales)[at >> 2] = (unsigned char)vs;
+    }
   }
 }
 
@@ -142,7 +142,7 @@ hipError_t launch_mx_dequant(const MxRowArgs& a, hipStream_t st) {
 template <typename T, int BITS, int D>
 static hipError_t launch_fill(const FillArgs& a, hipStream_t st) {
   constexpr int rows = kRowThreads / (D / 8);
-  const dim3 grid((a.C + rows - 1) / rows, a.B * a.Hkv);
+  const dim3 grid(std::min((a.C + rows - 1) / rows, 1 << 16), a.B * a.Hkv);
   return a.cache_w ? launch_kernel<0>(mx_fill_kernel<T, BITS, D, true>, grid, kRowThreads, a, st)
                    : launch_kernel<0>(mx_fill_kernel<T, BITS, D, false>, grid, kRowThreads, a, st);
 }

@@ -450,6 +450,59 @@ def test_eviction_in_joined_ranges(bits, Hq, D, C, empty, dt):
     one_eviction(1, Hq, 2, D, C, bits, dt, empty=empty)
 
 
+def test_slots_by_ties_specials_and_repeats():
+    """The slot rule of the cache of plain rows: both caches give the same slots, positions and, for one live token, weight."""
+    B, Hkv, D, C = 1, 1, 64, 6
+    q, k, v = normal((B, 1, D), "bf16", 1), normal((B, 1, D), "bf16", 2), normal((B, 1, D), "bf16", 3)
+    for w, held, pos in (([0.0, 2.0, 1.0, 1.0, 5.0, 0.0], [0, 1, 2, 3, 4, 9], 10), ([0.0, math.nan, 7.0, math.inf, 8.0, 0.0], [0, 1, 2, 3, 4, 9], 10),
+                         ([0.0, 2.0, -0.0, 0.0, 5.0, 0.0], [0, 1, 2, 3, 4, 9], 10), ([0.0, 2.0, 1.0, -3.0, 5.0, 0.0], [0, 1, 2, 3, 4, 9], 10),
+                         ([9.0, 0.0, 1.0, 1.0, 5.0, 0.0], [0, 1, -1, -7, 4, 9], 10), ([9.0, 0.0, 1.0, 1.0, 5.0, 0.0], [0, 10, -1, -7, 4, 9], 10)):
+        plain, coded = carve.budget_cache(B, Hkv, D, C), carve.budget_cache_mx(B, Hkv, D, C)
+        for cw, cp in (plain[2:], coded[4:]):
+            cw.copy_(torch.tensor(w).view(1, 1, C))
+            cp.copy_(torch.tensor(held, dtype=torch.int32).view(1, 1, C))
+        one = carve.budget_decode(q, k, v, plain, ints([pos]), sinks=1, recent=2)[1]
+        two = carve.budget_decode_mx(q, k, v, coded, ints([pos]), sinks=1, recent=2)[1]
+        assert torch.equal(one, two) and torch.equal(plain[3], coded[5])
+    cache = carve.budget_cache_mx(B, Hkv, D, C)
+    for _ in range(3):                        # the call repeated stores the token once
+        _, slot = carve.budget_decode_mx(q, k, v, cache, ints([0]), sinks=1, recent=2)
+        assert int(slot) == 0
+    assert cache[5][0, 0].tolist() == [0, -1, -1, -1, -1, -1] and float(cache[4][0, 0, 0]) == 1.0
+
+
+@pytest.mark.parametrize("C", [70, 5000])
+def test_rows_without_a_token(C):
+    """Rows with a negative position (in one range and in several): output zero, slot -1, the cache as it was."""
+    B, Hq, Hkv, D = 3, 4, 2, 128
+    ring = [torch.randint(0, 255, x.shape, dtype=torch.uint8, device="cuda") for x in carve.swa_cache_mx(B, Hkv, D, C)]
+    kept = tuple(x.clone() for x in ring) + (torch.rand(B, Hkv, C, device="cuda"), torch.arange(C, dtype=torch.int32, device="cuda").repeat(B, Hkv, 1))
+    q, k, v = normal((B, Hq, D), "bf16", 1), normal((B, Hkv, D), "bf16", 2), normal((B, Hkv, D), "bf16", 3)
+    pos, before = ints([-1, 2 * C, -2147483648]), [x.clone() for x in kept]
+    o = torch.full_like(q, 5.0)
+    assert carve.swa_decode_mx(q, k, v, ring, pos, C, o=o) is o
+    o2, slot = carve.budget_decode_mx(q, k, v, kept, pos, recent=3, o=torch.full_like(q, 5.0))
+    for b in (0, 2):
+        assert not o[b].any() and not o2[b].any() and (slot[b] == -1).all()
+        assert all(torch.equal(x[b], y[b]) for x, y in zip(ring, before)) and all(torch.equal(x[b], y[b]) for x, y in zip(kept, before))
+    assert o[1].any() and (slot[1] >= 0).all()
+
+
+def test_written_in_bf16_read_in_float32():
+    """A cache has no type of its own: a bf16 prompt's, with float32 tokens on it, and a scale of the caller's."""
+    B, Hq, Hkv, T, D, W = 1, 6, 2, 40, 64, 50
+    k, v = normal((B, Hkv, T, D), "bf16", 1), normal((B, Hkv, T, D), "bf16", 2)
+    ring = carve.swa_cache_mx(B, Hkv, D, W, bits=8)
+    carve.swa_fill_mx(k, v, ring, W)
+    q1, k1, v1 = normal((B, Hq, D), "f32", 3), normal((B, Hkv, D), "f32", 4), normal((B, Hkv, D), "f32", 5)
+    o = carve.swa_decode_mx(q1, k1, v1, ring, ints([T]), W, scale=0.37)
+    assert o.dtype == torch.float32
+    live = torch.ones(T + 1, dtype=torch.bool, device="cuda")
+    for g in range(Hq):
+        kk, vv = (torch.cat([mx_ref.written(x[0, g // 3], 8)[0], mx_ref.written(y[0, g // 3][None], 8)[0]]).cuda() for x, y in ((k, k1), (v, v1)))
+        ref.within(o[0, g], mx_ref.rows(q1[0, g], kk, vv, live, 0.37)[:2], f"head {g}")
+
+
 # ------------------------------------------------------------------ as they are used
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_decode_in_a_graph_follows_the_positions(dt):
