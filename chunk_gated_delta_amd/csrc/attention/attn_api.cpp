@@ -198,11 +198,18 @@ carve_status check_budget(const carve_budget_shape* s) {
 // compute unit's only one anyway, up to one a unit or by the LDS that its rows take at D = 128.  At D = 64
 // two fit, and the scores' 16 KB would keep the second off: 300 key heads of 1,024 slots 26.5 us with
 // them in LDS, 22.0 without, 480 of 512 slots 20.5 and 16.6 (one sequence of four heads 13.4 and 14.9).
-// (Rows of codes have 8 waves up to 256 key heads only, in either type, and up to 32 heads a group.)
-bool near_scores(const carve_budget_shape* s, int bits, int n_split, int waves) {
+bool plain_near_scores(const carve_budget_shape* s, int n_split, int waves) {
   const long long G = s->Hq / s->Hkv;
-  return (bits || s->dtype == CARVE_BF16) && n_split == 1 && waves == 8 && (s->D == 128 || s->B * s->Hkv <= 256) && G <= (bits ? 32 : 16) &&
-         G * carve::score_row(s->C) <= (bits ? carve::mx_near_scores(bits, s->D) : carve::kNearScores);
+  return s->dtype == CARVE_BF16 && n_split == 1 && waves == 8 && (s->D == 128 || s->B * s->Hkv <= 256) && G <= 16 &&
+         G * carve::score_row(s->C) <= carve::kNearScores;
+}
+// The same for rows of codes: workgroups of 8 waves are one a compute unit at most; of 4, up to two are that few
+// (64 / 128 / 256 sequences of 2,048 slots, 16 heads on 4: 20.8 / 37 us in LDS, 24 / 41 without; 73 without, 74 in LDS).
+bool near_scores(const carve_budget_shape* s, int bits, int n_split, int waves) {
+  if (!bits) return plain_near_scores(s, n_split, waves);
+  const long long G = s->Hq / s->Hkv;
+  return n_split == 1 && (waves == 8 || s->B * s->Hkv <= 512) && G <= (waves == 8 ? 32 : 16) &&
+         G * carve::score_row(s->C) <= carve::mx_near_scores(bits, s->D, waves);
 }
 
 // A cache as the calls give it: rows of the call's dtype, or codes and scales.

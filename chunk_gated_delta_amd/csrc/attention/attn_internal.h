@@ -80,8 +80,11 @@ struct CacheArgs {
 __host__ __device__ constexpr int score_row(int C) { return (C + 3) & ~3; }
 constexpr int kNearScores = 4096;      // most scores of a key head that stay in LDS (bf16, one workgroup of 8 waves)
 
-// the same for rows of codes, beside the LDS that those take
-__host__ __device__ constexpr int mx_near_scores(int bits, int D) { return bits == 8 && D == 128 ? 4096 : 16384; }
+// the same for rows of codes, with a workgroup of 8 waves a compute unit or two of 4, beside the LDS that those take
+// (8 bits at D = 128 leave none to two)
+__host__ __device__ constexpr int mx_near_scores(int bits, int D, int waves) {
+  return bits == 8 && D == 128 ? (waves == 8 ? 4096 : 4) : waves == 8 ? 16384 : 8192;
+}
 
 // Rows of k and v copied into a cache.
 struct FillArgs {

@@ -2,12 +2,21 @@
 // and the cache kept by attention weight, with the split, the softmax and the joins of cache_decode.hip.
 //
 // What codes stand for is a bf16 exactly, so both products run on bf16 operands; where q is float32, q
-// and the weights go in as three bf16 parts each, which hold all their bits.  Cached rows go from
-// memory to registers without LDS: a lane's contraction elements of S^T = K Q^T may come in any order
-// that q's have too, so it takes D / 4 neighbouring elements of its key, with one scale; for O^T = V^T P^T it
-// takes D / 16 neighbouring elements of each of its eight slots and pairs the slots up as it converts.
-// The token's own row goes into the registers of the wave that holds its slot as well as
-// to the cache, so no wave waits for a store.
+// and the weights go in as three bf16 parts each, which hold all their bits (256 sequences, 16 heads on 4, window 4,096,
+// 4 bits: 127 us, bf16 108).  Codes reach LDS by loads that write it directly; a lane converts what it reads from there.
+// The contraction of S^T = K Q^T may run over a key's elements in any order that q's have too, so a lane takes D / 4
+// neighbouring ones, with one scale; for O^T = V^T P^T it takes D / 16 neighbouring elements of each of its eight
+// slots and pairs the slots up as it converts.  The token's own row is written over its place in LDS by the wave that
+// holds its slot, as well as to the cache, so no wave waits for a store.
+//
+// Bound by the cache's read where there are many key heads: 542 MB of a padded batch of 256 sequences (above) in 89 us,
+// 6.1 TB/s, what a plain read of as much has (88 us); 558 MB of full ones again and again 108 us.  The vector units
+// are busy for 0.43 of the time (conversions, their pairing, exponentials), the matrix units for 0.14; without the
+// value products, or without exponentials, the time is the same.  With few key heads it is latency:
+// 4 of 1,028 slots 8.6 us, about 5 of them before and after the slots, 0.9 a step of 256 slots.  With weights
+// 64 sequences of 2,048 slots 20 us (the slot's search before, the weights after the steps); 256 of 4,096 139 us:
+// the scores' way to memory and back, 134 MB, beside 557 MB of codes.  More than 32 float32 heads of D = 128
+// on a key head do not fit the registers (64 heads on one: 137 us where bf16 takes 39).
 #include <algorithm>
 
 #include "cache_step.h"
@@ -40,10 +49,10 @@ __device__ __forceinline__ void bf16_parts(const float (&x)[8], Frag<bf16> (&f)[
 }
 
 // 32 slots of a wave in LDS, where buffer loads that write it directly put them (the scales come through a
-// register each).  Such loads fill LDS in lane order, 16 bytes a lane; which row they come from is free:
-// keys: lane (lr, lg) reads back what it brought, elements lg D / 4 .. of slots lr and 16 + lr (4 bits and
-// D = 64, 8 bytes a key: rows in order); values: rows 4 lg + i stand at i-major places of their 16, so that the
-// lanes' elements lr D / 16 .. of slots 4 lg + i, one i a read, are neighbours.  No bank conflicts either way.
+// register each).  Such loads fill LDS in lane order, 16 bytes a lane; which row they come from is free.
+// Keys stand row by row, the 16-byte pieces of a row swizzled: lane (lr, lg) reads elements lg D / 4 .. of slots lr and
+// 16 + lr, sixteen rows at one piece.  Of each 16 values, rows 4 lg + i stand at places 4 i + lg: lanes
+// (lr, lg) read elements lr D / 16 .. of slots 4 lg + i, one i at a time, which are then neighbours.
 template <int BITS, int D>
 struct MxTile {
   static constexpr int RB = D * BITS / 8, SB = D / 32;                  // bytes of a row, of its scales
@@ -238,7 +247,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
   __shared__ float st[16 * NT][2];
   __shared__ __align__(16) u32 fresh[2][RB / 4];                 // the token's k and v
   __shared__ unsigned char fresh_scale[2][SB];
-  __shared__ __align__(16) float near_score[NEAR ? mx_near_scores(BITS, D) : 4];
+  __shared__ __align__(16) float near_score[NEAR ? mx_near_scores(BITS, D, NW) : 4];
   const int G = a.Hq / a.Hkv;
   const int split = uniform(blockIdx.x % a.n_split), bk = uniform(blockIdx.x / a.n_split), b = uniform(bk / a.Hkv);
   const int lane = lane_id(), wave = wave_uid(), lr = lane & 15, lg = lane >> 4;
@@ -561,6 +570,8 @@ static hipError_t launch_nt(const CacheArgs& a, hipStream_t st) {
     e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, N8, 8, BUDGET, BUDGET>, grid, 512, a, st);
   else if (NT < 4 && a.waves == 8)
     e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, N8, 8, BUDGET, false>, grid, 512, a, st);
+  else if (NT == 1 && BUDGET && !a.score)
+    e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, 1, 4, BUDGET, BUDGET>, grid, kDecThreads, a, st);
   else
     e = launch_kernel<0>(mx_decode_kernel<T, BITS, D, NT, 4, BUDGET, false>, grid, kDecThreads, a, st);
   if (e != hipSuccess || a.n_split == 1) return e;

@@ -101,7 +101,7 @@ def main(argv=None):
 
 def attention(args, wl, dev):
     """The attention operators at the workload's batch, heads (four query heads a key head), length and
-    width: window T / 4, four sinks, caches of T / 2 slots."""
+    width: window T / 4, four sinks, caches of T / 2 slots, as rows and in codes of 4 bits."""
     import torch
     from chunk_gated_delta_amd import carve
     B, Hq, T, D, Bd = wl.B, wl.H, wl.T, wl.Dk, args.decode_batch
@@ -117,15 +117,29 @@ def attention(args, wl, dev):
     pos = torch.full((Bd,), T, dtype=torch.int32, device=dev)
     cache = (normal(Bd, Hkv, C, D), normal(Bd, Hkv, C, D), torch.rand(Bd, Hkv, C, generator=gen, device=dev),
              torch.arange(C, dtype=torch.int32, device=dev).repeat(Bd, Hkv, 1))
+    # both caches in codes of 4 bits
+    ring4, cache4 = carve.swa_cache_mx(Bd, Hkv, D, window, sinks), carve.budget_cache_mx(Bd, Hkv, D, C)
+    for codes, rows in ((ring4, ring), (cache4, cache)):
+        for i in (0, 1):
+            carve.mx_quant(rows[i], codes=codes[2 * i], scales=codes[2 * i + 1])
+    cache4[4].copy_(cache[2])
+    cache4[5].copy_(cache[3])
+    prompt4 = carve.swa_cache_mx(B, Hkv, D, window, sinks)
     print(f"[profile_step] attention inputs ready: B{B} Hq{Hq} Hkv{Hkv} T{T} d{D} window {window}, "
           f"decode batch {Bd}, {C} slots", flush=True)
     for _ in range(args.warmup + args.steps):
         o, lse = carve.swa_fwd(q, k, v, window, sinks=sinks)
         carve.swa_bwd(q, k, v, o, lse, dO, window, sinks=sinks)
         _, lse = carve.swa_fwd(q, k, v, T)
-        carve.budget_keep(k, v, carve.budget_weights(q, k, lse), C, sinks=sinks, recent=C // 4)
+        weights = carve.budget_weights(q, k, lse)
+        carve.budget_keep(k, v, weights, C, sinks=sinks, recent=C // 4)
+        carve.budget_keep_mx(k, v, weights, C, sinks=sinks, recent=C // 4)
+        carve.swa_fill_mx(k, v, prompt4, window, sinks=sinks)
+        carve.mx_dequant(*prompt4[:2])
         carve.swa_decode(q1, k1, v1, *ring, pos, window, sinks=sinks)
         carve.budget_decode(q1, k1, v1, cache, pos, sinks=sinks, recent=C // 4)
+        carve.swa_decode_mx(q1, k1, v1, ring4, pos, window, sinks=sinks)
+        carve.budget_decode_mx(q1, k1, v1, cache4, pos, sinks=sinks, recent=C // 4)
     torch.cuda.synchronize()
     print(f"[profile_step] attention: {args.warmup} warm-up + {args.steps} steps", flush=True)
     return 0
