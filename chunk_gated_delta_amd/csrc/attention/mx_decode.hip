@@ -9,14 +9,14 @@
 // slots and pairs the slots up as it converts.  The token's own row is written over its place in LDS by the wave that
 // holds its slot, as well as to the cache, so no wave waits for a store.
 //
-// Bound by the cache's read where there are many key heads: 542 MB of a padded batch of 256 sequences (above) in 89 us,
-// 6.1 TB/s, what a plain read of as much has (88 us); 558 MB of full ones again and again 108 us.  The vector units
-// are busy for 0.43 of the time (conversions, their pairing, exponentials), the matrix units for 0.14; without the
-// value products, or without exponentials, the time is the same.  With few key heads it is latency:
-// 4 of 1,028 slots 8.6 us, about 5 of them before and after the slots, 0.9 a step of 256 slots.  With weights
-// 64 sequences of 2,048 slots 20 us (the slot's search before, the weights after the steps); 256 of 4,096 139 us:
-// the scores' way to memory and back, 134 MB, beside 557 MB of codes.  More than 32 float32 heads of D = 128
-// on a key head do not fit the registers (64 heads on one: 137 us where bf16 takes 39).
+// Bound by the cache's read where there are many key heads: 256 sequences as above, some still filling (about 540 MB),
+// in 89 to 104 us, 5.2 to 6.1 TB/s; a plain read of as much takes 88.  The vector units are then busy for 0.58 of the time
+// (conversions, their pairing, exponentials), the matrix units for 0.15; without the value products, or without
+// exponentials, the time is the same.  With few key heads it is latency: 4 of 1,028 slots 8.6 us, about 5 of
+// them before and after the slots, 0.9 a step of 256 slots.  With weights 64 sequences of 2,048 slots 20 us (the
+// slot's search before, the weights after the steps); 256 of 4,096 slots 137 us: the scores' way to memory and
+// back, 134 MB, beside 570 MB of rows.  More than 32 float32 heads of D = 128 on a key head do not fit the registers
+// (64 heads on one: 137 us where bf16 takes 39).
 #include <algorithm>
 
 #include "cache_step.h"

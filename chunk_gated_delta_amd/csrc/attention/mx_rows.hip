@@ -6,7 +6,8 @@
 // loads and stores marked so; codes, which the next kernel reads, keep their places in the caches:
 // 67 M values to 8 bits and back 63 us (73 after other work has filled the caches; unmarked 69 and 98), the
 // ring of 32 sequences of 8,192 tokens, 4 key heads, window 4,096, 4 bits, written and read back 110 us
-// (122; unmarked 136 and 160; codes marked too 120 and 129), 5.5 TB/s of 5.9 that a copy has.
+// (122; unmarked 136 and 160; codes marked too 120 and 129).  Both move 400 and 680 MB, at 5.9 TB/s, a copy's rate, in 69
+// and 115 us: part of the codes is read back from the last-level cache.
 #include <algorithm>
 
 #include "mx_device.h"

@@ -537,6 +537,39 @@ def test_decode_in_a_graph_follows_the_positions(dt):
         pos += 1
 
 
+def test_joined_ranges_in_two_graphs():
+    """Two captured graphs of steps on long caches (a workspace each, of the graph's own memory), replayed in turn with
+    positions that go on and eager work between, against the same steps run eagerly."""
+    D, C, Hq, Hkv = 128, 5001, 8, 2
+    graphs = []
+    for seed in (0, 50):
+        ring = sum((carve.mx_quant(normal((1, Hkv, C, D), "bf16", seed + i)) for i in range(2)), ())
+        kept = tuple(x.clone() for x in ring) + (torch.rand(1, Hkv, C, generator=torch.Generator().manual_seed(seed)).cuda(),
+                                                torch.arange(C, dtype=torch.int32, device="cuda").repeat(1, Hkv, 1))
+        q, k, v = normal((1, Hq, D), "bf16", seed + 2), normal((1, Hkv, D), "bf16", seed + 3), normal((1, Hkv, D), "bf16", seed + 4)
+        pos = ints([C])
+
+        def step(ring, kept, q=q, k=k, v=v, pos=pos):
+            return (carve.swa_decode_mx(q, k, v, ring, pos, C), *carve.budget_decode_mx(q, k, v, kept, pos, sinks=2, recent=9))
+
+        mirror = [x.clone() for x in ring], tuple(x.clone() for x in kept)
+        g = torch.cuda.CUDAGraph()
+        step([x.clone() for x in ring], tuple(x.clone() for x in kept))
+        with torch.cuda.graph(g):
+            got = step(ring, kept)
+        graphs.append((g, step, got, ring, kept, mirror, pos))
+    for i in range(4):
+        for g, *_ in graphs:
+            g.replay()
+        torch.zeros(1 << 20, device="cuda").sum()
+        for g, step, got, ring, kept, mirror, pos in graphs:
+            want = step(*mirror)
+            torch.cuda.synchronize()
+            for a, b in zip(list(got) + list(ring) + list(kept), list(want) + list(mirror[0]) + list(mirror[1])):
+                assert torch.equal(a, b), i
+            pos += 1
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with caches and workspaces of its own, give the bits of the same calls one after the other."""
     D, window, C, Hq, Hkv = 128, 9000, 9000, 8, 2
