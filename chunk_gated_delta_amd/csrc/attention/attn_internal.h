@@ -83,7 +83,7 @@ constexpr int kNearScores = 4096;      // most scores of a key head that stay in
 // the same for rows of codes, with a workgroup of 8 waves a compute unit or two of 4, beside the LDS that those take
 // (8 bits at D = 128 leave none to two)
 __host__ __device__ constexpr int mx_near_scores(int bits, int D, int waves) {
-  return bits == 8 && D == 128 ? (waves == 8 ? 4096 : 4) : waves == 8 ? 16384 : 8192;
+  return bits == 8 && D == 128 ? (waves == 8 ? 4096 : 4) : waves == 8 ? 20480 : 8192;
 }
 
 // Rows of k and v copied into a cache.

@@ -437,7 +437,7 @@ def one_eviction(B, Hq, Hkv, D, C, bits, dt, sinks=4, recent=20, empty=0):
 @pytest.mark.parametrize("empty", [0, 5])
 @pytest.mark.parametrize("B,Hq,Hkv,D,C", [
     (1, 8, 2, 128, 500), (1, 2, 1, 64, 1023), (2, 16, 1, 128, 250), (1, 8, 2, 64, 2049), (1, 34, 1, 64, 700),
-    (1, 128, 2, 128, 333), (75, 16, 4, 64, 500), (75, 8, 4, 128, 130), (150, 40, 4, 64, 140), (140, 4, 2, 128, 301), (130, 24, 4, 64, 260)])
+    (1, 128, 2, 128, 333), (75, 16, 4, 64, 500), (75, 8, 4, 128, 130), (150, 40, 4, 64, 140), (140, 4, 2, 128, 301), (130, 24, 4, 64, 260), (1, 40, 2, 64, 1024), (1, 16, 1, 128, 1281)])
 def test_eviction(B, Hq, Hkv, D, C, empty, bits, dt):
     """Small caches of few and many key heads, scores near and far."""
     one_eviction(B, Hq, Hkv, D, C, bits, dt, empty=empty)
