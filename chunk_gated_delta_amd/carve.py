@@ -8,6 +8,7 @@ or a call is rejected, a RuntimeError is raised.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -716,9 +717,13 @@ def _swa_shape(q, k, ndim, window, sinks, scale):
     return B, Hq, Hkv, T, D, dev, dt, s, ctypes.byref(s)
 
 
-def _workspace(what, s, dev, workspace, *more):
+def _workspace(what, s, dev, workspace):
     """(workspace kept alive, its address, its bytes) for a call that needs one."""
-    need = getattr(load_library(), what)(s, *more)
+    return _room(getattr(load_library(), what)(s), dev, workspace)
+
+
+def _room(need, dev, workspace):
+    """The same for a call that needs so many bytes."""
     if workspace is not None:
         if workspace.device != dev:
             raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
@@ -974,15 +979,30 @@ def swa_fill_mx(k, v, cache, window, sinks=0, lens=None):
           _fit_opt(lens, "lens", (B,), torch.int32, dev), ctypes.byref(rows))
 
 
+# What a decode step's call needs beyond its tensors, by its sizes alone: (the shape's address, bytes of workspace).
+@functools.lru_cache(maxsize=1024, typed=True)
+def _swa_decode_mx_plan(B, Hq, Hkv, D, window, sinks, scale, dtype, bits):
+    s = ctypes.byref(carve_swa_shape(B, Hq, Hkv, 1, D, window, sinks, D ** -0.5 if scale is None else scale, dtype))
+    return s, load_library().carve_swa_decode_mx_workspace_size(s, bits)
+
+
+@functools.lru_cache(maxsize=1024, typed=True)
+def _budget_decode_mx_plan(B, Hq, Hkv, D, C, sinks, recent, scale, dtype, bits):
+    s = ctypes.byref(carve_budget_shape(B, Hq, Hkv, 1, D, C, sinks, recent, D ** -0.5 if scale is None else scale, dtype))
+    return s, load_library().carve_budget_decode_mx_workspace_size(s, bits)
+
+
 def swa_decode_mx(q, k, v, cache, pos, window, sinks=0, scale=None, o=None, workspace=None):
     """swa_decode on a ring cache as swa_cache_mx makes it: the new token's k, v are written in codes and
     scales first, and attended to as written; o [B,Hq,D] of q's type."""
-    B, Hq, Hkv, _, D, dev, dt, s, sp = _swa_shape(q, k, 3, window, sinks, scale)
+    _whole(window=window, sinks=sinks)
+    B, Hq, Hkv, _, D, dev, dt = _heads(q, k, 3)
     kv, rows = (B, Hkv, D), _mx_rows(cache, B, Hkv, window + sinks, D, dev)
+    sp, need = _swa_decode_mx_plan(B, Hq, Hkv, D, window, sinks, scale, _dtype_code(q), rows.bits)
     ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev), ctypes.byref(rows),
             _fit(pos, "pos", (B,), torch.int32, dev))
     o, to_o = _given_as(o, "o", q)
-    workspace, ws, nbytes = _workspace("carve_swa_decode_mx_workspace_size", sp, dev, workspace, rows.bits)
+    workspace, ws, nbytes = _room(need, dev, workspace)
     _call("carve_swa_decode_mx", dev, sp, *ptrs, to_o, ws, nbytes)
     return o
 
@@ -1016,15 +1036,15 @@ def budget_decode_mx(q, k, v, cache, pos, sinks=0, recent=1, scale=None, o=None,
     _whole(sinks=sinks, recent=recent)
     B, Hq, Hkv, _, D, dev, dt = _heads(q, k, 3)
     C = cache[0].shape[2]
-    s = carve_budget_shape(B, Hq, Hkv, 1, D, C, sinks, recent, D ** -0.5 if scale is None else scale, _dtype_code(q))
-    sp, kv, slots, rows = ctypes.byref(s), (B, Hkv, D), (B, Hkv), _mx_rows(cache[:4], B, Hkv, C, D, dev)
+    kv, slots, rows = (B, Hkv, D), (B, Hkv), _mx_rows(cache[:4], B, Hkv, C, D, dev)
+    sp, need = _budget_decode_mx_plan(B, Hq, Hkv, D, C, sinks, recent, scale, _dtype_code(q), rows.bits)
     cache_w, cache_pos = cache[4:]
     ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev), ctypes.byref(rows),
             _fit(cache_w, "cache_w", (B, Hkv, C), torch.float32, dev),
             _fit(cache_pos, "cache_pos", (B, Hkv, C), torch.int32, dev), _fit(pos, "pos", (B,), torch.int32, dev))
     o, to_o = _given_as(o, "o", q)
     slot, to_slot = _given(slot, "slot", slots, torch.int32, pos)
-    workspace, ws, nbytes = _workspace("carve_budget_decode_mx_workspace_size", sp, dev, workspace, rows.bits)
+    workspace, ws, nbytes = _room(need, dev, workspace)
     _call("carve_budget_decode_mx", dev, sp, *ptrs, to_o, to_slot, ws, nbytes)
     return o, slot
 

@@ -160,7 +160,7 @@ void split_plan(int units, int C, int row_bytes, int* n_split, int* split_len, i
 // 128 of 2,052 / 4,100 / 8,196 slots 13.8 / 22 / 39 and 14.7 / 19.5 / 34, with weights 20 / 32 / 55
 // and 23 / 34 / 55; 256 not at any length.  (A caller that launches each step anew pays the second launch's 4 us too.)
 void mx_split_plan(int units, int C, bool weights, int* n_split, int* split_len, int* waves) {
-  const int most = units <= 64 ? 1536 : weights ? 8192 : 3072;      // slots of one workgroup
+  const int most = units <= 64 ? 1536 : weights ? 8192 : 3000;      // slots of one workgroup
   int n = 1;
   *waves = units <= 256 ? 8 : 4;
   if (units < 256 && C > most) {

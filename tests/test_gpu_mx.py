@@ -488,6 +488,29 @@ def test_rows_without_a_token(C):
     assert o[1].any() and (slot[1] >= 0).all()
 
 
+def test_most_key_heads():
+    """65,535 sequences of one head, the most that a call takes: prompt, read back and one token, all rows checked."""
+    B, D, W, T = 65535, 64, 4, 3
+    k, v = normal((B, 1, T, D), "bf16", 1), normal((B, 1, T, D), "bf16", 2)
+    ring = carve.swa_cache_mx(B, 1, D, W)
+    carve.swa_fill_mx(k, v, ring, W)
+    q1, k1, v1 = normal((B, 1, D), "bf16", 3), normal((B, 1, D), "bf16", 4), normal((B, 1, D), "bf16", 5)
+    kk, vv = (torch.cat([mx_ref.written(x.view(-1, D), 4)[0].view(B, T, D), mx_ref.written(y.view(-1, D), 4)[0].view(B, 1, D)], 1).cuda()
+              for x, y in ((k, k1), (v, v1)))
+    assert torch.equal(carve.mx_dequant(*ring[:2], dtype=torch.float32)[:, 0, :T].double(), kk[:, :T])
+    o = carve.swa_decode_mx(q1, k1, v1, ring, torch.full((B,), T, dtype=torch.int32, device="cuda"), W)
+    kept = carve.budget_keep_mx(k, v, torch.ones(B, 1, T, device="cuda"), W)
+    o2, slot = carve.budget_decode_mx(q1, k1, v1, kept, torch.full((B,), T, dtype=torch.int32, device="cuda"))
+    assert (slot == T).all() and torch.equal(o2, o)
+    p = torch.softmax((kk * q1.double()).sum(-1) * D ** -0.5, -1)[..., None]
+    want, size = (p * vv).sum(1), (p * vv.abs()).sum(1)
+    A = (kk.abs() * q1.double().abs()).sum(-1).amax() * D ** -0.5
+    u = ref.half_step(torch.bfloat16)
+    ref.within(o[:, 0], (want, (2 * ref.F32 * (2 * (D + 4) * A + W + 32) + u) * size + u * want.abs()), "o")
+    for x, y in zip(ring, kept):
+        assert torch.equal(x, y)
+
+
 def test_written_in_bf16_read_in_float32():
     """A cache has no type of its own: a bf16 prompt's, with float32 tokens on it, and a scale of the caller's."""
     B, Hq, Hkv, T, D, W = 1, 6, 2, 40, 64, 50
