@@ -9,6 +9,7 @@ or a call is rejected, a RuntimeError is raised.
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -980,6 +981,7 @@ def swa_fill_mx(k, v, cache, window, sinks=0, lens=None):
 
 
 # What a decode step's call needs beyond its tensors, by its sizes alone: (the shape's address, bytes of workspace).
+# The arguments are plain numbers: a tensor that holds one would be found again after it has changed.
 @functools.lru_cache(maxsize=1024, typed=True)
 def _swa_decode_mx_plan(B, Hq, Hkv, D, window, sinks, scale, dtype, bits):
     s = ctypes.byref(carve_swa_shape(B, Hq, Hkv, 1, D, window, sinks, D ** -0.5 if scale is None else scale, dtype))
@@ -998,7 +1000,8 @@ def swa_decode_mx(q, k, v, cache, pos, window, sinks=0, scale=None, o=None, work
     _whole(window=window, sinks=sinks)
     B, Hq, Hkv, _, D, dev, dt = _heads(q, k, 3)
     kv, rows = (B, Hkv, D), _mx_rows(cache, B, Hkv, window + sinks, D, dev)
-    sp, need = _swa_decode_mx_plan(B, Hq, Hkv, D, window, sinks, scale, _dtype_code(q), rows.bits)
+    sp, need = _swa_decode_mx_plan(B, Hq, Hkv, D, operator.index(window), operator.index(sinks), None if scale is None else float(scale),
+                                   _dtype_code(q), rows.bits)
     ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev), ctypes.byref(rows),
             _fit(pos, "pos", (B,), torch.int32, dev))
     o, to_o = _given_as(o, "o", q)
@@ -1037,7 +1040,8 @@ def budget_decode_mx(q, k, v, cache, pos, sinks=0, recent=1, scale=None, o=None,
     B, Hq, Hkv, _, D, dev, dt = _heads(q, k, 3)
     C = cache[0].shape[2]
     kv, slots, rows = (B, Hkv, D), (B, Hkv), _mx_rows(cache[:4], B, Hkv, C, D, dev)
-    sp, need = _budget_decode_mx_plan(B, Hq, Hkv, D, C, sinks, recent, scale, _dtype_code(q), rows.bits)
+    sp, need = _budget_decode_mx_plan(B, Hq, Hkv, D, C, operator.index(sinks), operator.index(recent), None if scale is None else float(scale),
+                                      _dtype_code(q), rows.bits)
     cache_w, cache_pos = cache[4:]
     ptrs = (q.data_ptr(), _fit(k, "k", kv, dt, dev), _fit(v, "v", kv, dt, dev), ctypes.byref(rows),
             _fit(cache_w, "cache_w", (B, Hkv, C), torch.float32, dev),

@@ -488,6 +488,27 @@ def test_rows_without_a_token(C):
     assert o[1].any() and (slot[1] >= 0).all()
 
 
+def test_numbers_held_by_tensors():
+    """A scale given as a tensor counts as it is at the call, and so do window and sinks; other numbers are refused."""
+    q, k, v = normal((1, 2, 64), "bf16", 1), normal((1, 1, 64), "bf16", 2), normal((1, 1, 64), "bf16", 3)
+    ring = carve.mx_quant(normal((1, 1, 12, 64), "bf16", 4)) + carve.mx_quant(normal((1, 1, 12, 64), "bf16", 5))
+    pos, scale, window, sinks = ints([30]), torch.tensor(0.5), torch.tensor(10), torch.tensor(2)
+
+    def step(scale, window=10, sinks=2):
+        return carve.swa_decode_mx(q, k, v, [x.clone() for x in ring], pos, window, sinks=sinks, scale=scale)
+
+    assert torch.equal(step(scale, window, sinks), step(0.5))
+    scale.fill_(0.125)
+    window.fill_(9)
+    sinks.fill_(3)
+    assert torch.equal(step(scale, window, sinks), step(0.125, 9, 3)) and not torch.equal(step(0.125), step(0.5))
+    with pytest.raises(TypeError):
+        step(0.5, 10.0)
+    for bad in (0.0, -1.0, math.nan, math.inf):
+        with pytest.raises(RuntimeError):
+            step(bad)
+
+
 def test_most_key_heads():
     """65,535 sequences of one head, the most that a call takes: prompt, read back and one token, all rows checked."""
     B, D, W, T = 65535, 64, 4, 3
