@@ -3,7 +3,10 @@
 //
 // What codes stand for is a bf16 exactly, so both products run on bf16 operands; where q is float32, q
 // and the weights go in as three bf16 parts each, which hold all their bits (256 sequences, 16 heads on 4, window 4,096,
-// 4 bits: 127 us, bf16 108).  Codes reach LDS by loads that write it directly; a lane converts what it reads from there.
+// 4 bits: 127 us, bf16 110).  With bf16 queries the weights are two parts: rounded to one, the largest weight of a row would be
+// off by as much as the output's own rounding, and the error of a step's output half as large again.  (One part: 108 us;
+// 4 key heads of 1,028 slots 8.6 us, two parts 9.2; 64 heads on one, 2,048 slots 39 and 45.)
+// Codes reach LDS by loads that write it directly; a lane converts what it reads from there.
 // The contraction of S^T = K Q^T may run over a key's elements in any order that q's have too, so a lane takes D / 4
 // neighbouring ones, with one scale; for O^T = V^T P^T it takes D / 16 neighbouring elements of each of its eight
 // slots and pairs the slots up as it converts.  The token's own row is written over its place in LDS by the wave that
@@ -24,28 +27,27 @@
 
 namespace carve {
 
-// x as N bf16 parts that add up to it (N = 1: rounded; 3: all bits of a float)
+// x as N bf16 parts that add up to it (N = 2: but for 2^-15 of it, the second part's rounding; 3: all bits of a float)
 template <int N>
 __device__ __forceinline__ void bf16_parts(const float (&x)[8], Frag<bf16> (&f)[N]) {
-  if constexpr (N == 1) {
+  u32 w[N][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[0].v[j] = (bf16)x[j];
-  } else {
-    u32 w[N][4];
+  for (int j = 0; j < 8; j += 2) {
+    float a = x[j], b = x[j + 1];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      float a = x[j], b = x[j + 1];
-#pragma unroll
-      for (int n = 0; n < N; ++n) {               // the upper half of a float is a bf16; the rest is exact
-        const u32 ua = __builtin_bit_cast(u32, a), ub = __builtin_bit_cast(u32, b);
-        w[n][j / 2] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
-        a -= __builtin_bit_cast(float, ua & 0xffff0000u);
-        b -= __builtin_bit_cast(float, ub & 0xffff0000u);
+    for (int n = 0; n < N; ++n) {                 // the upper half of a float is a bf16; the rest is exact
+      if (N == 2 && n == 1) {
+        w[n][j / 2] = __builtin_bit_cast(u32, bf16x2{(bf16)a, (bf16)b});
+        break;
       }
+      const u32 ua = __builtin_bit_cast(u32, a), ub = __builtin_bit_cast(u32, b);
+      w[n][j / 2] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+      a -= __builtin_bit_cast(float, ua & 0xffff0000u);
+      b -= __builtin_bit_cast(float, ub & 0xffff0000u);
     }
-#pragma unroll
-    for (int n = 0; n < N; ++n) f[n].v = __builtin_bit_cast(bf16x8, u32x4{w[n][0], w[n][1], w[n][2], w[n][3]});
   }
+#pragma unroll
+  for (int n = 0; n < N; ++n) f[n].v = __builtin_bit_cast(bf16x8, u32x4{w[n][0], w[n][1], w[n][2], w[n][3]});
 }
 
 // 32 slots of a wave in LDS, where buffer loads that write it directly put them (the scales come through a
@@ -236,7 +238,7 @@ __device__ __forceinline__ float group_max(float x) {
 template <typename T, int BITS, int D, int NT, int NW, bool BUDGET, bool NEAR>
 __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) void mx_decode_kernel(CacheArgs a) {
   using Tile = MxTile<BITS, D>;
-  constexpr int STEP = 32 * NW, N = sizeof(T) == 2 ? 1 : 3, KK = D / 32, DT = D / 16;
+  constexpr int STEP = 32 * NW, N = sizeof(T) == 2 ? 1 : 3, NP = sizeof(T) == 2 ? 2 : 3, KK = D / 32, DT = D / 16;
   constexpr int RB = Tile::RB, SB = Tile::SB;
   constexpr int AHEAD = 2;                                       // steps whose rows are on their way or in use
   constexpr int BUFFERS = NW * AHEAD * Tile::kBytes, MERGE = NW * 16 * D * 4;
@@ -409,7 +411,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
     live[stage] = next;
     __builtin_amdgcn_sched_barrier(0);
     fetch_k(stage, j0 + AHEAD * STEP, rows_of(next));            // (behind the last slots: no rows)
-    Frag<bf16> P[NT][N];
+    Frag<bf16> P[NT][NP];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -446,7 +448,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
         y[j] = __builtin_amdgcn_exp2f(X[nt][j >> 2][j & 3] - m[nt]);
         l[nt] += y[j];
       }
-      bf16_parts<N>(y, P[nt]);                   // (bf16: rounded for the product with v, the sum l is not)
+      bf16_parts<NP>(y, P[nt]);
     }
     // V^T operands, two rows d of it at a time: two values of each of the eight slots, paired up by slot
     u32 v[8][Tile::VW];
@@ -477,7 +479,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int n = N - 1; n >= 0; --n) {
+        for (int n = NP - 1; n >= 0; --n) {
           mma(O[nt][2 * X2], F0, P[nt][n]);
           mma(O[nt][2 * X2 + 1], F1, P[nt][n]);
         }

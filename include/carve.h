@@ -579,8 +579,9 @@ typedef struct {
  * carve_swa_fill, carve_swa_decode, carve_budget_keep and carve_budget_decode on such caches; all other
  * arguments as there (q, k, v and o of shape->dtype).  k and v of the tokens are rounded as above
  * when they are written, the new token's too: it sees itself as the next ones will.  What a cache holds
- * enters the products exactly; q and, with float32, the weights are not rounded either (with bf16
- * the weights are, as in carve_swa_decode); parts of them below 2^-126 count as zero.
+ * enters the products exactly; q and, with float32, the weights are not rounded either (with bf16 the
+ * weights enter as two bf16 parts, off by less than 2^-15 of them: what carve_swa_decode rounds to bf16
+ * is not rounded here); parts of them below 2^-126 count as zero.
  * A key that is read as not a number gives all heads of its group a row that is not a number, a value the
  * 32 places of its block, and a query that is not finite its own row.
  */
