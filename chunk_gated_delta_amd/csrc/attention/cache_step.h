@@ -106,6 +106,8 @@ __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, i
 
 // Joins the ranges of one key head: the output (a workgroup per head of the group, its ranges'
 // partial sums read at once), and for a cache kept by weight the weights, a range of slots a workgroup.
+// The token sees itself, so a head's sum is 1 or more unless all its scores are -inf, as an infinite query
+// makes them: then it is zero, and its output and weights 0 / 0, not a number.
 constexpr int kMaxSplit = 64;
 template <typename T, int D, bool BUDGET>
 __global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
@@ -128,7 +130,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
     for (int o = 1; o < 64; o <<= 1) L += __shfl_xor(L, o);
     if (lane == 0) {
       st[g][0] = M;
-      st[g][1] = L != 0.f ? 1.f / L : 0.f;
+      st[g][1] = 1.f / L;
     }
     return x;
   };

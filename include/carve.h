@@ -480,6 +480,7 @@ carve_status carve_swa_bwd(const carve_swa_shape* s, const void* q, const void* 
  *       this row (o = 0, its cache stays as it is).  Read on the device, so a captured
  *       graph follows it; the caller advances it (one array serves every layer).
  * At most 64 query heads per key head (decode entry points).
+ * A query that is not finite gives its own row not a number.
  */
 carve_status carve_swa_fill(const carve_swa_shape* s, const void* k, const void* v, const int* lens, void* cache_k,
                             void* cache_v, void* stream);
@@ -539,6 +540,8 @@ carve_status carve_budget_keep(const carve_budget_shape* s, const void* k, const
  * slot's weight is its own p).
  *   q, k, v, pos, o as for carve_swa_decode; slot (device) [B,Hkv] int32 written: the
  *   slot taken, -1 for a row without a token
+ * A query or key that is not finite makes the weights of all live slots of its key head not a number, from
+ * then on: they count as the largest, so the next token takes the lowest slot that may be given up.
  */
 size_t carve_budget_decode_workspace_size(const carve_budget_shape* s);
 carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, const void* k, const void* v,
@@ -583,7 +586,8 @@ typedef struct {
  * weights enter as two bf16 parts, off by less than 2^-15 of them: what carve_swa_decode rounds to bf16
  * is not rounded here); parts of them below 2^-126 count as zero.
  * A key that is read as not a number gives all heads of its group a row that is not a number, a value the
- * 32 places of its block, and a query that is not finite its own row.
+ * 32 places of its block, and a query that is not finite its own row.  Cached weights are reached as in
+ * carve_budget_decode, by queries and keys.
  */
 carve_status carve_swa_fill_mx(const carve_swa_shape* s, const void* k, const void* v, const int* lens,
                                const carve_mx_rows* cache, void* stream);

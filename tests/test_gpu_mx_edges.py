@@ -1,5 +1,7 @@
-"""Decode steps on caches in codes where one rounding decides the result (tests/mx_ref.py states the definition and the
-bounds)."""
+"""Decode steps on caches in codes where results are decided by one rounding or one value: bf16
+weights, values that are not finite (tests/mx_ref.py states the definition and the bounds)."""
+import math
+
 import pytest
 import torch
 
@@ -80,3 +82,125 @@ def test_a_step_repeats_itself(B, C, dt):
         got = [carve.swa_decode_mx(q, k, v, ring, pos, C), *carve.budget_decode_mx(q, k, v, now, pos, sinks=4, recent=9), *ring, *now]
         want = want or got
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+# ------------------------------------------------------------------ values that are not finite
+SIZES = [(1, 6, 2, 128, 1), (2, 6, 2, 64, 70), (1, 40, 2, 128, 33), (2, 8, 2, 128, 9001), (130, 4, 2, 64, 300), (1, 68, 2, 64, 50)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("B,Hq,Hkv,D,C", SIZES)
+def test_query_that_is_not_finite(B, Hq, Hkv, D, C, bits, dt):
+    """Its own row is not a number, also where every key has the same sign at the infinite element (all scores are
+    then infinite with one sign).  Other key heads keep their bits; heads that share its key head may be scaled anew where
+    it is, so they are compared by value: either side is off by less than (2 e + 2^-8) max |v| + 2^-8 |o|, with scores of A < 40
+    and 3 C < 2^15 terms e < 2^-24 (2 (3 128 + 4) 40 + 2^15 + 32) < 2^-8, so by less than 2^-5 max |v| together.  In a
+    cache kept by weight all slots of its key head weigh not a number from then on, and the next token takes the first that
+    may be given up."""
+    G, sinks, recent = Hq // Hkv, min(2, C - 1), 1
+    k = normal((B, Hkv, C, D), dt, 1).abs() + 0.5
+    kept = kept_of(k, normal((B, Hkv, C, D), dt, 2), bits)
+    q, k1, v1 = normal((B, Hq, D), dt, 3), normal((B, Hkv, D), dt, 4).abs() + 0.5, normal((B, Hkv, D), dt, 5)
+    pos, b, g = ints([C] * B), B - 1, Hq - 1
+    h = g // G
+
+    def step(q):
+        ring, now = copy_of(kept[:4]), copy_of(kept)
+        return carve.swa_decode_mx(q, k1, v1, ring, pos, C), carve.budget_decode_mx(q, k1, v1, now, pos, sinks=sinks, recent=recent), now
+
+    clean, (clean2, slot), held = step(q)
+    rest, group = torch.ones(B, Hq, dtype=torch.bool), torch.zeros(B, Hq, dtype=torch.bool)
+    rest[b, h * G:h * G + G] = False
+    group[b, h * G:g] = True
+    others = torch.ones(B, Hkv, dtype=torch.bool)
+    others[b, h] = False
+    most = 2.0 ** -5 * 6                                      # (of normal values, none is past 6)
+    for bad in (-math.inf, math.inf, math.nan):
+        q2 = q.clone()
+        q2[b, g, 9] = bad
+        o, (o2, slot2), now = step(q2)
+        assert torch.isnan(o[b, g]).all() and torch.isnan(o2[b, g]).all(), bad
+        assert torch.equal(o[rest], clean[rest]) and torch.equal(o2[rest], clean2[rest])
+        assert ((o[group] - clean[group]).abs() <= most).all() and ((o2[group] - clean2[group]).abs() <= most).all()
+        assert torch.equal(slot2, slot) and all(torch.equal(now[i], held[i]) for i in (0, 1, 2, 3, 5))
+        assert torch.isnan(now[4][b, h]).all() and torch.equal(now[4][others], held[4][others])
+        at = next(j for j in range(C) if sinks <= int(now[5][b, h, j]) <= C + 1 - recent)
+        _, slot3 = carve.budget_decode_mx(q, k1, v1, now, pos + 1, sinks=sinks, recent=recent)
+        assert int(slot3[b, h]) == at
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("B,Hq,Hkv,D,C", SIZES)
+def test_key_or_value_that_is_not_finite(B, Hq, Hkv, D, C, bits, dt):
+    """A key gives all heads of its group a row that is not a number, and the slots of its key head such weights; a
+    value the places of its block, and no weight.  So do a scale byte 255 in the cache and, at its own place, the code of 8
+    bits that is not a number."""
+    G = Hq // Hkv
+    kept = kept_of(normal((B, Hkv, C, D), dt, 1), normal((B, Hkv, C, D), dt, 2), bits)
+    if C > 1:
+        kept[4][:, :, C // 2] = 2.0 ** 20                     # the slot that is spoilt is not the one that the token takes
+    q, k1, v1 = normal((B, Hq, D), dt, 3), normal((B, Hkv, D), dt, 4), normal((B, Hkv, D), dt, 5)
+    pos, b, h, recent = ints([C] * B), B - 1, Hkv - 1, 1
+    heads = slice(h * G, h * G + G)
+
+    def step(k1, v1, cache=kept):
+        ring, now = copy_of(cache[:4]), copy_of(cache)
+        return carve.swa_decode_mx(q, k1, v1, ring, pos, C), carve.budget_decode_mx(q, k1, v1, now, pos, recent=recent)[0], now[4]
+
+    clean = step(k1, v1)
+    rest = torch.ones(B, Hq, dtype=torch.bool)
+    rest[b, heads] = False
+    others = torch.ones(B, Hkv, dtype=torch.bool)
+    others[b, h] = False
+
+    def spoilt_key(got):
+        for o, c in zip(got[:2], clean):
+            assert torch.isnan(o[b, heads]).all() and torch.equal(o[rest], c[rest])
+        assert torch.isnan(got[2][b, h]).all() and torch.equal(got[2][others], clean[2][others])
+
+    def spoilt_value(got, places):
+        for o, c in zip(got[:2], clean):
+            assert torch.isnan(o[b, heads][:, places]).all() and torch.equal(o[rest], c[rest])
+            keep = torch.ones(D, dtype=torch.bool)
+            keep[places] = False
+            assert torch.equal(o[b, heads][:, keep], c[b, heads][:, keep])
+        assert torch.equal(got[2], clean[2])
+
+    for bad in (math.nan, math.inf, -math.inf):
+        k2, v2 = k1.clone(), v1.clone()
+        k2[b, h, 5] = bad
+        spoilt_key(step(k2, v1))
+        v2[b, h, 40] = bad
+        spoilt_value(step(k1, v2), slice(32, 64))
+    if C > 1:
+        for i, check in ((1, spoilt_key), (3, lambda got: spoilt_value(got, slice(32, 64)))):
+            cache = copy_of(kept)
+            cache[i][b, h, C // 2, 1] = 255
+            check(step(k1, v1, cache))
+        if bits == 8:
+            for i, check in ((0, spoilt_key), (2, lambda got: spoilt_value(got, slice(37, 38)))):
+                for code in (0x7f, 0xff):
+                    cache = copy_of(kept)
+                    cache[i][b, h, C // 2, 37] = code
+                    check(step(k1, v1, cache))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hq,Hkv,D,C", SIZES)
+def test_infinite_query_on_plain_rows(B, Hq, Hkv, D, C, dt):
+    """The same on caches of rows as they are: all scores of a head infinite with one sign give not a number."""
+    G, h = Hq // Hkv, Hkv - 1
+    k, v = normal((B, Hkv, C, D), dt, 1).abs() + 0.5, normal((B, Hkv, C, D), dt, 2)
+    kept = (k, v) + kept_of(k, v, 4)[4:]
+    q, k1, v1 = normal((B, Hq, D), dt, 3), normal((B, Hkv, D), dt, 4).abs() + 0.5, normal((B, Hkv, D), dt, 5)
+    q[B - 1, Hq - 1, 9] = -math.inf
+    now = copy_of(kept)
+    o = carve.swa_decode(q, k1, v1, k.clone(), v.clone(), ints([C] * B), C)
+    o2, _ = carve.budget_decode(q, k1, v1, now, ints([C] * B))
+    keep = torch.ones(B, Hq, dtype=torch.bool)
+    keep[B - 1, Hq - 1] = False
+    for x in (o, o2):
+        assert torch.isnan(x[B - 1, Hq - 1]).all() and torch.isfinite(x[keep]).all()
+    assert torch.isnan(now[2][B - 1, h]).all() and int(torch.isnan(now[2]).sum()) == C
