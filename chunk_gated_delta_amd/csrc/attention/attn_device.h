@@ -19,7 +19,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNegBig = -1.0e30f;     // running maximum before any visible score
+constexpr float kNegBig = -1.0e30f;     // running maximum before any visible score (whole sequences)
 
 __device__ __forceinline__ f32x16 zero16() {
   f32x16 z;

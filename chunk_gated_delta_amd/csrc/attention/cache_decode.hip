@@ -57,7 +57,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
   float m[NT], l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = kNegBig;
+    m[nt] = kLeast;
     l[nt] = 0.f;
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) O[nt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
     for (int i = threadIdx.x; i < 16 * D / 4; i += kDecThreads) {
       const int h = i / (D / 4), d = 4 * (i % (D / 4)), g = 16 * nt + h;
       if (g >= G) continue;
-      float M = kNegBig, L = 0.f;
+      float M = kLeast, L = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[w][h][0]);
       f32x4 x = {0.f, 0.f, 0.f, 0.f};
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
   float m[NT], l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = kNegBig;
+    m[nt] = kLeast;
     l[nt] = 0.f;
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) O[nt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
     for (int i = threadIdx.x; i < 16 * D / 4; i += 64 * NW) {
       const int h = i / (D / 4), c4 = i % (D / 4), g = 16 * nt + h;
       if (g >= G) continue;
-      float M = kNegBig, L = 0.f;
+      float M = kLeast, L = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w][h][0]);
       f32x4 x = {0.f, 0.f, 0.f, 0.f};

@@ -6,6 +6,9 @@
 namespace carve {
 
 constexpr int kDecThreads = 256;
+// Running maximum before the first live slot, at or below every finite score.  Ranges and waves without one have it as theirs:
+// the factor that joins them in is then 0, or 1 of a sum of 0.
+constexpr float kLeast = -__FLT_MAX__;
 
 // Slot of the new token in a cache kept by weight, by the least (class, weight, slot):
 // class 0 the slot that holds this position already (a repeated call), 1 an empty one, 2 one
@@ -120,7 +123,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_join_kernel(CacheArgs a) {
   auto stats = [&](int g) {                      // lanes of a wave: max and sum of head g over the ranges
     const int lane = lane_id();
     const float* q = part + ((size_t)min(lane, a.n_split - 1) * G + g) * (D + 4);
-    const float m = lane < a.n_split ? q[0] : kNegBig;
+    const float m = lane < a.n_split ? q[0] : kLeast;
     float M = m;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) M = fmaxf(M, __shfl_xor(M, o));

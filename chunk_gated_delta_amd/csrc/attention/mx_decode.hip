@@ -361,7 +361,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
   float m[NT], l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = kNegBig;
+    m[nt] = kLeast;
     l[nt] = 0.f;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) O[nt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -529,7 +529,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
     for (int i = threadIdx.x; i < 16 * D / 4; i += 64 * NW) {
       const int h = i / (D / 4), c4 = i % (D / 4), g = 16 * nt + h;
       if (g >= G) continue;
-      float M = kNegBig, L = 0.f;
+      float M = kLeast, L = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w][h][0]);
       f32x4 y = {0.f, 0.f, 0.f, 0.f};

@@ -1,5 +1,5 @@
 """Decode steps on caches in codes where results are decided by one rounding or one value: bf16
-weights, values that are not finite (tests/mx_ref.py states the definition and the bounds)."""
+weights, values that are not finite, scores far below zero (tests/mx_ref.py states the definition and the bounds)."""
 import math
 
 import pytest
@@ -204,3 +204,50 @@ def test_infinite_query_on_plain_rows(B, Hq, Hkv, D, C, dt):
     for x in (o, o2):
         assert torch.isnan(x[B - 1, Hq - 1]).all() and torch.isfinite(x[keep]).all()
     assert torch.isnan(now[2][B - 1, h]).all() and int(torch.isnan(now[2]).sum()) == C
+
+
+# ------------------------------------------------------------------ scores far below zero
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("Hq,D,C,have", [(1, 64, 1, 0), (3, 128, 4, 2), (40, 64, 70, 69), (2, 64, 9001, 3), (64, 128, 33, 2)])
+def test_scores_below_every_start(Hq, D, C, have, bits, dt):
+    """All scores finite and below -10^33: the token nearest to zero has all the weight (scores differ by a
+    quarter and more), in one range and in several with nothing in most of them."""
+    far = torch.arange(have + 1, 0, -1, dtype=torch.float32).view(1, 1, -1, 1).expand(1, 1, have + 1, D)
+    far = (-1e16 * torch.where(far > 4, 4.0, far)).to(DT[dt]).cuda()        # -4 .. -4, -3, -2 and, of the new token, -1
+    v = normal((1, 1, have + 1, D), dt, 2)
+    q = torch.full((1, Hq, D), 1e16, device="cuda").to(DT[dt])
+    ring = carve.swa_cache_mx(1, 1, D, C, bits=bits)
+    kept = carve.budget_cache_mx(1, 1, D, C, bits=bits)
+    if have:
+        prompt = [x[:, :, :have].contiguous() for x in (far, v)]
+        carve.swa_fill_mx(*prompt, ring, C)
+        carve.budget_keep_mx(*prompt, torch.ones(1, 1, have, device="cuda"), C, cache=kept)
+    k1, v1 = (x[:, :, have].contiguous() for x in (far, v))
+    o = carve.swa_decode_mx(q, k1, v1, ring, ints([have]), C)
+    o2, slot = carve.budget_decode_mx(q, k1, v1, kept, ints([have]))
+    want = mx_ref.written(v1, bits)[0].view(D).to(DT[dt]).cuda()         # (a bf16 exactly)
+    for x in (o, o2):
+        assert all(torch.equal(x[0, g], want) for g in range(Hq))
+    assert int(slot) == have and float(kept[4][0, 0, have]) == Hq and (kept[4][0, 0, :have] == 1).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,D,C,have", [(1, 64, 1, 0), (3, 128, 4, 2), (40, 64, 70, 69), (2, 64, 9001, 3)])
+def test_scores_below_every_start_on_plain_rows(Hq, D, C, have, dt):
+    """The same on caches of rows as they are."""
+    far = torch.arange(have + 1, 0, -1, dtype=torch.float32).view(1, 1, -1, 1).expand(1, 1, have + 1, D)
+    far = (-1e16 * torch.where(far > 4, 4.0, far)).to(DT[dt]).cuda()
+    v = normal((1, 1, have + 1, D), dt, 2)
+    q = torch.full((1, Hq, D), 1e16, device="cuda").to(DT[dt])
+    ring, kept = carve.swa_cache(1, 1, D, C, dtype=DT[dt]), carve.budget_cache(1, 1, D, C, dtype=DT[dt])
+    if have:
+        prompt = [x[:, :, :have].contiguous() for x in (far, v)]
+        carve.swa_fill(*prompt, *ring, C)
+        carve.budget_keep(*prompt, torch.ones(1, 1, have, device="cuda"), C, cache=kept)
+    k1, v1 = (x[:, :, have].contiguous() for x in (far, v))
+    o = carve.swa_decode(q, k1, v1, *ring, ints([have]), C)
+    o2, slot = carve.budget_decode(q, k1, v1, kept, ints([have]))
+    for x in (o, o2):
+        assert all(torch.equal(x[0, g], v1.view(D)) for g in range(Hq))
+    assert int(slot) == have and float(kept[2][0, 0, have]) == Hq and (kept[2][0, 0, :have] == 1).all()
