@@ -72,7 +72,7 @@ struct CacheArgs {
   void* o;                    // [B,Hq,D]
   int* slot;                  // [B,Hkv]
   int n_split, split_len;     // slots of a workgroup
-  int waves;                  // of a workgroup, 4 or 8 (bf16, at most 16 heads a group)
+  int waves;                  // of a workgroup, 4 or 8 (rows: bf16 and at most 16 heads a group; codes: at most 32)
   float* part;                // [B*Hkv][n_split][G][4 + D]: max, sum, two unused, sum of p v
   float* score;               // [B*Hkv][G][score_row(C)] scores (log2 domain), budget cache only;
                               // null: they stay in LDS
@@ -80,10 +80,12 @@ struct CacheArgs {
 __host__ __device__ constexpr int score_row(int C) { return (C + 3) & ~3; }
 constexpr int kNearScores = 4096;      // most scores of a key head that stay in LDS (bf16, one workgroup of 8 waves)
 
-// the same for rows of codes, with a workgroup of 8 waves a compute unit or two of 4, beside the LDS that those take
-// (8 bits at D = 128 leave none to two)
+// The same for rows of codes: what a compute unit's 160 KB of LDS leave beside one workgroup of 8 waves, or two of 4.
+// Such a workgroup holds two steps of 32 slots a wave (k and v; later, in the same place, its 16 heads' sums in float),
+// a step's scales, 136 bytes of sums a wave, 32 heads' maxima and sums, and the token's row (1 KB for these two).
 __host__ __device__ constexpr int mx_near_scores(int bits, int D, int waves) {
-  return bits == 8 && D == 128 ? (waves == 8 ? 4096 : 4) : waves == 8 ? 20480 : 8192;
+  const int rows = waves * 128 * (D * bits / 8), sums = waves * 64 * D;
+  return ((160 << 10) / (waves == 8 ? 1 : 2) - (rows > sums ? rows : sums) - waves * (2 * D + 136) - 1024) / 16 * 4;
 }
 
 // Rows of k and v copied into a cache.

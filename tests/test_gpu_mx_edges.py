@@ -1,5 +1,6 @@
 """Decode steps on caches in codes where results are decided by one rounding or one value: bf16
 weights, values that are not finite, scores far below zero (tests/mx_ref.py states the definition and the bounds)."""
+import ctypes
 import math
 
 import pytest
@@ -8,6 +9,7 @@ import torch
 from chunk_gated_delta_amd import carve
 from tests import attention_ref as ref
 from tests import mx_ref
+from tests.test_gpu_mx import one_eviction
 
 pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -251,3 +253,14 @@ def test_scores_below_every_start_on_plain_rows(Hq, D, C, have, dt):
     for x in (o, o2):
         assert all(torch.equal(x[0, g], v1.view(D)) for g in range(Hq))
     assert int(slot) == have and float(kept[2][0, 0, have]) == Hq and (kept[2][0, 0, :have] == 1).all()
+
+
+# ------------------------------------------------------------------ where the scores of a step are held
+@pytest.mark.parametrize("B,Hq,Hkv,D,C,bits,dt", [
+    (33, 8, 2, 128, 5884, 4, "bf16"), (33, 8, 2, 128, 1788, 8, "bf16"), (33, 8, 2, 64, 7996, 4, "f32"), (33, 8, 2, 64, 5948, 8, "bf16"),
+    (2, 30, 1, 64, 1064, 4, "f32"), (129, 8, 2, 128, 860, 8, "bf16"), (129, 8, 2, 128, 860, 8, "f32"), (129, 2, 2, 64, 2940, 8, "bf16")])
+def test_eviction_with_the_most_scores_in_lds(B, Hq, Hkv, D, C, bits, dt):
+    """As many scores as LDS leaves room for, or nearly: a step without a workspace, against the definition."""
+    s = carve.carve_budget_shape(B, Hq, Hkv, 1, D, C, 4, 20, D ** -0.5, 1 if dt == "bf16" else 0)
+    assert carve.load_library().carve_budget_decode_mx_workspace_size(ctypes.byref(s), bits) == 0
+    one_eviction(B, Hq, Hkv, D, C, bits, dt, empty=3)
