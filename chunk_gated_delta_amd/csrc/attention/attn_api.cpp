@@ -153,17 +153,28 @@ void split_plan(int units, int C, int row_bytes, int* n_split, int* split_len, i
   *n_split = ceil_div(C, *split_len);
 }
 // The same for rows of codes, which are read sooner than a step of 128 slots is computed.  Up to 256 key heads one
-// workgroup of 8 waves each, above of 4 (400 of 512 slots with weights: 13.8 against 18.6 us, without 9.8
-// against 10.2; 256: 11.1 against 10.4, 7.6 against 7.4).  Few key heads are cut into ranges where that saves more than the
-// launch that joins them: 4 key heads of 1,028 / 2,052 / 4,100 slots 8.6 / 12.2 / 19.7 us in one, 7.7 / 8.2 / 8.9
-// in ranges, with weights 12.2 / 17.0 / 26.9 and 10.9 / 11.7 / 13.1; 32 of 2,052 slots 12.5 and 10.1;
-// 128 of 2,052 / 4,100 / 8,196 slots 13.8 / 22 / 39 and 14.7 / 19.5 / 34, with weights 20 / 32 / 55
-// and 23 / 34 / 55; 256 not at any length.  (A caller that launches each step anew pays the second launch's 4 us too.)
+// workgroup of 8 waves each, above of 4 (400 of 512 slots with weights: 14.5 us of 4 waves, 20.0 of 8, without 10.8 and
+// 11.1; 256: 10.6 and 10.6, 8.4 and 7.9; of 2,048 slots with weights 28.1 and 22.3).  Up to 128 key heads, half a chip of workgroups, are cut into ranges
+// where that saves more than the launch that joins them.  In one workgroup / in ranges, D = 128, 4 heads on one, bf16, 4 bits, us:
+//   key heads            4          64          68          96         128        160         240
+//   ring    1,024     9.1/7.9
+//           1,536               11.7/11.7   11.7/11.7
+//           2,048    13.4/8.2   14.2/12.7   14.3/13.0   14.3/14.9   14.6/15.6
+//           4,096    22.2/9.0   22.9/15.6   23.0/16.3   23.7/20.6   24.3/21.5   25.3/27.2   28.5/33.3
+//   weights 1,024    12.0/10.3
+//           1,536               16.4/15.5
+//           2,048    17.2/11.1  19.3/16.6   19.1/18.3   19.7/20.8
+//           4,096               -           31.4/26.6   32.2/31.0   33.0/32.4               (192: 34.5/44.7)
+//           8,192               -           54.0/39.0   55.2/47.8   56.9/53.7               74.9/82.9
+// 8 bits, D = 64, float32 and 16 heads on one cross over at the same lengths or a little below (128 key heads of 2,999 slots
+// in 8 bits 27.5/25.3, d64 14.6/13.6, fp32 24.0/20.1; 160 of 8,192 in 8 bits 71.7/73.1, d64 32.2/29.4, fp32 55/49, with
+// weights 90/99, 51/50, 73/70).  A caller that launches each step anew pays the second launch's 4 us too, so few
+// key heads of up to 1,536 slots stay in one.
 void mx_split_plan(int units, int C, bool weights, int* n_split, int* split_len, int* waves) {
-  const int most = units <= 64 ? 1536 : weights ? 8192 : 3000;      // slots of one workgroup
+  const int most = units <= 64 ? 1536 : weights ? 4096 : 3000;      // slots of one workgroup
   int n = 1;
   *waves = units <= 256 ? 8 : 4;
-  if (units < 256 && C > most) {
+  if (units <= 128 && C > most) {
     n = std::min({ceil_div(512, units), ceil_div(C, 128), 64});
     *waves = 4;
   }

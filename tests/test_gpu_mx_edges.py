@@ -257,7 +257,7 @@ def test_scores_below_every_start_on_plain_rows(Hq, D, C, have, dt):
 
 # ------------------------------------------------------------------ where the scores of a step are held
 @pytest.mark.parametrize("B,Hq,Hkv,D,C,bits,dt", [
-    (33, 8, 2, 128, 5884, 4, "bf16"), (33, 8, 2, 128, 1788, 8, "bf16"), (33, 8, 2, 64, 7996, 4, "f32"), (33, 8, 2, 64, 5948, 8, "bf16"),
+    (65, 8, 2, 128, 5884, 4, "bf16"), (65, 8, 2, 128, 1788, 8, "bf16"), (65, 8, 2, 64, 7996, 4, "f32"), (65, 8, 2, 64, 5948, 8, "bf16"),
     (2, 30, 1, 64, 1064, 4, "f32"), (129, 8, 2, 128, 860, 8, "bf16"), (129, 8, 2, 128, 860, 8, "f32"), (129, 2, 2, 64, 2940, 8, "bf16")])
 def test_eviction_with_the_most_scores_in_lds(B, Hq, Hkv, D, C, bits, dt):
     """As many scores as LDS leaves room for, or nearly: a step without a workspace, against the definition."""
