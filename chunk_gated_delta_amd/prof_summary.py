@@ -34,12 +34,13 @@ DIGEST_LINE = "Kernel sources digest at measurement: "
 
 def short_name(mangled):
     for key in ("bwd_chunk_kernel", "bwd_state_kernel", "fwd_prep_kernel", "fwd_state_kernel",
-                "fwd_content_kernel", "fwd_affine_kernel", "seg_scan_kernel", "decode_kernel",
+                "fwd_content_kernel", "fwd_affine_kernel", "seg_scan_kernel", "mx_decode_kernel", "decode_kernel",
                 "content_gate_bwd_kernel", "content_gates_kernel", "add_grad_mean_kernel",
                 "init_grad_mean_kernel", "sum_over_batch_kernel", "logit_grads_kernel", "sum_heads_kernel",
                 "copy_or_zero_kernel", "stream_copy_kernel", "swa_fwd_bf16_kernel", "swa_dq_bf16_kernel",
                 "swa_dkdv_bf16_kernel", "swa_sink_kernel", "weight_bf16_kernel", "weight_sum_kernel",
-                "cache_decode_bf16_kernel", "cache_join_kernel", "keep_select_kernel", "fill_rows_kernel"):
+                "cache_decode_bf16_kernel", "cache_join_kernel", "keep_select_kernel", "fill_rows_kernel",
+                "mx_quant_kernel", "mx_dequant_kernel", "mx_fill_kernel"):
         if key in mangled:
             return key
     return mangled[:48]

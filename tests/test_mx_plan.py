@@ -31,3 +31,10 @@ def test_ranges_of_few_key_heads_only(bits, D, dtype):
         assert budget_bytes(units, most + 1, bits, D, dtype) > scores + units * 4 * 16 + 4 * units * D
     for units in (129, 192, 255, 256):
         assert budget_bytes(units, 100000, bits, D, dtype) == units * 4 * 100000 * 4 + 256
+
+
+def test_kernels_have_names_of_their_own_in_summaries():
+    """A summary tells these kernels from each other, and from the delta rule's decode step."""
+    from chunk_gated_delta_amd.prof_summary import short_name
+    for name in ("mx_decode_kernel", "mx_quant_kernel", "mx_dequant_kernel", "mx_fill_kernel", "decode_kernel", "cache_decode_bf16_kernel"):
+        assert short_name(f"_ZN5carve{len(name)}{name}IDF16bLi4EEEvNS_9CacheArgsE") == name
