@@ -215,7 +215,7 @@ bool plain_near_scores(const carve_budget_shape* s, int n_split, int waves) {
          G * carve::score_row(s->C) <= carve::kNearScores;
 }
 // The same for rows of codes: workgroups of 8 waves are one a compute unit at most; of 4, up to two are that few
-// (64 / 128 / 256 sequences of 2,048 slots, 16 heads on 4: 20.8 / 37 us in LDS, 24 / 41 without; 73 without, 74 in LDS).
+// (64 / 128 sequences of 2,048 slots, 16 heads on 4: 22 / 38 us in LDS, 25 / 42 without; 129: 57 in LDS, 50 without).
 bool near_scores(const carve_budget_shape* s, int bits, int n_split, int waves) {
   if (!bits) return plain_near_scores(s, n_split, waves);
   const long long G = s->Hq / s->Hkv;

@@ -57,8 +57,6 @@ __device__ __forceinline__ int ring_slot(const CacheArgs& a, int p) {
   return p < a.sinks ? p : a.sinks + (p - a.sinks) % a.window;
 }
 
-// Adds the token's weights to the cache's: slots lo .. hi - 1, with max and sum of every head
-// (log2 domain) in st[head] = {m, 1 / l}, scores [G][score_row(C)] of the key head in `score`.
 // Slots a thread takes at a time, their positions and weights in flight together; a kernel may ask for the
 // first of them (from `lo` on) early.
 template <int NW>
@@ -76,6 +74,8 @@ struct WeightBatch {
     }
   }
 };
+// Adds the token's weights to the cache's: slots lo .. hi - 1, with max and sum of every head
+// (log2 domain) in st[head] = {m, 1 / l}, scores [G][score_row(C)] of the key head in `score`; b: the first batch.
 template <int NW>
 __device__ __forceinline__ void add_weights(const CacheArgs& a, int bk, int p, int at, int lo, int hi, const float* st,
                                             const float* score, WeightBatch<NW> b) {

@@ -3,23 +3,25 @@
 //
 // What codes stand for is a bf16 exactly, so both products run on bf16 operands; where q is float32, q
 // and the weights go in as three bf16 parts each, which hold all their bits (256 sequences, 16 heads on 4, window 4,096,
-// 4 bits: 127 us, bf16 110).  With bf16 queries the weights are two parts: rounded to one, the largest weight of a row would be
-// off by as much as the output's own rounding, and the error of a step's output half as large again.  (One part: 108 us;
-// 4 key heads of 1,028 slots 8.6 us, two parts 9.2; 64 heads on one, 2,048 slots 39 and 45.)
+// 4 bits: 130 us, bf16 111).  With bf16 queries the weights are two parts: rounded to one, the largest weight of a row would be
+// off by as much as the output's own rounding (error against 64 bits 2.0e-3 to 2.5e-3; two parts 1.5e-3 to 1.6e-3, the
+// rounding of the output alone).  One part: 108 us; 4 key heads of 1,028 slots 8.6 us, two parts 9.1; 64 heads on one,
+// 2,048 slots 39 and 45.
 // Codes reach LDS by loads that write it directly; a lane converts what it reads from there.
 // The contraction of S^T = K Q^T may run over a key's elements in any order that q's have too, so a lane takes D / 4
 // neighbouring ones, with one scale; for O^T = V^T P^T it takes D / 16 neighbouring elements of each of its eight
 // slots and pairs the slots up as it converts.  The token's own row is written over its place in LDS by the wave that
 // holds its slot, as well as to the cache, so no wave waits for a store.
 //
-// Bound by the cache's read where there are many key heads: 256 sequences as above, some still filling (about 540 MB),
-// in 89 to 104 us, 5.2 to 6.1 TB/s; a plain read of as much takes 88.  The vector units are then busy for 0.58 of the time
-// (conversions, their pairing, exponentials), the matrix units for 0.15; without the value products, or without
-// exponentials, the time is the same.  With few key heads it is latency: 4 of 1,028 slots 8.6 us, about 5 of
-// them before and after the slots, 0.9 a step of 256 slots.  With weights 64 sequences of 2,048 slots 20 us (the
-// slot's search before, the weights after the steps); 256 of 4,096 slots 137 us: the scores' way to memory and
-// back, 134 MB, beside 570 MB of rows.  More than 32 float32 heads of D = 128 on a key head do not fit the registers
-// (64 heads on one: 137 us where bf16 takes 39).
+// Bound by the cache's read where a compute unit has several key heads: 256 sequences as above, some still
+// filling (about 540 MB), in 91 to 106 us, 5.1 to 5.9 TB/s; a plain read of as much takes 88.  The vector units are then busy for
+// 0.71 of the time (conversions, their pairing, exponentials), the matrix units for 0.28 (one part of the weights: 0.58 and
+// 0.15; then the time was the same without the value products, and without exponentials).  With few key heads it is latency:
+// 4 of 1,028 slots 9.1 us, about 5 of them before and after the slots, 1.05 a step of 256 slots.  With weights 64
+// sequences of 2,048 slots 22 us (the slot's search before, the weights after the steps); 256 of 4,096 slots 140 us:
+// the scores' way to memory and back, 134 MB, beside 570 MB of rows and 50 of positions and weights.  More than 32 heads on a
+// key head take 64 columns of registers, one wave a SIMD (80 heads on 2, 256 sequences of 4,096 slots: 153 us, read in 50),
+// and spill in float32 with D = 128 (64 heads on one, 2,048 slots: 138 us, bf16 45).
 #include <algorithm>
 
 #include "cache_step.h"
@@ -69,9 +71,9 @@ struct MxTile {
   // place of a key row's piece of 16 bytes within the row: ^ this
   static __device__ __forceinline__ int swz(int row) { return RB == 32 ? 0 : RB == 64 ? (row >> 2) & 3 : (row >> 1) & 7; }
   // 16 bytes a lane to LDS, marked as not used again (2): codes are read once a step, and a load that takes no place in
-  // the caches need not move out what others wrote there.  256 / 64 sequences, 16 heads on 4, window 4,096, 4 bits: 108 /
-  // 29 us again and again, 137 / 44 after other work has filled the caches; without the mark 122 / 26.5 and 180 / 69.
-  // (The scales, 128 bytes of a line at a time, are left their places: 107 against 111 us.)
+  // the caches need not move out what others wrote there.  256 / 64 sequences, 16 heads on 4, window 4,096, 4 bits: 111 /
+  // 30 us again and again, 134 / 44 after other work has filled the caches; without the mark 124 / 27 and 178 / 66.
+  // (The scales, 128 bytes of a line at a time, are left their places: marked too, 4 us more of the 107 at the time.)
   static __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, unsigned char* dst, int off, int more) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, off, more, 0, 2);
   }

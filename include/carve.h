@@ -584,7 +584,7 @@ typedef struct {
  * when they are written, the new token's too: it sees itself as the next ones will.  What a cache holds
  * enters the products exactly; q and, with float32, the weights are not rounded either (with bf16 the
  * weights enter as two bf16 parts, off by less than 2^-15 of them: what carve_swa_decode rounds to bf16
- * is not rounded here); parts of them below 2^-126 count as zero.
+ * is not rounded here); sizes and parts below 2^-126 may count as zero.
  * Scores are float32: one past its range is infinite.
  * A key that is read as not a number gives all heads of its group a row that is not a number, a value the
  * 32 places of its block, and a query that is not finite its own row.  Cached weights are reached as in
