@@ -154,8 +154,9 @@ void split_plan(int units, int C, int row_bytes, int* n_split, int* split_len, i
 }
 // The same for rows of codes, which are read sooner than a step of 128 slots is computed.  Up to 256 key heads one
 // workgroup of 8 waves each, above of 4 (400 of 512 slots with weights: 14.5 us of 4 waves, 20.0 of 8, without 10.8 and
-// 11.1; 256: 10.6 and 10.6, 8.4 and 7.9; of 2,048 slots with weights 28.1 and 22.3).  Up to 128 key heads, half a chip of workgroups, are cut into ranges
-// where that saves more than the launch that joins them.  In one workgroup / in ranges, D = 128, 4 heads on one, bf16, 4 bits, us:
+// 11.1; 256: 10.6 and 10.6, 8.4 and 7.9; of 2,048 slots with weights 28.1 and 22.3).  Up to 128 key heads, half a chip of
+// workgroups, are cut into ranges where that saves more than the launch that joins them.  In one workgroup / in ranges,
+// D = 128, 4 heads on one, bf16, 4 bits, us:
 //   key heads            4          64          68          96         128        160         240
 //   ring    1,024     9.1/7.9
 //           1,536               11.7/11.7   11.7/11.7

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(kDecThreads) void cache_decode_f32_kernel(CacheArgs
         x += load4f(mg + (w * 16 + h) * LDM + d) * f;
       }
       if (a.n_split == 1) {
-        const float f = 1.f / L;                 // (no sum is zero: see cache_join_kernel)
+        const float f = 1.f / L;                 // (where that is zero: see cache_join_kernel)
         store4(ob + (size_t)g * D + d, x * f);
         if (d == 0) {
           st[g][0] = M;
@@ -435,7 +435,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? 2 : 1) void cache_decode_bf16_ke
         x += load4f(mg + (w * 16 + h) * D + ((c4 ^ h) << 2)) * f;
       }
       if (a.n_split == 1) {
-        const float f = 1.f / L;                 // (no sum is zero: see cache_join_kernel)
+        const float f = 1.f / L;                 // (where that is zero: see cache_join_kernel)
         store4(ob + (size_t)g * D + 4 * c4, x * f);
         if (c4 == 0) {
           st[g][0] = M;

@@ -542,7 +542,7 @@ __global__ __launch_bounds__(64 * NW, NT == 1 ? (sizeof(T) == 2 ? 4 : 2) : 1) vo
         y += load4f(mg + (w * 16 + h) * D + ((c4 ^ h) << 2)) * f;
       }
       if (a.n_split == 1) {
-        const float f = 1.f / L;                 // (no sum is zero: see cache_join_kernel)
+        const float f = 1.f / L;                 // (where that is zero: see cache_join_kernel)
         store4(ob + (size_t)g * D + 4 * c4, y * f);
         if (c4 == 0) {
           st[g][0] = M;

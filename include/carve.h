@@ -540,8 +540,9 @@ carve_status carve_budget_keep(const carve_budget_shape* s, const void* k, const
  * slot's weight is its own p).
  *   q, k, v, pos, o as for carve_swa_decode; slot (device) [B,Hkv] int32 written: the
  *   slot taken, -1 for a row without a token
- * A query or key that is not finite makes the weights of all live slots of its key head not a number, from
- * then on: they count as the largest, so the next token takes the lowest slot that may be given up.
+ * A query that is not finite, or a key that is not a number, makes the weights of all live slots of its key
+ * head not a number, from then on: they count as the largest, so the next token takes the lowest slot
+ * that may be given up.
  */
 size_t carve_budget_decode_workspace_size(const carve_budget_shape* s);
 carve_status carve_budget_decode(const carve_budget_shape* s, const void* q, const void* k, const void* v,
@@ -587,8 +588,8 @@ typedef struct {
  * is not rounded here); sizes and parts below 2^-126 may count as zero.
  * Scores are float32: one past its range is infinite.
  * A key that is read as not a number gives all heads of its group a row that is not a number, a value the
- * 32 places of its block, and a query that is not finite its own row.  Cached weights are reached as in
- * carve_budget_decode, by queries and keys.
+ * 32 places of its block, and a query that is not finite its own row.  Queries and such keys reach cached
+ * weights as in carve_budget_decode.
  */
 carve_status carve_swa_fill_mx(const carve_swa_shape* s, const void* k, const void* v, const int* lens,
                                const carve_mx_rows* cache, void* stream);

@@ -191,13 +191,14 @@ def test_key_or_value_that_is_not_finite(B, Hq, Hkv, D, C, bits, dt):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("B,Hq,Hkv,D,C", SIZES)
-def test_infinite_query_on_plain_rows(B, Hq, Hkv, D, C, dt):
+@pytest.mark.parametrize("bad", [-math.inf, math.inf, math.nan])
+def test_infinite_query_on_plain_rows(B, Hq, Hkv, D, C, dt, bad):
     """The same on caches of rows as they are: all scores of a head infinite with one sign give not a number."""
     G, h = Hq // Hkv, Hkv - 1
     k, v = normal((B, Hkv, C, D), dt, 1).abs() + 0.5, normal((B, Hkv, C, D), dt, 2)
     kept = (k, v) + kept_of(k, v, 4)[4:]
     q, k1, v1 = normal((B, Hq, D), dt, 3), normal((B, Hkv, D), dt, 4).abs() + 0.5, normal((B, Hkv, D), dt, 5)
-    q[B - 1, Hq - 1, 9] = -math.inf
+    q[B - 1, Hq - 1, 9] = bad
     now = copy_of(kept)
     o = carve.swa_decode(q, k1, v1, k.clone(), v.clone(), ints([C] * B), C)
     o2, _ = carve.budget_decode(q, k1, v1, now, ints([C] * B))
